@@ -9,6 +9,11 @@ include/ddtree.h); this package only binds it:
     ddtree_mask      parents -> bit-packed ancestor-only attention mask
     ddtree_accept    tree + target tokens -> accepted path, new bonus token
     ddtree_compact_kv  KV caches keep only the accepted path's rows (in place)
+    ddtree_append_kv  a verified block's keys and values into a paged cache, rotated on the way
+    ddtree_attention  the verified block's attention over its cache under the ancestor mask
+    ddtree_compact_kv_paged  paged caches keep only the accepted path's rows (in place)
+    ddtree_accept_sampled  a tree's accepted path at a temperature, from given random numbers
+    dspark_accept_sampled  the same for a chain sampled from the drafter
     ddtree_row_topk  stage 1 alone: per-row sorted top-K and log-sum-exp
     ddtree_read_probe  measurement: stage 1's read path alone (the read ceiling)
     ddtree_ts_load_probe  measurement: a TreeSpark head evaluation's loads alone
@@ -18,17 +23,19 @@ include/ddtree.h); this package only binds it:
     dspark_budget    DSpark survival-ranked verification budget across the batch
 """
 
-from ._lib import (DDT_BF16, DDT_F32, DDTreeError, ddtree_accept, ddtree_build,
-                   ddtree_build_noalloc, ddtree_compact_kv,
+from ._lib import (DDT_BF16, DDT_F16, DDT_F32, DDTreeError, ddtree_accept,
+                   ddtree_accept_sampled, ddtree_append_kv, ddtree_attention, ddtree_build,
+                   ddtree_build_noalloc, ddtree_compact_kv, ddtree_compact_kv_paged,
                    ddtree_mask, ddtree_read_probe, ddtree_row_topk, ddtree_select,
                    ddtree_ts_load_probe,
-                   dspark_budget, lib,
+                   dspark_accept_sampled, dspark_budget, lib,
                    sparkling_beam, sparkling_build, status_string, treespark_expand)
 
-__all__ = ["DDT_BF16", "DDT_F32", "DDTreeError", "ddtree_accept", "ddtree_build",
+__all__ = ["DDT_BF16", "DDT_F16", "DDT_F32", "DDTreeError", "ddtree_accept",
+           "ddtree_accept_sampled", "ddtree_append_kv", "ddtree_attention", "ddtree_build",
            "ddtree_build_noalloc",
-           "ddtree_compact_kv", "ddtree_mask", "ddtree_read_probe", "ddtree_row_topk",
+           "ddtree_compact_kv", "ddtree_compact_kv_paged", "ddtree_mask", "ddtree_read_probe", "ddtree_row_topk",
            "ddtree_ts_load_probe",
-           "ddtree_select", "dspark_budget",
+           "ddtree_select", "dspark_accept_sampled", "dspark_budget",
            "lib", "sparkling_beam", "sparkling_build", "status_string",
            "treespark_expand"]

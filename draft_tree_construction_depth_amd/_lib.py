@@ -17,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libddtree.so")
 
 DDT_OK, DDT_EINVAL, DDT_ENOTSUP, DDT_EWORKSPACE, DDT_EHIP = 0, -1, -2, -3, -4
-DDT_BF16, DDT_F32 = 0, 1
+DDT_BF16, DDT_F32, DDT_F16 = 0, 1, 2
 
 _lib = None
 
@@ -77,6 +77,27 @@ def lib() -> C.CDLL:
         L.sparkling_beam.restype = C.c_int
         L.sparkling_beam.argtypes = [p, C.c_int, p, p, i64, i32, i64, i32, i32, p, i32, p, p, p,
                                      p, p, p, p, sz, p]
+        L.ddtree_append_kv.restype = C.c_int
+        L.ddtree_append_kv.argtypes = [p, p, p, C.c_int, i64, i32, i32, i32, i32, i64, i64, i64, p,
+                                       i64, i32, i32, p, p, p, p, i64, i64, i32, p, p, p, p]
+        L.ddtree_attention_workspace_size.restype = sz
+        L.ddtree_attention_workspace_size.argtypes = [i64, i32, i32, i32, i32, i64, i32]
+        L.ddtree_attention.restype = C.c_int
+        L.ddtree_attention.argtypes = [p, C.c_int, i64, i32, i32, i32, i32, p, p, p, i64, i64, i32,
+                                       p, p, p, C.c_float, p, p, p, sz, p]
+        L.ddtree_compact_kv_paged.restype = C.c_int
+        L.ddtree_compact_kv_paged.argtypes = [p, p, i64, i64, i32, i32, i32, p, i64, i64, p, p, p,
+                                              i32, p, p]
+        L.ddtree_accept_sampled_workspace_size.restype = sz
+        L.ddtree_accept_sampled_workspace_size.argtypes = [i64, i32, i32, i64, C.c_int]
+        L.ddtree_accept_sampled.restype = C.c_int
+        L.ddtree_accept_sampled.argtypes = [p, p, p, p, C.c_int, p, p, i64, i32, i32, i64, p, p, p,
+                                            p, p, sz, p]
+        L.dspark_accept_sampled_workspace_size.restype = sz
+        L.dspark_accept_sampled_workspace_size.argtypes = [i64, i32, i64, C.c_int]
+        L.dspark_accept_sampled.restype = C.c_int
+        L.dspark_accept_sampled.argtypes = [p, p, p, p, C.c_int, p, p, i64, i32, i64, p, p, p, p,
+                                            sz, p]
         _lib = L
     return _lib
 
@@ -453,4 +474,301 @@ def sparkling_beam(logits: torch.Tensor, W1: torch.Tensor, W2t: torch.Tensor, wi
                               _ptr(out.get("depths")), _ptr(out["num_nodes"]),
                               _ptr(out.get("mask")), _ptr(ws), ws.numel(), _stream(dev))
     _check("sparkling_beam", rc)
+    return out
+
+
+# ---- the verification pass --------------------------------------------------
+_HALF = (torch.bfloat16, torch.float16)
+_F32 = (torch.float32,)
+
+
+def _half_code(t: torch.Tensor) -> int:
+    return DDT_BF16 if t.dtype == torch.bfloat16 else DDT_F16
+
+
+def _on(dev, **tensors):
+    """Check that every tensor given lies on device dev."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _scratch(kind: str, size: int, device) -> torch.Tensor:
+    """Workspace for one call: the stream's own buffer of this kind (grown as
+    needed), or, under graph capture, one of the graph's, so that no two graphs
+    and no eager call share it."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    return workspace(kind, size, device, ())
+
+
+def _block_rows(t, name, dtype, batch, T, dh):
+    """Check [batch, T, heads, head_dim] rows at one distance; (tensor's heads, that distance)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[0] != batch or t.shape[1] != T or t.shape[3] != dh:
+        raise ValueError(f"{name} must have shape ({batch}, {T}, heads, {dh}), got {tuple(t.shape)}")
+    heads = t.shape[2]
+    step = t.stride(1) if T > 1 else (t.stride(0) if batch > 1 else heads * dh)
+    if (t.stride(3) != 1 and dh > 1) or (heads > 1 and t.stride(2) != dh) or \
+            (batch > 1 and t.stride(0) != T * step):
+        raise ValueError(f"{name} must hold its heads side by side and its rows at one distance")
+    return heads, step
+
+
+def _paged_cache(k_cache, v_cache, page_table, batch, dims):
+    """Check a cache [(layers,) pages, kv_heads, page_size, head_dim] and its page
+    table [batch, width]; (pages, kv_heads, page_size, head_dim, width)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != dims:
+        raise ValueError(f"k_cache must be a {dims}-d tensor "
+                         f"[{'layers, ' if dims == 5 else ''}pages, kv_heads, page_size, head_dim]")
+    _arg(k_cache, "k_cache", (k_cache.dtype,))
+    _arg(v_cache, "v_cache", (k_cache.dtype,), tuple(k_cache.shape))
+    _on(k_cache.device, v_cache=v_cache, page_table=page_table)
+    pages, heads, page_size, dh = k_cache.shape[-4:]
+    width = 1
+    if page_table is not None:
+        _arg(page_table, "page_table", _I32)
+        if page_table.dim() != 2 or page_table.shape[0] != batch:
+            raise ValueError(f"page_table must have shape ({batch}, width), got "
+                             f"{tuple(page_table.shape)}")
+        width = page_table.shape[1]
+    elif pages != batch:
+        raise ValueError(f"without a page table the cache must hold one page per request "
+                         f"({batch}), got {pages}")
+    return pages, heads, page_size, dh, width
+
+
+def ddtree_append_kv(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, past_len: torch.Tensor, *,
+                     rope: torch.Tensor | None = None, interleaved: bool = False,
+                     page_table: torch.Tensor | None = None, depths: torch.Tensor | None = None,
+                     num_nodes: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
+    """Verified block into one layer's cache: q [batch, T, q_heads, dh] (or None), k / v
+    [batch, T, kv_heads, dh] (bf16/f16; slices of a fused projection are read in place), caches
+    [pages, kv_heads, page_size, dh], rope [positions, rope_dim] float32 (cosines, then sines),
+    depths [batch, T-1]; writes the caches and returns the rotated queries q_out (None for q None)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be [batch, T, kv_heads, head_dim]")
+    if k.dtype not in _HALF:
+        raise TypeError(f"k must have dtype {' or '.join(map(str, _HALF))}, got {k.dtype}")
+    batch, T, _, dh = k.shape
+    dev = k.device
+    kv_heads, ks = _block_rows(k, "k", k.dtype, batch, T, dh)
+    hv, vs = _block_rows(v, "v", k.dtype, batch, T, dh)
+    q_heads, qs = (0, 0) if q is None else _block_rows(q, "q", k.dtype, batch, T, dh)
+    pages, hc, page_size, dc, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
+    if k_cache.dtype != k.dtype:
+        raise TypeError(f"k_cache must have dtype {k.dtype}, got {k_cache.dtype}")
+    if hv != kv_heads or hc != kv_heads or dc != dh:
+        raise ValueError("k, v and the caches must have the same heads and head_dim")
+    _arg(past_len, "past_len", _I32, (batch,))
+    rot = rope_len = 0
+    if rope is not None:
+        _arg(rope, "rope", _F32)
+        if rope.dim() != 2:
+            raise ValueError("rope must be [positions, rope_dim]")
+        rope_len, rot = rope.shape
+    if depths is not None:
+        _arg(depths, "depths", _I32, (batch, T - 1))
+    if num_nodes is not None:
+        _arg(num_nodes, "num_nodes", _I32, (batch,))
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.zeros((batch, T, q_heads, dh), dtype=q.dtype, device=dev)
+    else:
+        _arg(q_out, "q_out", (q.dtype,), (batch, T, q_heads, dh))
+    _on(dev, q=q, v=v, k_cache=k_cache, past_len=past_len, rope=rope, depths=depths,
+        num_nodes=num_nodes, q_out=q_out)
+    with torch.cuda.device(dev):
+        rc = lib().ddtree_append_kv(_ptr(q), _ptr(k), _ptr(v), _half_code(k), batch, T, q_heads,
+                                    kv_heads, dh, qs, ks, vs, _ptr(rope), rope_len, rot,
+                                    int(bool(interleaved)), _ptr(past_len), _ptr(depths),
+                                    _ptr(num_nodes), _ptr(page_table), width, pages, page_size,
+                                    _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _stream(dev))
+    _check("ddtree_append_kv", rc)
+    return q_out
+
+
+def ddtree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     past_len: torch.Tensor, *, page_table: torch.Tensor | None = None,
+                     num_nodes: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                     scale: float | None = None, with_lse: bool = False, out: dict | None = None,
+                     ws: torch.Tensor | None = None) -> dict:
+    """Verified block's attention: q [batch, T, q_heads, dh] (bf16/f16) over one layer's caches
+    [pages, kv_heads, page_size, dh] under the ancestor mask [batch, T, ceil(T/64)] (int64, as
+    ddtree_mask's; None: a chain); scale defaults to dh ** -0.5. Returns out (and lse)."""
+    _arg(q, "q", _HALF)
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, T, q_heads, head_dim]")
+    batch, T, q_heads, dh = q.shape
+    dev = q.device
+    pages, kv_heads, page_size, dc, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
+    if k_cache.dtype != q.dtype:
+        raise TypeError(f"k_cache must have dtype {q.dtype}, got {k_cache.dtype}")
+    if dc != dh:
+        raise ValueError(f"the caches must have head_dim {dh}, got {dc}")
+    _arg(past_len, "past_len", _I32, (batch,))
+    if num_nodes is not None:
+        _arg(num_nodes, "num_nodes", _I32, (batch,))
+    if mask is not None:
+        _arg(mask, "mask", (torch.int64,), (batch, T, (T + 63) // 64))
+    if out is None:
+        out = dict(out=torch.empty_like(q))
+        if with_lse:
+            out["lse"] = torch.empty((batch, T, q_heads), dtype=torch.float32, device=dev)
+    _arg(out["out"], "out", (q.dtype,), tuple(q.shape))
+    lse = out.get("lse")
+    if lse is not None:
+        _arg(lse, "lse", _F32, (batch, T, q_heads))
+    _on(dev, k_cache=k_cache, past_len=past_len, num_nodes=num_nodes, mask=mask, out=out["out"],
+        lse=lse, ws=ws)
+    with torch.cuda.device(dev):
+        if ws is None:
+            size = lib().ddtree_attention_workspace_size(batch, T, q_heads, kv_heads, dh, width,
+                                                         page_size)
+            ws = _scratch("attention", size, dev)
+        rc = lib().ddtree_attention(_ptr(q), _half_code(q), batch, T, q_heads, kv_heads, dh,
+                                    _ptr(k_cache), _ptr(v_cache), _ptr(page_table), width, pages,
+                                    page_size, _ptr(past_len), _ptr(num_nodes), _ptr(mask),
+                                    dh ** -0.5 if scale is None else float(scale),
+                                    _ptr(out["out"]), _ptr(lse), _ptr(ws), ws.numel(),
+                                    _stream(dev))
+    _check("ddtree_attention", rc)
+    return out
+
+
+def ddtree_compact_kv_paged(k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            page_table: torch.Tensor, past_len: torch.Tensor,
+                            accepted_nodes: torch.Tensor, accept_len: torch.Tensor,
+                            new_len: torch.Tensor | None = None) -> torch.Tensor:
+    """In place: paged caches [layers, pages, heads, page_size, head_dim] keep the accepted
+    path's rows (page_table [batch, width]); returns new_len [batch]."""
+    _arg(past_len, "past_len", _I32)
+    if past_len.dim() != 1:
+        raise ValueError("past_len must be [batch]")
+    batch = past_len.shape[0]
+    if page_table is None:
+        raise ValueError("page_table is required; ddtree_compact_kv takes contiguous caches")
+    pages, heads, page_size, dh, width = _paged_cache(k_cache, v_cache, page_table, batch, 5)
+    _arg(accepted_nodes, "accepted_nodes", _I32)
+    L = accepted_nodes.shape[-1]
+    _arg(accepted_nodes, "accepted_nodes", _I32, (batch, L))
+    _arg(accept_len, "accept_len", _I32, (batch,))
+    dev = k_cache.device
+    if new_len is None:
+        new_len = torch.empty((batch,), dtype=torch.int32, device=dev)
+    _arg(new_len, "new_len", _I32, (batch,))
+    _on(dev, past_len=past_len, accepted_nodes=accepted_nodes, accept_len=accept_len,
+        new_len=new_len)
+    with torch.cuda.device(dev):
+        rc = lib().ddtree_compact_kv_paged(_ptr(k_cache), _ptr(v_cache), k_cache.shape[0], pages,
+                                           heads, page_size, dh * k_cache.element_size(),
+                                           _ptr(page_table), width, batch, _ptr(past_len),
+                                           _ptr(accepted_nodes), _ptr(accept_len), L,
+                                           _ptr(new_len), _stream(dev))
+    _check("ddtree_compact_kv_paged", rc)
+    return new_len
+
+
+def ddtree_accept_sampled(tree_tokens: torch.Tensor, parents: torch.Tensor,
+                          num_nodes: torch.Tensor | None, target_logits: torch.Tensor,
+                          temperature: torch.Tensor | None, u: torch.Tensor, *,
+                          out: dict | None = None, ws: torch.Tensor | None = None) -> dict:
+    """Tree acceptance at a temperature: target_logits [batch, B+1, V] (bf16/f32), temperature
+    [batch] (None: 1; 0: greedy), u [batch, L+1] uniforms -> accepted_nodes [batch, L],
+    accept_len, next_token, logp [batch, L+1]."""
+    _arg(tree_tokens, "tree_tokens", _I32)
+    if tree_tokens.dim() != 2:
+        raise ValueError("tree_tokens must be [batch, B]")
+    batch, B = tree_tokens.shape
+    _arg(parents, "parents", _I32, (batch, B))
+    if num_nodes is not None:
+        _arg(num_nodes, "num_nodes", _I32, (batch,))
+    _arg(target_logits, "target_logits", _LOGITS)
+    V = target_logits.shape[-1]
+    _arg(target_logits, "target_logits", _LOGITS, (batch, B + 1, V))
+    if temperature is not None:
+        _arg(temperature, "temperature", _F32, (batch,))
+    _arg(u, "u", _F32)
+    if u.dim() != 2 or u.shape[0] != batch:
+        raise ValueError(f"u must have shape ({batch}, L + 1), got {tuple(u.shape)}")
+    L = u.shape[1] - 1
+    dev = target_logits.device
+    dt = _dtype_code(target_logits)
+    if out is None:
+        out = dict(accepted_nodes=torch.empty((batch, L), dtype=torch.int32, device=dev),
+                   accept_len=torch.empty((batch,), dtype=torch.int32, device=dev),
+                   next_token=torch.empty((batch,), dtype=torch.int32, device=dev),
+                   logp=torch.empty((batch, L + 1), dtype=torch.float32, device=dev))
+    _accepted_out(out, dev, batch, L)
+    _arg(out["accepted_nodes"], "accepted_nodes", _I32, (batch, L))
+    _on(dev, tree_tokens=tree_tokens, parents=parents, num_nodes=num_nodes,
+        temperature=temperature, u=u, ws=ws, accepted_nodes=out["accepted_nodes"])
+    with torch.cuda.device(dev):
+        if ws is None:
+            size = lib().ddtree_accept_sampled_workspace_size(batch, B, L, V, dt)
+            ws = _scratch("accept_sampled", size, dev)
+        rc = lib().ddtree_accept_sampled(_ptr(tree_tokens), _ptr(parents), _ptr(num_nodes),
+                                         _ptr(target_logits), dt, _ptr(temperature), _ptr(u),
+                                         batch, B, L, V, _ptr(out["accepted_nodes"]),
+                                         _ptr(out["accept_len"]), _ptr(out["next_token"]),
+                                         _ptr(out.get("logp")), _ptr(ws), ws.numel(),
+                                         _stream(dev))
+    _check("ddtree_accept_sampled", rc)
+    return out
+
+
+def _accepted_out(out, dev, batch, L):
+    _arg(out["accept_len"], "accept_len", _I32, (batch,))
+    _arg(out["next_token"], "next_token", _I32, (batch,))
+    if out.get("logp") is not None:
+        _arg(out["logp"], "logp", _F32, (batch, L + 1))
+    _on(dev, accept_len=out["accept_len"], next_token=out["next_token"], logp=out.get("logp"))
+
+
+def dspark_accept_sampled(tokens: torch.Tensor, target_logits: torch.Tensor,
+                          draft_logits: torch.Tensor, temperature: torch.Tensor | None,
+                          u: torch.Tensor, *, keep: torch.Tensor | None = None,
+                          out: dict | None = None, ws: torch.Tensor | None = None) -> dict:
+    """Verification of a sampled chain: tokens [batch, P], target_logits [batch, P+1, V],
+    draft_logits [batch, P, V] (bf16/f32), temperature [batch] (None: 1; 0: greedy), u
+    [batch, P+1] uniforms, keep [batch] -> accept_len, next_token, logp [batch, P+1]."""
+    _arg(tokens, "tokens", _I32)
+    if tokens.dim() != 2:
+        raise ValueError("tokens must be [batch, P]")
+    batch, P = tokens.shape
+    _arg(target_logits, "target_logits", _LOGITS)
+    V = target_logits.shape[-1]
+    _arg(target_logits, "target_logits", _LOGITS, (batch, P + 1, V))
+    _arg(draft_logits, "draft_logits", (target_logits.dtype,), (batch, P, V))
+    if temperature is not None:
+        _arg(temperature, "temperature", _F32, (batch,))
+    _arg(u, "u", _F32, (batch, P + 1))
+    if keep is not None:
+        _arg(keep, "keep", _I32, (batch,))
+    dev = target_logits.device
+    dt = _dtype_code(target_logits)
+    if out is None:
+        out = dict(accept_len=torch.empty((batch,), dtype=torch.int32, device=dev),
+                   next_token=torch.empty((batch,), dtype=torch.int32, device=dev),
+                   logp=torch.empty((batch, P + 1), dtype=torch.float32, device=dev))
+    _accepted_out(out, dev, batch, P)
+    _on(dev, tokens=tokens, draft_logits=draft_logits, temperature=temperature, u=u, keep=keep,
+        ws=ws)
+    with torch.cuda.device(dev):
+        if ws is None:
+            size = lib().dspark_accept_sampled_workspace_size(batch, P, V, dt)
+            ws = _scratch("chain_accept_sampled", size, dev)
+        rc = lib().dspark_accept_sampled(_ptr(tokens), _ptr(keep), _ptr(target_logits),
+                                         _ptr(draft_logits), dt, _ptr(temperature), _ptr(u), batch,
+                                         P, V, _ptr(out["accept_len"]), _ptr(out["next_token"]),
+                                         _ptr(out.get("logp")), _ptr(ws), ws.numel(),
+                                         _stream(dev))
+    _check("dspark_accept_sampled", rc)
     return out

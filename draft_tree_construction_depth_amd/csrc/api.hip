@@ -12,6 +12,9 @@
 #include "treespark.hpp"
 #include "walk.hpp"
 #include "kv.hpp"
+#include "append.hpp"
+#include "attention.hpp"
+#include "sampled.hpp"
 #include "sparkling.hpp"
 #include "dspark.hpp"
 #include "beam.hpp"
@@ -441,6 +444,130 @@ int build_launch(const void* logits, int dtype, int64_t batch, int32_t L, int64_
                        num_nodes, mask, stream);
 }
 
+// ---- paged caches -------------------------------------------------------------
+// A layer's cache of `pages` pages and the table that maps `batch` requests'
+// rows onto it (null: page b is request b's). Page sizes behind a table are
+// powers of two, so that no row needs a division.
+int paged_rows(const int32_t* table, int64_t width, int64_t batch, int64_t pages,
+               int64_t page_size, ddt::PagedRows& r) {
+  if (pages <= 0 || page_size <= 0 || (table && width <= 0)) return DDT_EINVAL;
+  if (!table && pages != batch) return DDT_EINVAL;
+  if (pages > 0x7FFFFFFFLL || page_size > 0x7FFFFFFFLL || width > 0x7FFFFFFFLL) return DDT_ENOTSUP;
+  if (table && (page_size & (page_size - 1))) return DDT_ENOTSUP;
+  r.table = table;
+  r.width = table ? width : 1;
+  r.pages = pages;
+  r.page_size = (int32_t)page_size;
+  r.shift = 31;
+  if (table)
+    for (r.shift = 0; ((int64_t)1 << r.shift) < page_size; ++r.shift) {
+    }
+  r.cap = r.width * page_size;
+  if (r.cap > 0x7FFFFFFFLL) r.cap = 0x7FFFFFFFLL;  // lengths are 32-bit
+  return DDT_OK;
+}
+
+bool valid_half(int dtype) { return dtype == DDT_BF16 || dtype == DDT_F16; }
+
+template <typename H>
+void launch_append(const ddt::AppendParams& ap, int64_t blocks, int interleaved, hipStream_t st) {
+  if (interleaved)
+    hipLaunchKernelGGL((ddt::append_kernel<H, true>), dim3((unsigned)blocks), dim3(ddt::kApThreads),
+                       0, st, ap);
+  else
+    hipLaunchKernelGGL((ddt::append_kernel<H, false>), dim3((unsigned)blocks),
+                       dim3(ddt::kApThreads), 0, st, ap);
+}
+
+template <typename H>
+void launch_attn(const ddt::AttnParams& ap, int head_dim, hipStream_t st) {
+  const dim3 grid((unsigned)(ap.batch * ap.T * ap.q_heads)), block(ddt::kWave);
+  switch (head_dim) {
+    case 64: hipLaunchKernelGGL((ddt::attn_row_kernel<H, 64>), grid, block, 0, st, ap); break;
+    case 128: hipLaunchKernelGGL((ddt::attn_row_kernel<H, 128>), grid, block, 0, st, ap); break;
+    default: hipLaunchKernelGGL((ddt::attn_row_kernel<H, 256>), grid, block, 0, st, ap); break;
+  }
+}
+
+int attn_check(int dtype, int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
+               int32_t head_dim) {
+  if (!valid_half(dtype) || batch < 0 || T <= 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0)
+    return DDT_EINVAL;
+  if (q_heads % kv_heads != 0) return DDT_EINVAL;
+  if (T > DDT_MAX_B + 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return DDT_ENOTSUP;
+  if (batch > 0x7FFFFFFFLL || batch * T > 0x7FFFFFFFLL / q_heads) return DDT_ENOTSUP;
+  return DDT_OK;
+}
+
+// ---- acceptance at a temperature: schedule and workspace ------------------------
+struct SvPlan {
+  int S;         // chunks per row
+  bool stepped;  // records of the path's rows only, one launch per depth
+  size_t rec, rec_q, state, rest, end;
+};
+
+int accept_check(int dtype, int64_t batch, int32_t T, int32_t L, int64_t V) {
+  if (!valid_dtype(dtype) || batch < 0 || T <= 1 || L <= 0 || V <= 0) return DDT_EINVAL;
+  if (T > DDT_MAX_B + 1 || L > DDT_MAX_L || V > ((int64_t)1 << 22)) return DDT_ENOTSUP;
+  if (batch > 0x7FFFFFFFLL / (2 * ddt::kSvMaxS) ||
+      batch * T > 0x7FFFFFFFLL / (2 * ddt::kSvMaxS))  // workgroups of a launch
+    return DDT_ENOTSUP;
+  return DDT_OK;
+}
+
+SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bool chain) {
+  const int N = elems_per_vec(dtype);
+  const int64_t chunk = (int64_t)ddt::kSvThreads * ddt::kSvVecs * N;
+  SvPlan pl;
+  pl.S = (int)((V + (V % N ? N - 1 : 0) + chunk - 1) / chunk);
+  const int64_t rows = batch * T + (chain ? batch * (T - 1) : 0);
+  pl.stepped = false;
+  const size_t rec = sizeof(ddt::SvRec);
+  size_t o = 0;
+  pl.rec = o;
+  o = align_up(o + (pl.stepped ? 2 * (size_t)batch : (size_t)batch * T) * pl.S * rec);
+  pl.rec_q = o;
+  if (chain) o = align_up(o + (pl.stepped ? 2 * (size_t)batch : (size_t)batch * (T - 1)) * pl.S * rec);
+  pl.state = o;
+  o = align_up(o + (size_t)batch * (L + 2) * sizeof(ddt::SvState));
+  pl.rest = o;
+  if (chain) o = align_up(o + (size_t)batch * pl.S * sizeof(double));
+  pl.end = o;
+  (void)rows;
+  return pl;
+}
+
+template <int DT, bool CHAIN>
+int accept_launch(const SvPlan& pl, const ddt::SvParams& sp, hipStream_t st) {
+  const dim3 block(ddt::kSvThreads), each((unsigned)sp.batch);
+  const int64_t per = CHAIN ? 2 : 1;
+  if (pl.stepped) {
+    for (int step = 0; step <= sp.L; ++step) {
+      hipLaunchKernelGGL((ddt::sv_step_kernel<DT, CHAIN>), dim3((unsigned)(sp.batch * per * pl.S)),
+                         block, 0, st, sp, step);
+      if (hipGetLastError() != hipSuccess) return DDT_EHIP;
+    }
+  } else {
+    const int64_t rows = sp.batch * sp.T + (CHAIN ? sp.batch * (sp.T - 1) : 0);
+    hipLaunchKernelGGL((ddt::sv_rows_kernel<DT, CHAIN>), dim3((unsigned)(rows * pl.S)), block, 0,
+                       st, sp);
+    if (hipGetLastError() != hipSuccess) return DDT_EHIP;
+  }
+  if (!CHAIN) {
+    hipLaunchKernelGGL((ddt::sv_finish_kernel<DT>), each, block, 0, st, sp, sp.L);
+    return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+  }
+  const int at = pl.stepped ? sp.L + 1 : 0;  // the walk's last state
+  hipLaunchKernelGGL((ddt::sv_chain_walk_kernel<DT>), each, block, 0, st, sp, sp.L);
+  if (hipGetLastError() != hipSuccess) return DDT_EHIP;
+  hipLaunchKernelGGL((ddt::sv_chain_rest_kernel<DT>), dim3((unsigned)(sp.batch * pl.S)), block, 0,
+                     st, sp, at);
+  if (hipGetLastError() != hipSuccess) return DDT_EHIP;
+  hipLaunchKernelGGL((ddt::sv_chain_finish_kernel<DT>), each, block, 0, st, sp, at);
+  return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+}
+
 // ---- the static scratch of ddtree_build_noalloc ------------------------------
 // One array per GPU, held until the process ends. In host code `scratch`
 // names a host-side stand-in, never the device memory: every use goes
@@ -686,6 +813,242 @@ int ddtree_compact_kv(void* k_cache, void* v_cache, int64_t layers, int64_t batc
   hipLaunchKernelGGL(ddt::kv_compact_kernel, dim3((unsigned)blocks), dim3(ddt::kKvThreads), 0,
                      stream, kp);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+}
+
+int ddtree_compact_kv_paged(void* k_cache, void* v_cache, int64_t layers, int64_t pages,
+                            int32_t heads, int32_t page_size, int32_t row_bytes,
+                            const int32_t* page_table, int64_t table_width, int64_t batch,
+                            const int32_t* past_len, const int32_t* accepted_nodes,
+                            const int32_t* accept_len, int32_t L, int32_t* new_len,
+                            hipStream_t stream) {
+  if (layers < 0 || batch < 0 || heads < 0 || row_bytes <= 0 || L <= 0) return DDT_EINVAL;
+  if (layers == 0 || batch == 0 || heads == 0) return DDT_OK;
+  if (!k_cache || !v_cache || !page_table || !past_len || !accepted_nodes || !accept_len)
+    return DDT_EINVAL;
+  if (((uintptr_t)k_cache | (uintptr_t)v_cache) & 15) return DDT_EINVAL;
+  ddt::KvPagedParams kp;
+  const int chk = paged_rows(page_table, table_width, batch, pages, page_size, kp.rows);
+  if (chk != DDT_OK) return chk;
+  if (row_bytes % 16 != 0 || row_bytes > 1024 || L > DDT_MAX_L) return DDT_ENOTSUP;
+  const int64_t per_block = ddt::kKvThreads / ddt::kWave;
+  if (batch > 0x7FFFFFFFLL || layers > 0x7FFFFFFFLL / batch ||
+      (layers * batch) > 0x7FFFFFFFLL * per_block / heads)
+    return DDT_ENOTSUP;
+  const int64_t blocks = (layers * batch * heads + per_block - 1) / per_block;
+  kp.k = (unsigned char*)k_cache;
+  kp.v = (unsigned char*)v_cache;
+  kp.layers = layers;
+  kp.batch = batch;
+  kp.heads = heads;
+  kp.row_bytes = row_bytes;
+  kp.past_len = past_len;
+  kp.accepted = accepted_nodes;
+  kp.accept_len = accept_len;
+  kp.L = L;
+  kp.new_len = new_len;
+  hipLaunchKernelGGL(ddt::kv_compact_paged_kernel, dim3((unsigned)blocks), dim3(ddt::kKvThreads),
+                     0, stream, kp);
+  return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+}
+
+int ddtree_append_kv(const void* q, const void* k, const void* v, int dtype, int64_t batch,
+                     int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                     int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* rope,
+                     int64_t rope_len, int32_t rope_dim, int32_t interleaved,
+                     const int32_t* past_len, const int32_t* depths, const int32_t* num_nodes,
+                     const int32_t* page_table, int64_t table_width, int64_t pages,
+                     int32_t page_size, void* k_cache, void* v_cache, void* q_out,
+                     hipStream_t stream) {
+  if (!valid_half(dtype) || batch < 0 || T <= 0 || q_heads < 0 || kv_heads <= 0 || head_dim <= 0 ||
+      rope_dim < 0 || rope_dim > head_dim || rope_len < 0 || (interleaved != 0 && interleaved != 1))
+    return DDT_EINVAL;
+  if (q_heads > 0 && q_heads % kv_heads != 0) return DDT_EINVAL;
+  if (batch == 0) return DDT_OK;
+  if (!k || !v || !past_len || !k_cache || !v_cache || (rope_dim > 0 && !rope)) return DDT_EINVAL;
+  if (q_heads > 0 && (!q || !q_out)) return DDT_EINVAL;
+  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)rope | (uintptr_t)k_cache |
+       (uintptr_t)v_cache | (uintptr_t)q_out) & 15)
+    return DDT_EINVAL;
+  if ((q_heads > 0 && q_stride < (int64_t)q_heads * head_dim) ||
+      k_stride < (int64_t)kv_heads * head_dim || v_stride < (int64_t)kv_heads * head_dim)
+    return DDT_EINVAL;
+  ddt::AppendParams ap;
+  const int chk = paged_rows(page_table, table_width, batch, pages, page_size, ap.rows);
+  if (chk != DDT_OK) return chk;
+  if (T > DDT_MAX_B + 1 || head_dim % 8 != 0 || head_dim > 512 || rope_dim % 16 != 0 ||
+      q_heads > 0xFFFF || kv_heads > 0xFFFF)
+    return DDT_ENOTSUP;
+  if ((q_heads > 0 && q_stride % 8 != 0) || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return DDT_ENOTSUP;
+  if (batch > 0x7FFFFFFFLL / T) return DDT_ENOTSUP;
+  ap.q = q;
+  ap.k = k;
+  ap.v = v;
+  ap.q_stride = q_stride;
+  ap.k_stride = k_stride;
+  ap.v_stride = v_stride;
+  ap.T = T;
+  ap.q_heads = q_heads;
+  ap.kv_heads = kv_heads;
+  ap.head_dim = head_dim;
+  ap.rope = rope;
+  ap.rope_len = rope_len;
+  ap.rot = rope_dim;
+  ap.past_len = past_len;
+  ap.depths = depths;
+  ap.num_nodes = num_nodes;
+  ap.k_cache = k_cache;
+  ap.v_cache = v_cache;
+  ap.q_out = q_out;
+  if (dtype == DDT_BF16)
+    launch_append<__bf16>(ap, batch * T, interleaved, stream);
+  else
+    launch_append<_Float16>(ap, batch * T, interleaved, stream);
+  return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+}
+
+size_t ddtree_attention_workspace_size(int64_t batch, int32_t T, int32_t q_heads,
+                                       int32_t kv_heads, int32_t head_dim, int64_t pages_per_request,
+                                       int32_t page_size) {
+  if (batch <= 0 || pages_per_request <= 0 || page_size <= 0 ||
+      attn_check(DDT_BF16, batch, T, q_heads, kv_heads, head_dim) != DDT_OK)
+    return 0;
+  return kAlign;
+}
+
+int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
+                     int32_t kv_heads, int32_t head_dim, const void* k_cache, const void* v_cache,
+                     const int32_t* page_table, int64_t table_width, int64_t pages,
+                     int32_t page_size, const int32_t* past_len, const int32_t* num_nodes,
+                     const uint64_t* mask, float scale, void* out, float* lse, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream) {
+  const int chk = attn_check(dtype, batch, T, q_heads, kv_heads, head_dim);
+  if (chk == DDT_EINVAL) return chk;
+  if (batch == 0) return DDT_OK;
+  if (!q || !k_cache || !v_cache || !past_len || !out || !workspace) return DDT_EINVAL;
+  if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out |
+       (uintptr_t)workspace) & 15)
+    return DDT_EINVAL;
+  if (!(scale > 0.0f && scale < INFINITY)) return DDT_EINVAL;
+  ddt::AttnParams ap;
+  const int chk2 = paged_rows(page_table, table_width, batch, pages, page_size, ap.rows);
+  if (chk2 == DDT_EINVAL) return chk2;
+  if (chk != DDT_OK || chk2 != DDT_OK) return DDT_ENOTSUP;
+  if (workspace_bytes < ddtree_attention_workspace_size(batch, T, q_heads, kv_heads, head_dim,
+                                                        ap.rows.width, page_size))
+    return DDT_EWORKSPACE;
+  ap.q = q;
+  ap.k_cache = k_cache;
+  ap.v_cache = v_cache;
+  ap.batch = batch;
+  ap.T = T;
+  ap.q_heads = q_heads;
+  ap.kv_heads = kv_heads;
+  ap.past_len = past_len;
+  ap.num_nodes = num_nodes;
+  ap.mask = mask;
+  ap.W = (T + 63) / 64;
+  ap.scale2 = scale * ddt::kLog2e;
+  ap.out = out;
+  ap.lse = lse;
+  if (dtype == DDT_BF16)
+    launch_attn<__bf16>(ap, head_dim, stream);
+  else
+    launch_attn<_Float16>(ap, head_dim, stream);
+  return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+}
+
+size_t ddtree_accept_sampled_workspace_size(int64_t batch, int32_t B, int32_t L, int64_t V,
+                                            int dtype) {
+  if (batch <= 0 || B <= 0 || B > DDT_MAX_B || accept_check(dtype, batch, B + 1, L, V) != DDT_OK)
+    return 0;
+  return accept_plan(batch, B + 1, L, V, dtype, false).end;
+}
+
+int ddtree_accept_sampled(const int32_t* tree_tokens, const int32_t* parents,
+                          const int32_t* num_nodes, const void* target_logits, int dtype,
+                          const float* temperature, const float* u, int64_t batch, int32_t B,
+                          int32_t L, int64_t V, int32_t* accepted_nodes, int32_t* accept_len,
+                          int32_t* next_token, float* logp, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  if (B <= 0) return DDT_EINVAL;
+  const int chk = B > DDT_MAX_B ? DDT_ENOTSUP : accept_check(dtype, batch, B + 1, L, V);
+  if (chk != DDT_OK) return chk;
+  if (batch == 0) return DDT_OK;
+  if (!tree_tokens || !parents || !target_logits || !u || !accepted_nodes || !accept_len ||
+      !next_token || !workspace)
+    return DDT_EINVAL;
+  if (((uintptr_t)target_logits | (uintptr_t)workspace) & 15) return DDT_EINVAL;
+  const SvPlan pl = accept_plan(batch, B + 1, L, V, dtype, false);
+  if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
+  char* ws = (char*)workspace;
+  ddt::SvParams sp{};
+  sp.logits = target_logits;
+  sp.batch = batch;
+  sp.V = V;
+  sp.T = B + 1;
+  sp.L = L;
+  sp.tokens = tree_tokens;
+  sp.parents = parents;
+  sp.count = num_nodes;
+  sp.temperature = temperature;
+  sp.u = u;
+  sp.accepted = accepted_nodes;
+  sp.accept_len = accept_len;
+  sp.next_token = next_token;
+  sp.logp = logp;
+  sp.S = pl.S;
+  sp.stepped = pl.stepped;
+  sp.rec = (ddt::SvRec*)(ws + pl.rec);
+  sp.state = (ddt::SvState*)(ws + pl.state);
+  return dtype == DDT_BF16 ? accept_launch<0, false>(pl, sp, stream)
+                           : accept_launch<1, false>(pl, sp, stream);
+}
+
+size_t dspark_accept_sampled_workspace_size(int64_t batch, int32_t P, int64_t V, int dtype) {
+  if (batch <= 0 || P <= 0 || P > DDT_MAX_L || accept_check(dtype, batch, P + 1, P, V) != DDT_OK)
+    return 0;
+  return accept_plan(batch, P + 1, P, V, dtype, true).end;
+}
+
+int dspark_accept_sampled(const int32_t* tokens, const int32_t* keep, const void* target_logits,
+                          const void* draft_logits, int dtype, const float* temperature,
+                          const float* u, int64_t batch, int32_t P, int64_t V,
+                          int32_t* accept_len, int32_t* next_token, float* logp, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  if (P <= 0) return DDT_EINVAL;
+  const int chk = P > DDT_MAX_L ? DDT_ENOTSUP : accept_check(dtype, batch, P + 1, P, V);
+  if (chk != DDT_OK) return chk;
+  if (batch == 0) return DDT_OK;
+  if (!tokens || !target_logits || !draft_logits || !u || !accept_len || !next_token || !workspace)
+    return DDT_EINVAL;
+  if (((uintptr_t)target_logits | (uintptr_t)draft_logits | (uintptr_t)workspace) & 15)
+    return DDT_EINVAL;
+  const SvPlan pl = accept_plan(batch, P + 1, P, V, dtype, true);
+  if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
+  char* ws = (char*)workspace;
+  ddt::SvParams sp{};
+  sp.logits = target_logits;
+  sp.draft = draft_logits;
+  sp.batch = batch;
+  sp.V = V;
+  sp.T = P + 1;
+  sp.L = P;
+  sp.tokens = tokens;
+  sp.count = keep;
+  sp.temperature = temperature;
+  sp.u = u;
+  sp.accept_len = accept_len;
+  sp.next_token = next_token;
+  sp.logp = logp;
+  sp.S = pl.S;
+  sp.stepped = pl.stepped;
+  sp.rec = (ddt::SvRec*)(ws + pl.rec);
+  sp.rec_q = (ddt::SvRec*)(ws + pl.rec_q);
+  sp.state = (ddt::SvState*)(ws + pl.state);
+  sp.rest = (double*)(ws + pl.rest);
+  return dtype == DDT_BF16 ? accept_launch<0, true>(pl, sp, stream)
+                           : accept_launch<1, true>(pl, sp, stream);
 }
 
 size_t treespark_workspace_size(int64_t batch, int32_t D, int64_t V, int32_t H, int32_t k,

@@ -17,7 +17,7 @@
 // have returned.
 #pragma once
 
-#include "common.hpp"
+#include "paged.hpp"
 
 namespace ddt {
 
@@ -81,6 +81,77 @@ __global__ __launch_bounds__(kKvThreads) void kv_compact_kernel(KvParams p) {
         const size_t dof = slice_off + (size_t)dst[g] * p.row_bytes + 16 * ch;
         *(kv_u32x4*)(p.k + dof) = kr[g];
         *(kv_u32x4*)(p.v + dof) = vr[g];
+      }
+    }
+  }
+}
+
+struct KvPagedParams {
+  unsigned char* k;  // [layers][pages][heads][page_size][row_bytes]
+  unsigned char* v;
+  int64_t layers, batch;
+  int32_t heads;
+  int32_t row_bytes;  // multiple of 16, <= 1024
+  PagedRows rows;
+  const int32_t* past_len;
+  const int32_t* accepted;
+  const int32_t* accept_len;
+  int32_t L;
+  int32_t* new_len;  // [batch], may be null
+};
+
+// The same compaction through a page table: one wavefront per (layer,
+// request, head), the rows' pages looked up per lane. The argument for doing
+// it in place is the same, since a request's rows lie on pages of its own.
+__global__ __launch_bounds__(kKvThreads) void kv_compact_paged_kernel(KvPagedParams p) {
+  const int64_t slices = p.layers * p.batch * p.heads;
+  const int64_t slice = (int64_t)blockIdx.x * (kKvThreads / kWave) + (threadIdx.x >> 6);
+  if (slice >= slices) return;  // whole wave
+  const int lane = threadIdx.x & 63;
+  const int64_t b = (slice / p.heads) % p.batch;
+  const int head = (int)(slice % p.heads);
+  const int64_t layer = slice / (p.heads * p.batch);
+  const int past = p.past_len[b];
+  int n = p.accept_len[b];
+  n = n < 0 ? 0 : (n > p.L ? p.L : n);
+  if (layer == 0 && head == 0 && lane == 0 && p.new_len) p.new_len[b] = past + n + 1;
+  if (past < 0) return;
+  const int lpr = p.row_bytes >> 4;  // lanes per row
+  const int rpi = kWave / lpr;       // rows per load instruction
+  const int q = lane / lpr, ch = lane - q * lpr;
+  const bool lane_on = q < rpi;
+  const int32_t* acc = p.accepted + b * p.L;
+  // byte offset of this lane's part of cache row r, -1 where no page holds it
+  auto offset = [&](int64_t r) -> int64_t {
+    if (r >= p.rows.cap) return -1;
+    const int page = page_of(p.rows, b, (int)r);
+    if (page < 0) return -1;
+    return ((((layer * p.rows.pages + page) * p.heads + head) * p.rows.page_size) +
+            row_in_page(p.rows, (int)r)) * (int64_t)p.row_bytes + 16 * ch;
+  };
+  for (int i0 = 1; i0 <= n; i0 += kKvBatch * rpi) {  // uniform
+    kv_u32x4 kr[kKvBatch], vr[kKvBatch];
+    int64_t dst[kKvBatch];
+#pragma unroll
+    for (int g = 0; g < kKvBatch; ++g) {
+      const int i = i0 + g * rpi + q;
+      dst[g] = -1;
+      if (lane_on && i <= n) {
+        const int node = acc[i - 1];
+        const int64_t so = node >= 0 ? offset((int64_t)past + node) : -1;
+        const int64_t d = offset((int64_t)past + i);
+        if (so >= 0 && d >= 0) {
+          kr[g] = *(const kv_u32x4*)(p.k + so);
+          vr[g] = *(const kv_u32x4*)(p.v + so);
+          dst[g] = d;
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kKvBatch; ++g) {
+      if (dst[g] >= 0) {
+        *(kv_u32x4*)(p.k + dst[g]) = kr[g];
+        *(kv_u32x4*)(p.v + dst[g]) = vr[g];
       }
     }
   }

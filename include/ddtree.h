@@ -34,6 +34,16 @@
  *  - dspark_budget: DSpark's survival-ranked verification budget. DSpark
  *    explainer, section "Hardware aware prefix scheduler"; DSpark guide,
  *    sections "Survival probability" and "Picking the budget".
+ *  - ddtree_append_kv, ddtree_attention, ddtree_compact_kv_paged: the
+ *    verification pass's side of the round. The block's keys and values go
+ *    into a paged cache (rotated by the position of each node's depth), its
+ *    attention reads the cache under the ancestor mask, and the accepted
+ *    path's rows are kept. DDTree explainer, section 5; SparklingTree post,
+ *    section "Step 4".
+ *  - ddtree_accept_sampled, dspark_accept_sampled: acceptance at a
+ *    temperature from given random numbers, for trees and for sampled chains
+ *    (DSpark explainer, speculative decoding basics), in place of the greedy
+ *    walk.
  *  - ddtree_select: stage 2 alone, from stage 1's tables. DDTree explainer,
  *    sections 3-4; SparklingTree post, section "Step 3".
  *    ddtree_build = ddtree_row_topk + ddtree_select in one call.
@@ -76,7 +86,9 @@ enum {
   DDT_EHIP = -4        /* a HIP launch failed */
 };
 
-enum { DDT_BF16 = 0, DDT_F32 = 1 };
+/* Element types. Logits are DDT_BF16 or DDT_F32; the verification pass's
+ * queries, keys and values are DDT_BF16 or DDT_F16. */
+enum { DDT_BF16 = 0, DDT_F32 = 1, DDT_F16 = 2 };
 
 /* Supported region. */
 #define DDT_MAX_B 512   /* node budget */
@@ -221,6 +233,174 @@ int ddtree_compact_kv(void* k_cache, void* v_cache, int64_t layers, int64_t batc
                       int32_t heads, int64_t cap, int32_t row_bytes, const int32_t* past_len,
                       const int32_t* accepted_nodes, const int32_t* accept_len, int32_t L,
                       int32_t* new_len, hipStream_t stream);
+
+/*
+ * Paged caches. ddtree_append_kv, ddtree_attention and ddtree_compact_kv_paged
+ * share one layout: a layer's cache is [pages][kv_heads][page_size][head_dim],
+ * and row r of request b lies on page page_table[b][r / page_size] at row
+ * r % page_size. page_table is [batch][table_width] int32; page_size is then a
+ * power of two (DDT_ENOTSUP otherwise). An entry outside [0, pages) (such as
+ * -1) maps no page: its rows are neither written nor seen. Rows at or past
+ * table_width * page_size (and past 2^31 - 2) do not exist. A page that holds
+ * rows at or behind past_len belongs to one request; pages before it may be
+ * shared. With page_table NULL (append and attention) the cache is contiguous,
+ * [batch][kv_heads][capacity][head_dim]: one layer of ddtree_compact_kv's
+ * cache, pages = batch (DDT_EINVAL otherwise) and page_size = any capacity.
+ *
+ * The verified block of request b has T rows: the root (row 0) and up to
+ * T - 1 nodes in output order; row j lies at cache row past_len[b] + j. Only
+ * rows 0..num_nodes[b] take part (num_nodes NULL: all; values are clamped
+ * into [0, T - 1]). T = 1 is plain decoding. A negative past_len[b] takes the
+ * request out: nothing is written for it, and its attention is that of rows
+ * that see nothing.
+ */
+
+/*
+ * ddtree_append_kv -- the verified block's keys and values into a paged cache,
+ * with the position rotation applied on the way (to the queries as well).
+ * Row j stands at position past_len[b] + depths[b][j-1] (the root: past_len;
+ * depths NULL: past_len + j, a chain or a prompt's piece), since nodes of one
+ * depth are alternatives for one place. Elements 0..rope_dim-1 of every query
+ * and key head turn in pairs, (x, y) -> (x cos - y sin, y cos + x sin): pair i
+ * is elements (i, i + rope_dim/2), or with interleaved = 1 (2i, 2i + 1).
+ * rope is [rope_len][rope_dim] float: rope_dim/2 cosines, then as many sines,
+ * per position. The rotation is float32, rounded once; elements from rope_dim
+ * on and the values are copied bit for bit. rope_dim = 0 rotates nothing
+ * (rope may be NULL then).
+ * q, k, v      rows of [heads][head_dim] elements, row j of request b at
+ *              (b * T + j) * stride elements: slices of one fused projection
+ *              are read in place. q and q_out may be NULL with q_heads = 0;
+ * q_out        [batch][T][q_heads][head_dim], contiguous. May be q itself if
+ *              q is contiguous; otherwise it must not overlap the inputs.
+ * A row past num_nodes, or whose position is outside [0, rope_len) (with
+ * rope_dim > 0), is left out: q_out and the caches keep what they hold there.
+ * A row without a cache row (see above) still writes its q_out.
+ * Supported: head_dim a multiple of 8 up to 512, rope_dim a multiple of 16 up
+ * to head_dim, T <= DDT_MAX_B + 1, strides multiples of 8 (DDT_ENOTSUP
+ * otherwise); pointers 16-byte aligned, strides at least a row (DDT_EINVAL).
+ */
+int ddtree_append_kv(const void* q, const void* k, const void* v, int dtype, int64_t batch,
+                     int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                     int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* rope,
+                     int64_t rope_len, int32_t rope_dim, int32_t interleaved,
+                     const int32_t* past_len, const int32_t* depths, const int32_t* num_nodes,
+                     const int32_t* page_table, int64_t table_width, int64_t pages,
+                     int32_t page_size, void* k_cache, void* v_cache, void* q_out,
+                     hipStream_t stream);
+
+/*
+ * ddtree_attention -- the verified block's attention over its paged cache.
+ * Row i of request b sees the cache rows before past_len[b] and, of the
+ * block's own, row j <= num_nodes[b] iff bit j of mask row i is set (mask
+ * [batch][T][ceil(T/64)] uint64 as written by ddtree_mask with B = T - 1;
+ * mask NULL: iff j <= i). With a_n = softmax of scale * q_i . K_n over the
+ * rows seen: out_i = sum_n a_n V_n, and lse_i = the natural log of
+ * sum_n exp(scale * q_i . K_n). Query head h reads key/value head
+ * h / (q_heads / kv_heads). Rows that see nothing (past num_nodes, an empty
+ * mask row with no past) give out 0 and lse -inf; what lies in cache rows
+ * that a row does not see (NaN and infinities included) does not reach it.
+ * q, out [batch][T][q_heads][head_dim], contiguous, 16-byte aligned, like the
+ *        caches of dtype DDT_BF16 or DDT_F16; lse [batch][T][q_heads] float,
+ *        may be NULL.
+ * Scores, maxima, sums and accumulators are float32; a weight is rounded to
+ * dtype for its product with V.
+ * Supported: head_dim 64, 128 or 256, q_heads a multiple of kv_heads
+ * (DDT_EINVAL otherwise), T <= DDT_MAX_B + 1, 0 < scale < inf (DDT_EINVAL).
+ * The workspace (ddtree_attention_workspace_size bytes, no zero-fill needed;
+ * pages_per_request = table_width, or 1 without a table) holds partial
+ * results of long caches split over workgroups.
+ */
+size_t ddtree_attention_workspace_size(int64_t batch, int32_t T, int32_t q_heads,
+                                       int32_t kv_heads, int32_t head_dim,
+                                       int64_t pages_per_request, int32_t page_size);
+int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
+                     int32_t kv_heads, int32_t head_dim, const void* k_cache, const void* v_cache,
+                     const int32_t* page_table, int64_t table_width, int64_t pages,
+                     int32_t page_size, const int32_t* past_len, const int32_t* num_nodes,
+                     const uint64_t* mask, float scale, void* out, float* lse, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ddtree_compact_kv_paged -- ddtree_compact_kv through a page table, for
+ * caches [layers][pages][heads][page_size][row_bytes]: rows past_len[b] + i,
+ * i = 1..accept_len[b], take the rows at past_len[b] + accepted_nodes[b][i-1]
+ * in every layer and head, in place; every other row is left as it was. Rows
+ * whose source or destination no page holds are skipped, as is a request with
+ * a negative past_len. new_len, row_bytes, L and alignment as in
+ * ddtree_compact_kv; page_table is required here.
+ */
+int ddtree_compact_kv_paged(void* k_cache, void* v_cache, int64_t layers, int64_t pages,
+                            int32_t heads, int32_t page_size, int32_t row_bytes,
+                            const int32_t* page_table, int64_t table_width, int64_t batch,
+                            const int32_t* past_len, const int32_t* accepted_nodes,
+                            const int32_t* accept_len, int32_t L, int32_t* new_len,
+                            hipStream_t stream);
+
+/*
+ * ddtree_accept_sampled -- the walk of ddtree_accept at a temperature, from
+ * given random numbers, for trees whose drafts are a function of the drafter's
+ * rows (ddtree_build, treespark_expand, sparkling_build, sparkling_beam). At a
+ * node of depth d with target row x let w(v) = exp((x_v - max x) / T), Z their
+ * sum and t = u[b][d] * Z. The node's children c_1, c_2, ... (in node order)
+ * take the line [0, w(c_1)), [w(c_1), w(c_1) + w(c_2)), ...; the remaining
+ * tokens take the rest of [0, Z) in order of id. If t falls on a child the
+ * walk goes on there, otherwise the token it falls on is next_token. So every
+ * committed token has exactly the target's distribution softmax(x / T), and a
+ * child is accepted with its probability. At temperature 0 (or below, or NaN)
+ * the distribution is the point mass at the first largest logit, and the walk
+ * is ddtree_accept's with that target.
+ * target_logits [batch][B+1][V] (DDT_BF16 or DDT_F32, 16-byte aligned): the
+ *               target's row at each node (index 0 = root). -inf masks a
+ *               token; NaN counts as -inf, +inf as the largest finite value.
+ *               A row with every token masked gives next_token -1 and logp
+ *               -inf;
+ * temperature   [batch] float, NULL: 1;
+ * u             [batch][L+1] float in [0, 1) (clamped into it; NaN: 0): the
+ *               number of depth d decides at the d-th node of the path;
+ * accepted_nodes, accept_len, next_token as in ddtree_accept (num_nodes may be
+ *               NULL: B nodes); nodes whose token is outside [0, V) are never
+ *               accepted, nor is a second sibling with the same token;
+ * logp          [batch][L+1] float or NULL: log-probability of the i-th
+ *               accepted token, next_token's at accept_len, 0 behind it.
+ * Weights and sums are float64 with relative errors below 1e-13: a token
+ * differs from exact arithmetic only where t comes that near a border.
+ * Supported: B <= DDT_MAX_B, L <= DDT_MAX_L, V <= 2^22. Workspace:
+ * ddtree_accept_sampled_workspace_size bytes, no zero-fill needed.
+ */
+size_t ddtree_accept_sampled_workspace_size(int64_t batch, int32_t B, int32_t L, int64_t V,
+                                            int dtype);
+int ddtree_accept_sampled(const int32_t* tree_tokens, const int32_t* parents,
+                          const int32_t* num_nodes, const void* target_logits, int dtype,
+                          const float* temperature, const float* u, int64_t batch, int32_t B,
+                          int32_t L, int64_t V, int32_t* accepted_nodes, int32_t* accept_len,
+                          int32_t* next_token, float* logp, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * dspark_accept_sampled -- verification of a chain whose guesses were sampled
+ * from the drafter (DSpark explainer, speculative decoding basics). With
+ * p_i = softmax(target row i / T) and q_i = softmax(draft row i / T), guess
+ * x_i = tokens[b][i] (i < keep[b]) stands iff every earlier one does and
+ * u[b][i] * q_i(x_i) < p_i(x_i). At the first guess that falls, next_token is
+ * drawn from max(0, p_i - q_i) (normalised); if all keep[b] stand, from
+ * p_keep: with r those weights and R their sum, the first token in order of
+ * id whose running sum exceeds u[b][P] * R. Temperature 0 as in
+ * ddtree_accept_sampled (p and q are then the point masses at the first
+ * largest logits).
+ * tokens [batch][P] int32 (outside [0, V): falls); keep [batch] int32 (as
+ * written by dspark_budget), NULL: P, clamped into [0, P]; target_logits
+ * [batch][P+1][V]; draft_logits [batch][P][V], the rows the guesses were
+ * drawn from; u [batch][P+1] float; logp [batch][P+1] or NULL; values,
+ * precision, masks and the other arguments as in ddtree_accept_sampled.
+ * Supported: P <= DDT_MAX_L, V <= 2^22. Workspace:
+ * dspark_accept_sampled_workspace_size bytes, no zero-fill needed.
+ */
+size_t dspark_accept_sampled_workspace_size(int64_t batch, int32_t P, int64_t V, int dtype);
+int dspark_accept_sampled(const int32_t* tokens, const int32_t* keep, const void* target_logits,
+                          const void* draft_logits, int dtype, const float* temperature,
+                          const float* u, int64_t batch, int32_t P, int64_t V,
+                          int32_t* accept_len, int32_t* next_token, float* logp, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
 
 /*
  * ddtree_row_topk -- stage 1 alone over `rows` independent rows of length V

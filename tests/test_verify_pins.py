@@ -1,0 +1,281 @@
+"""Pins of the verification pass's oracle (append, attention, paged compaction,
+acceptance at a temperature) against facts fixed independently of it, and the
+library's refusals, which need no GPU."""
+
+import ctypes as C
+import os
+
+import numpy as np
+import pytest
+
+from draft_tree_construction_depth_amd import _lib
+from oracle import kv as OK
+from oracle import oracle as OR
+from oracle import verify as O
+
+
+# ---- append -------------------------------------------------------------------
+def test_rotation_keeps_relative_angles():
+    """q at position m times k at position n depends on m - n alone."""
+    rng = np.random.default_rng(0)
+    dh = 16
+    angle = rng.uniform(0, 3, dh // 2)
+    x, y = rng.standard_normal((1, dh)), rng.standard_normal((1, dh))
+    for inter in (False, True):
+        dots = [float(O.rotate(x, np.cos(m * angle), np.sin(m * angle), inter)[0] @
+                      O.rotate(y, np.cos(n * angle), np.sin(n * angle), inter)[0])
+                for m, n in ((3, 1), (9, 7), (2, 0))]
+        assert np.allclose(dots, dots[0], rtol=1e-12)
+
+
+def test_rotation_by_a_right_angle():
+    x = np.arange(1.0, 7.0)[None]  # rot 4 of 6 elements
+    c, s = np.zeros(2), np.ones(2)
+    assert O.rotate(x, c, s, False)[0].tolist() == [-3, -4, 1, 2, 5, 6]
+    assert O.rotate(x, c, s, True)[0].tolist() == [-2, 1, -4, 3, 5, 6]
+
+
+def test_append_places_rows_by_number_and_turns_them_by_depth():
+    T, dh, ps = 4, 2, 4
+    k = np.arange(1.0, 1 + T * dh).reshape(1, T, 1, dh)
+    rope = np.stack([np.full(10, 1.0), np.zeros(10)], 1)  # the identity ...
+    rope[6] = (0.0, 1.0)                                  # ... but a right angle at position 6
+    kc, vc = np.zeros((3, 1, ps, dh)), np.zeros((3, 1, ps, dh))
+    table = np.array([[2, 0]])
+    # past 5: rows 5..8, the last without a page; node depths 1, 1, 2; two nodes kept
+    q, k2, v2 = O.append(k, k, k, kc, vc, [5], rope, False, table, np.array([[1, 1, 2]]), [2])
+    assert k2[0, 0].tolist() == [[0, 0], [1, 2], [-4, 3], [-6, 5]]  # rows 5, 6, 7 on page 0
+    assert v2[0, 0].tolist() == [[0, 0], [1, 2], [3, 4], [5, 6]]
+    assert not k2[1:].any() and not q[0, 3].any()
+
+
+# ---- attention ------------------------------------------------------------------
+def test_attention_in_closed_form():
+    """Equal keys: the mean of the values seen; one huge score: that row's value."""
+    rng = np.random.default_rng(1)
+    v = rng.standard_normal((1, 1, 8, 4))
+    k = np.ones((1, 1, 8, 4))
+    q = rng.standard_normal((1, 3, 1, 4))
+    out, lse, _, _ = O.attend(q, k, v, [5])
+    for i in range(3):
+        assert np.allclose(out[0, i, 0], v[0, 0, :6 + i].mean(0))
+        assert np.allclose(lse[0, i, 0], q[0, i, 0].sum() / 2 + np.log(6 + i))
+    k[0, 0, 2] = 50 * q[0, 0, 0]
+    assert np.allclose(O.attend(q, k, v, [5])[0][0, 0, 0], v[0, 0, 2], atol=1e-6)
+
+
+def test_attention_mask_rows_and_padding():
+    """Under a tree's mask a node sees its path only; rows past the node count and
+    requests taken out see nothing; garbage in unseen rows does not matter."""
+    rng = np.random.default_rng(2)
+    par = np.array([[0, 0, 1]], np.int32)  # nodes 1, 2 under the root, 3 under 1
+    mask = OR.mask(par, np.array([3], np.int32), 3).view(np.int64)
+    q = rng.standard_normal((1, 4, 2, 4))
+    k, v = rng.standard_normal((1, 1, 9, 4)), rng.standard_normal((1, 1, 9, 4))
+    out, _, _, _ = O.attend(q, k, v, [4], mask=mask)
+    for i, path in enumerate([[0], [0, 1], [0, 2], [0, 1, 3]]):
+        rows = [0, 1, 2, 3] + [4 + j for j in path]
+        x = k[0, 0, rows] @ q[0, i, 1] / 2
+        a = np.exp(x) / np.exp(x).sum()
+        assert np.allclose(out[0, i, 1], a @ v[0, 0, rows])
+    k2, v2 = k.copy(), v.copy()
+    k2[0, 0, 7:], v2[0, 0, 7:] = np.nan, np.inf
+    o2, l2, _, _ = O.attend(q, k2, v2, [4], num_nodes=[2], mask=mask)
+    assert np.array_equal(o2[0, :3], out[0, :3]) and not o2[0, 3].any() and l2[0, 3, 0] == -np.inf
+    assert not O.attend(q, k, v, [-1])[0].any()
+
+
+def test_paged_attention_equals_contiguous():
+    rng = np.random.default_rng(3)
+    k, v = rng.standard_normal((2, 2, 12, 4)), rng.standard_normal((2, 2, 12, 4))
+    q = rng.standard_normal((2, 3, 4, 4))
+    table = np.array([[5, 1, 3], [0, 4, 2]])
+    kp, vp = np.zeros((6, 2, 4, 4)), np.zeros((6, 2, 4, 4))
+    for b in range(2):
+        for c in range(3):
+            kp[table[b, c]], vp[table[b, c]] = k[b, :, 4 * c:4 * c + 4], v[b, :, 4 * c:4 * c + 4]
+    a = O.attend(q, k, v, [9, 2])
+    p = O.attend(q, kp, vp, [9, 2], table)
+    assert all(np.array_equal(x, y) for x, y in zip(a, p))
+
+
+# ---- compaction -----------------------------------------------------------------
+def test_paged_compaction_equals_contiguous():
+    rng = np.random.default_rng(4)
+    k = rng.integers(0, 999, (2, 3, 2, 32, 4))
+    past = np.array([3, 0, 12], np.int32)
+    acc, n = np.array([[2, 5, -1], [1, 2, 9], [-1, -1, -1]], np.int32), np.array([2, 3, 0], np.int32)
+    k2, v2, nl = OK.compact(k, k + 1, past, acc, n)
+    table = rng.permutation(12).reshape(3, 4)
+    pool = np.zeros((2, 12, 2, 8, 4), k.dtype)
+    for b in range(3):
+        for c in range(4):
+            pool[:, table[b, c]] = k[:, b, :, 8 * c:8 * c + 8]
+    p2, w2, pl = O.compact_paged(pool, pool + 1, table, past, acc, n)
+    for b in range(3):
+        for c in range(4):
+            assert np.array_equal(p2[:, table[b, c]], k2[:, b, :, 8 * c:8 * c + 8])
+            assert np.array_equal(w2[:, table[b, c]], v2[:, b, :, 8 * c:8 * c + 8])
+    assert np.array_equal(nl, pl)
+
+
+# ---- acceptance -----------------------------------------------------------------
+def test_tree_line_gives_the_target_distribution():
+    """Over evenly spread numbers every first token comes out N p(v) times, whatever the tree."""
+    rng = np.random.default_rng(5)
+    V, N = 11, 4400
+    x = rng.standard_normal(V) * 2
+    p = np.exp(x / 0.7) / np.exp(x / 0.7).sum()
+    tok, par = np.array([[3, 7, 0, 5]]), np.array([[0, 0, 0, 1]])
+    logits = np.broadcast_to(x, (1, 5, V))
+    count = np.zeros(V)
+    for i in range(N):
+        u = np.array([[(i + 0.5) / N, 0.5, 0.5]])
+        path, n, last, _ = O.accept_tree(tok, par, None, logits, [0.7], u)
+        count[tok[0, path[0, 0] - 1] if n[0] else last[0]] += 1
+    assert np.abs(count - N * p).max() <= 1.0
+
+
+def test_chain_gives_the_target_distribution():
+    """q-sampled guesses and evenly spread numbers: each outcome's share is p(v).
+
+    P(v) = sum_x q(x) [share of u that keeps x] [x = v] + the share that falls times r(v) / R."""
+    rng = np.random.default_rng(6)
+    V, N = 7, 1000
+    x, y = rng.standard_normal(V), rng.standard_normal(V)
+    p, q = np.exp(x) / np.exp(x).sum(), np.exp(y) / np.exp(y).sum()
+    u = (np.arange(N) + 0.5) / N
+    share = np.zeros(V)
+    for guess in range(V):
+        n, _, _ = O.accept_chain(np.full((N, 1), guess), None, np.broadcast_to(x, (N, 2, V)),
+                                 np.broadcast_to(y, (N, 1, V)), None, np.stack([u, u * 0], 1))
+        kept = n.mean()
+        share[guess] += q[guess] * kept
+        if kept < 1:
+            fall = np.full((N, 1), 1.0 - 1e-9)  # a number that falls whenever any does
+            n, last, _ = O.accept_chain(np.full((N, 1), guess), None, np.broadcast_to(x, (N, 2, V)),
+                                        np.broadcast_to(y, (N, 1, V)), None,
+                                        np.concatenate([fall, u[:, None]], 1))
+            assert (n == 0).all()
+            share += q[guess] * (1 - kept) * np.bincount(last, minlength=V) / N
+    # each of the two shares is exact to one step of 1/N per guess
+    assert np.abs(share - p).max() <= 2.0 / N
+
+
+def test_temperature_zero_is_the_greedy_walk():
+    rng = np.random.default_rng(7)
+    B, V, L, batch = 12, 9, 4, 20
+    par = np.zeros((batch, B), np.int32)
+    tok = np.zeros((batch, B), np.int32)
+    for b in range(batch):
+        used = {}
+        for j in range(B):
+            par[b, j] = rng.integers(0, j + 1)
+            free = sorted(set(range(V)) - used.setdefault(par[b, j], set()))
+            tok[b, j] = rng.choice(free)
+            used[par[b, j]].add(tok[b, j])
+    logits = rng.integers(-3, 4, (batch, B + 1, V)).astype(float)  # ties
+    nn = rng.integers(1, B + 1, batch).astype(np.int32)
+    path, n, last, logp = O.accept_tree(tok, par, nn, logits, np.zeros(batch), rng.random((batch, L + 1)))
+    a, m, t = OR.accept(tok, par, nn, logits.argmax(2).astype(np.int32), L)
+    assert np.array_equal(path, a) and np.array_equal(n, m) and np.array_equal(last, t)
+    assert n.max() > 1 and not logp.any()
+
+
+def test_masked_rows_and_odd_numbers():
+    inf, nan = np.inf, np.nan
+    assert O.weights(np.array([-inf, 0.0, nan, -inf]), 1.0).tolist() == [0, 1, 0, 0]
+    assert O.weights(np.array([1.0, inf, inf]), 1.0).tolist() == [0, 1, 1]
+    assert not O.weights(np.full(4, -inf), 0.0).any()
+    assert [O.number(u) for u in (-1.0, nan, 0.25)] == [0, 0, 0.25] and O.number(1.0) < 1
+    tok = par = np.zeros((1, 1), np.int64)
+    got = O.accept_tree(tok, par, None, np.full((1, 2, 3), -inf), None, np.array([[0.3, 0.3]]))
+    assert got[1][0] == 0 and got[2][0] == -1 and got[3][0, 0] == -inf
+
+
+# ---- refusals: rejected on the host before anything is launched ------------------
+FAKE, ODD = C.c_void_p(0x100000), C.c_void_p(0x100008)  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(_lib.LIB_PATH):
+        from draft_tree_construction_depth_amd import _build
+        _build.build_library()
+    return _lib.lib()
+
+
+def test_append_refusals(L):
+    def call(q=FAKE, k=FAKE, dtype=0, batch=2, T=9, Hq=8, Hkv=2, dh=128, qs=1024, ks=256, vs=256, rope=FAKE,
+             rl=100, rot=128, inter=0, past=FAKE, table=FAKE, width=4, pages=16, ps=16, kc=FAKE, qo=FAKE):
+        return L.ddtree_append_kv(q, k, FAKE, dtype, batch, T, Hq, Hkv, dh, qs, ks, vs, rope, rl, rot, inter, past,
+                                  None, None, table, width, pages, ps, kc, FAKE, qo, None)
+    for bad in (dict(k=None), dict(q=None), dict(qo=None), dict(kc=None), dict(past=None), dict(rope=None),
+                dict(dtype=1), dict(dtype=3), dict(T=0), dict(Hkv=0), dict(Hq=7), dict(dh=0), dict(rot=-16),
+                dict(rot=256), dict(rl=-1), dict(inter=2), dict(qs=1016), dict(ks=128), dict(vs=128), dict(k=ODD),
+                dict(kc=ODD), dict(qo=ODD), dict(rope=ODD), dict(pages=0), dict(ps=0), dict(width=0),
+                dict(table=None), dict(batch=-1)):
+        assert call(**bad) == -1, bad
+    for bad in (dict(T=514), dict(dh=516, qs=4128, ks=1032, vs=1032), dict(dh=1024, qs=8192, ks=2048, vs=2048),
+                dict(rot=120), dict(ps=24), dict(qs=1028), dict(ks=260), dict(batch=1 << 31)):
+        assert call(**bad) == -2, bad
+    assert call(batch=0) == 0
+
+
+def test_attention_refusals(L):
+    size = L.ddtree_attention_workspace_size
+    assert size(2, 9, 8, 2, 128, 4, 16) > 0
+    assert size(0, 9, 8, 2, 128, 4, 16) == size(2, 9, 8, 2, 96, 4, 16) == size(2, 514, 8, 2, 128, 4, 16) == 0
+
+    def call(q=FAKE, dtype=0, batch=2, T=9, Hq=8, Hkv=2, dh=128, kc=FAKE, table=FAKE, width=4, pages=16, ps=16,
+             past=FAKE, scale=0.1, out=FAKE, ws=FAKE, n=1 << 40):
+        return L.ddtree_attention(q, dtype, batch, T, Hq, Hkv, dh, kc, FAKE, table, width, pages, ps, past, None,
+                                  None, scale, out, None, ws, n, None)
+    for bad in (dict(q=None), dict(kc=None), dict(past=None), dict(out=None), dict(ws=None), dict(q=ODD),
+                dict(kc=ODD), dict(out=ODD), dict(ws=ODD), dict(dtype=1), dict(T=0), dict(Hq=0), dict(Hq=7),
+                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
+                dict(table=None), dict(pages=0), dict(width=0), dict(batch=-1)):
+        assert call(**bad) == -1, bad
+    for bad in (dict(T=514), dict(dh=96), dict(dh=512), dict(ps=24), dict(batch=1 << 31)):
+        assert call(**bad) == -2, bad
+    assert call(n=0) == -3
+    assert call(batch=0) == 0
+
+
+def test_paged_compaction_refusals(L):
+    def call(k=FAKE, layers=2, pages=16, heads=4, ps=16, row=256, table=FAKE, width=4, batch=3, past=FAKE, depth=15):
+        return L.ddtree_compact_kv_paged(k, FAKE, layers, pages, heads, ps, row, table, width, batch, past, FAKE,
+                                         FAKE, depth, FAKE, None)
+    for bad in (dict(k=None), dict(k=ODD), dict(table=None), dict(past=None), dict(layers=-1), dict(pages=0),
+                dict(ps=0), dict(width=0), dict(row=0), dict(depth=0)):
+        assert call(**bad) == -1, bad
+    for bad in (dict(row=100), dict(row=2048), dict(depth=33), dict(ps=24), dict(layers=1 << 40)):
+        assert call(**bad) == -2, bad
+    assert call(batch=0) == call(layers=0) == call(heads=0) == 0
+
+
+def test_acceptance_refusals(L):
+    size = L.ddtree_accept_sampled_workspace_size
+    assert size(4, 64, 15, 151936, 0) > 0 and size(4, 513, 15, 151936, 0) == 0
+    assert size(4, 64, 33, 151936, 0) == size(4, 64, 15, (1 << 22) + 1, 0) == size(4, 64, 15, 9, 2) == 0
+
+    def tree(tok=FAKE, x=FAKE, dtype=0, u=FAKE, batch=2, B=64, depth=15, V=1000, path=FAKE, ws=FAKE, n=1 << 40):
+        return L.ddtree_accept_sampled(tok, FAKE, None, x, dtype, None, u, batch, B, depth, V, path, FAKE, FAKE,
+                                       None, ws, n, None)
+    for bad in (dict(tok=None), dict(x=None), dict(x=ODD), dict(u=None), dict(path=None), dict(ws=None),
+                dict(dtype=2), dict(B=0), dict(depth=0), dict(V=0), dict(batch=-1)):
+        assert tree(**bad) == -1, bad
+    for bad in (dict(B=513), dict(depth=33), dict(V=(1 << 22) + 1), dict(batch=1 << 40)):
+        assert tree(**bad) == -2, bad
+    assert tree(n=8) == -3 and tree(batch=0) == 0
+    assert L.dspark_accept_sampled_workspace_size(4, 16, 151936, 0) > 0
+    assert L.dspark_accept_sampled_workspace_size(4, 33, 151936, 0) == 0
+
+    def chain(tok=FAKE, x=FAKE, y=FAKE, dtype=0, u=FAKE, batch=2, P=7, V=1000, ws=FAKE, n=1 << 40):
+        return L.dspark_accept_sampled(tok, None, x, y, dtype, None, u, batch, P, V, FAKE, FAKE, None, ws, n, None)
+    for bad in (dict(tok=None), dict(x=None), dict(y=None), dict(y=ODD), dict(u=None), dict(ws=None), dict(dtype=2),
+                dict(P=0), dict(V=0), dict(batch=-1)):
+        assert chain(**bad) == -1, bad
+    for bad in (dict(P=33), dict(V=(1 << 22) + 1), dict(batch=1 << 40)):
+        assert chain(**bad) == -2, bad
+    assert chain(n=8) == -3 and chain(batch=0) == 0

@@ -479,13 +479,74 @@ void launch_append(const ddt::AppendParams& ap, int64_t blocks, int interleaved,
                        dim3(ddt::kApThreads), 0, st, ap);
 }
 
+// ---- attention: waves along the queries, workgroups, workspace -------------------
+struct AttnPlan {
+  int QW, MT;
+  int64_t target, least, grid, merge;  // workgroups of the launches; merge 0: nothing to merge
+  size_t part, ml, end;
+};
+
+// Waves side by side: as many as the query rows of a key/value head fill.
+int attn_waves(int32_t T, int32_t G, int32_t head_dim) {
+  const int64_t M = (int64_t)T * G;
+  const int qw = M <= 32 ? 1 : (M <= 64 ? 2 : 4);
+  return head_dim == 256 && qw == 1 ? 2 : qw;  // four groups' tiles would fill the LDS
+}
+
+AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
+                        int32_t head_dim, int64_t cap) {
+  AttnPlan pl;
+  const int G = q_heads / kv_heads;
+  pl.QW = attn_waves(T, G, head_dim);
+  pl.MT = (int)(((int64_t)T * G + 32 * pl.QW - 1) / (32 * pl.QW));
+  const int64_t units = (int64_t)kv_heads * pl.MT;
+  const int rows = pl.QW == 4 ? (head_dim <= 128 ? 64 : 32) : 32 * (4 / pl.QW);  // AttnTile::TR
+  pl.target = 512;  // two workgroups on each of 256 CUs
+  pl.least = 2;
+  pl.grid = (pl.target + batch * units + 7) & ~(int64_t)7;
+  const int64_t steps = (cap + rows - 1) / rows;
+  // split requests take at most twice the target's pieces (each has two or
+  // more, none of which but the last is shorter than the common size)
+  int64_t slots = 2 * pl.target;
+  const int64_t most = batch * units * ((steps + pl.least - 1) / pl.least);
+  if (steps <= pl.least) slots = 0;
+  else if (most < slots) slots = most;
+  pl.merge = slots > 0 ? batch * units * pl.QW : 0;
+  size_t o = align_up((size_t)batch * sizeof(ddt::AttnPlace));
+  pl.part = o;
+  o = align_up(o + (size_t)slots * pl.QW * 32 * head_dim * sizeof(float));
+  pl.ml = o;
+  o = align_up(o + (size_t)slots * pl.QW * 64 * 2 * sizeof(float));
+  pl.end = o;
+  return pl;
+}
+
+template <typename H, int DH, int QW>
+int launch_attn_tile(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
+  hipLaunchKernelGGL((ddt::attn_kernel<H, DH, QW>), dim3((unsigned)pl.grid), dim3(ddt::kAtThreads),
+                     0, st, ap);
+  if (hipGetLastError() != hipSuccess) return DDT_EHIP;
+  if (pl.merge == 0) return DDT_OK;
+  hipLaunchKernelGGL((ddt::attn_merge_kernel<H, DH, QW>), dim3((unsigned)pl.merge), dim3(DH * 2),
+                     0, st, ap);
+  return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+}
+
+template <typename H, int DH>
+int launch_attn_waves(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
+  if constexpr (DH < 256) {
+    if (pl.QW == 1) return launch_attn_tile<H, DH, 1>(ap, pl, st);
+  }
+  if (pl.QW == 2) return launch_attn_tile<H, DH, 2>(ap, pl, st);
+  return launch_attn_tile<H, DH, 4>(ap, pl, st);
+}
+
 template <typename H>
-void launch_attn(const ddt::AttnParams& ap, int head_dim, hipStream_t st) {
-  const dim3 grid((unsigned)(ap.batch * ap.T * ap.q_heads)), block(ddt::kWave);
+int launch_attn(const ddt::AttnParams& ap, const AttnPlan& pl, int head_dim, hipStream_t st) {
   switch (head_dim) {
-    case 64: hipLaunchKernelGGL((ddt::attn_row_kernel<H, 64>), grid, block, 0, st, ap); break;
-    case 128: hipLaunchKernelGGL((ddt::attn_row_kernel<H, 128>), grid, block, 0, st, ap); break;
-    default: hipLaunchKernelGGL((ddt::attn_row_kernel<H, 256>), grid, block, 0, st, ap); break;
+    case 64: return launch_attn_waves<H, 64>(ap, pl, st);
+    case 128: return launch_attn_waves<H, 128>(ap, pl, st);
+    default: return launch_attn_waves<H, 256>(ap, pl, st);
   }
 }
 
@@ -496,7 +557,8 @@ int attn_check(int dtype, int64_t batch, int32_t T, int32_t q_heads, int32_t kv_
   if (q_heads % kv_heads != 0) return DDT_EINVAL;
   if (T > DDT_MAX_B + 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return DDT_ENOTSUP;
-  if (batch > 0x7FFFFFFFLL || batch * T > 0x7FFFFFFFLL / q_heads) return DDT_ENOTSUP;
+  // query rows (and with them the launches' workgroups) are counted in 31 bits
+  if (batch > 0x1FFFFFFFLL || batch * T > 0x1FFFFFFFLL / q_heads) return DDT_ENOTSUP;
   return DDT_OK;
 }
 
@@ -913,7 +975,10 @@ size_t ddtree_attention_workspace_size(int64_t batch, int32_t T, int32_t q_heads
   if (batch <= 0 || pages_per_request <= 0 || page_size <= 0 ||
       attn_check(DDT_BF16, batch, T, q_heads, kv_heads, head_dim) != DDT_OK)
     return 0;
-  return kAlign;
+  const int64_t cap = pages_per_request > 0x7FFFFFFFLL / page_size
+                          ? 0x7FFFFFFFLL
+                          : pages_per_request * page_size;
+  return attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap).end;
 }
 
 int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
@@ -934,9 +999,8 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   const int chk2 = paged_rows(page_table, table_width, batch, pages, page_size, ap.rows);
   if (chk2 == DDT_EINVAL) return chk2;
   if (chk != DDT_OK || chk2 != DDT_OK) return DDT_ENOTSUP;
-  if (workspace_bytes < ddtree_attention_workspace_size(batch, T, q_heads, kv_heads, head_dim,
-                                                        ap.rows.width, page_size))
-    return DDT_EWORKSPACE;
+  const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap);
+  if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
   ap.q = q;
   ap.k_cache = k_cache;
   ap.v_cache = v_cache;
@@ -944,6 +1008,10 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   ap.T = T;
   ap.q_heads = q_heads;
   ap.kv_heads = kv_heads;
+  ap.G = q_heads / kv_heads;
+  ap.MT = pl.MT;
+  ap.target = (int32_t)pl.target;
+  ap.least = (int32_t)pl.least;
   ap.past_len = past_len;
   ap.num_nodes = num_nodes;
   ap.mask = mask;
@@ -951,11 +1019,11 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   ap.scale2 = scale * ddt::kLog2e;
   ap.out = out;
   ap.lse = lse;
-  if (dtype == DDT_BF16)
-    launch_attn<__bf16>(ap, head_dim, stream);
-  else
-    launch_attn<_Float16>(ap, head_dim, stream);
-  return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
+  ap.place = (ddt::AttnPlace*)workspace;
+  ap.part = (float*)((char*)workspace + pl.part);
+  ap.part_ml = (float*)((char*)workspace + pl.ml);
+  return dtype == DDT_BF16 ? launch_attn<__bf16>(ap, pl, head_dim, stream)
+                           : launch_attn<_Float16>(ap, pl, head_dim, stream);
 }
 
 size_t ddtree_accept_sampled_workspace_size(int64_t batch, int32_t B, int32_t L, int64_t V,

@@ -9,6 +9,7 @@ fallback: if the library is missing, loading it raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -478,69 +479,109 @@ def sparkling_beam(logits: torch.Tensor, W1: torch.Tensor, W2t: torch.Tensor, wi
 
 
 # ---- the verification pass --------------------------------------------------
+# Calls of a few microseconds on the device: the checks below are one test per
+# tensor when it is right, and say what is wrong only when it is not.
 _HALF = (torch.bfloat16, torch.float16)
 _F32 = (torch.float32,)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _half_code(t: torch.Tensor) -> int:
-    return DDT_BF16 if t.dtype == torch.bfloat16 else DDT_F16
+def _half_code(dtype) -> int:
+    return DDT_BF16 if dtype == torch.bfloat16 else DDT_F16
 
 
-def _on(dev, **tensors):
-    """Check that every tensor given lies on device dev."""
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _dev_arg(t, name, dtype, shape, dev):
+    """Device pointer of a contiguous tensor of this dtype and shape on device dev."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and \
+            t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    _arg(t, name, (dtype,), shape)
+    raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
-def _scratch(kind: str, size: int, device) -> torch.Tensor:
-    """Workspace for one call: the stream's own buffer of this kind (grown as
-    needed), or, under graph capture, one of the graph's, so that no two graphs
-    and no eager call share it."""
+def _maybe_arg(t, name, dtype, shape, dev):
+    return None if t is None else _dev_arg(t, name, dtype, shape, dev)
+
+
+def _ws_arg(kind, size, ws, dev):
+    """Pointer and size of the workspace of one call: the caller's, or the
+    stream's own of this kind (grown as needed), or, under graph capture, one of
+    the graph's, so that no two graphs and no eager call share it. The second
+    return value keeps it alive until the call is enqueued."""
+    if ws is not None:
+        if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+            raise ValueError("ws must be a contiguous device tensor")
+        if ws.device != dev:
+            raise ValueError(f"ws must be on {dev}, got {ws.device}")
+        return ws.data_ptr(), ws, ws.numel() * ws.element_size()
     if torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(size, 1), dtype=torch.uint8, device=device)
-    return workspace(kind, size, device, ())
+        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+    else:
+        key = (kind, dev.index, _raw_stream(dev.index))
+        ws = _workspaces.get(key)
+        if ws is None or ws.numel() < size:
+            ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+            _workspaces[key] = ws
+    return ws.data_ptr(), ws, ws.numel()
 
 
-def _block_rows(t, name, dtype, batch, T, dh):
-    """Check [batch, T, heads, head_dim] rows at one distance; (tensor's heads, that distance)."""
+class _OnDevice:
+    """Makes a device the current one if it is not: launches go to the current device."""
+
+    def __init__(self, dev):
+        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _block_rows(t, name, dtype, batch, T, dh, dev):
+    """Check [batch, T, heads, head_dim] rows at one distance; (pointer, heads, that distance)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[0] != batch or t.shape[1] != T or t.shape[3] != dh:
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor (on the caches' device)")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [batch, T, heads, head_dim]")
+    b, n, heads, d = t.shape
+    if b != batch or n != T or d != dh:
         raise ValueError(f"{name} must have shape ({batch}, {T}, heads, {dh}), got {tuple(t.shape)}")
-    heads = t.shape[2]
-    step = t.stride(1) if T > 1 else (t.stride(0) if batch > 1 else heads * dh)
-    if (t.stride(3) != 1 and dh > 1) or (heads > 1 and t.stride(2) != dh) or \
-            (batch > 1 and t.stride(0) != T * step):
+    s0, s1, s2, s3 = t.stride()
+    step = s1 if T > 1 else (s0 if batch > 1 else heads * dh)
+    if (s3 != 1 and dh > 1) or (heads > 1 and s2 != dh) or (batch > 1 and s0 != T * step):
         raise ValueError(f"{name} must hold its heads side by side and its rows at one distance")
-    return heads, step
+    return t.data_ptr(), heads, step
 
 
 def _paged_cache(k_cache, v_cache, page_table, batch, dims):
     """Check a cache [(layers,) pages, kv_heads, page_size, head_dim] and its page
-    table [batch, width]; (pages, kv_heads, page_size, head_dim, width)."""
+    table [batch, width]; (pointers, shape, width)."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != dims:
         raise ValueError(f"k_cache must be a {dims}-d tensor "
                          f"[{'layers, ' if dims == 5 else ''}pages, kv_heads, page_size, head_dim]")
-    _arg(k_cache, "k_cache", (k_cache.dtype,))
-    _arg(v_cache, "v_cache", (k_cache.dtype,), tuple(k_cache.shape))
-    _on(k_cache.device, v_cache=v_cache, page_table=page_table)
-    pages, heads, page_size, dh = k_cache.shape[-4:]
-    width = 1
-    if page_table is not None:
-        _arg(page_table, "page_table", _I32)
-        if page_table.dim() != 2 or page_table.shape[0] != batch:
-            raise ValueError(f"page_table must have shape ({batch}, width), got "
-                             f"{tuple(page_table.shape)}")
-        width = page_table.shape[1]
-    elif pages != batch:
-        raise ValueError(f"without a page table the cache must hold one page per request "
-                         f"({batch}), got {pages}")
-    return pages, heads, page_size, dh, width
+    shape, dev = k_cache.shape, k_cache.device
+    k = _dev_arg(k_cache, "k_cache", k_cache.dtype, shape, dev)
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a device tensor")
+    v = _dev_arg(v_cache, "v_cache", k_cache.dtype, shape, dev)
+    if page_table is None:
+        if shape[-4] != batch:
+            raise ValueError(f"without a page table the cache must hold one page per request "
+                             f"({batch}), got {shape[-4]}")
+        return k, v, None, shape, 1
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or \
+            page_table.shape[0] != batch:
+        raise ValueError(f"page_table must be a tensor of shape ({batch}, width)")
+    width = page_table.shape[1]
+    return k, v, _dev_arg(page_table, "page_table", torch.int32, (batch, width), dev), shape, width
 
 
 def ddtree_append_kv(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -554,45 +595,48 @@ def ddtree_append_kv(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     depths [batch, T-1]; writes the caches and returns the rotated queries q_out (None for q None)."""
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be [batch, T, kv_heads, head_dim]")
-    if k.dtype not in _HALF:
-        raise TypeError(f"k must have dtype {' or '.join(map(str, _HALF))}, got {k.dtype}")
+    dt = k.dtype
+    if dt not in _HALF:
+        raise TypeError(f"k must have dtype {' or '.join(map(str, _HALF))}, got {dt}")
     batch, T, _, dh = k.shape
-    dev = k.device
-    kv_heads, ks = _block_rows(k, "k", k.dtype, batch, T, dh)
-    hv, vs = _block_rows(v, "v", k.dtype, batch, T, dh)
-    q_heads, qs = (0, 0) if q is None else _block_rows(q, "q", k.dtype, batch, T, dh)
-    pages, hc, page_size, dc, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
-    if k_cache.dtype != k.dtype:
-        raise TypeError(f"k_cache must have dtype {k.dtype}, got {k_cache.dtype}")
+    kc, vc, table, shape, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
+    dev = k_cache.device
+    if k_cache.dtype != dt:
+        raise TypeError(f"k_cache must have dtype {dt}, got {k_cache.dtype}")
+    kp, kv_heads, ks = _block_rows(k, "k", dt, batch, T, dh, dev)
+    vp, hv, vs = _block_rows(v, "v", dt, batch, T, dh, dev)
+    pages, hc, page_size, dc = shape
     if hv != kv_heads or hc != kv_heads or dc != dh:
         raise ValueError("k, v and the caches must have the same heads and head_dim")
-    _arg(past_len, "past_len", _I32, (batch,))
-    rot = rope_len = 0
-    if rope is not None:
-        _arg(rope, "rope", _F32)
-        if rope.dim() != 2:
-            raise ValueError("rope must be [positions, rope_dim]")
-        rope_len, rot = rope.shape
-    if depths is not None:
-        _arg(depths, "depths", _I32, (batch, T - 1))
-    if num_nodes is not None:
-        _arg(num_nodes, "num_nodes", _I32, (batch,))
+    qp, q_heads, qs, qo = None, 0, 0, None
     if q is None:
         q_out = None
-    elif q_out is None:
-        q_out = torch.zeros((batch, T, q_heads, dh), dtype=q.dtype, device=dev)
     else:
-        _arg(q_out, "q_out", (q.dtype,), (batch, T, q_heads, dh))
-    _on(dev, q=q, v=v, k_cache=k_cache, past_len=past_len, rope=rope, depths=depths,
-        num_nodes=num_nodes, q_out=q_out)
-    with torch.cuda.device(dev):
-        rc = lib().ddtree_append_kv(_ptr(q), _ptr(k), _ptr(v), _half_code(k), batch, T, q_heads,
-                                    kv_heads, dh, qs, ks, vs, _ptr(rope), rope_len, rot,
-                                    int(bool(interleaved)), _ptr(past_len), _ptr(depths),
-                                    _ptr(num_nodes), _ptr(page_table), width, pages, page_size,
-                                    _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _stream(dev))
-    _check("ddtree_append_kv", rc)
+        qp, q_heads, qs = _block_rows(q, "q", dt, batch, T, dh, dev)
+        if q_out is None:
+            q_out = torch.zeros((batch, T, q_heads, dh), dtype=dt, device=dev)
+        qo = _dev_arg(q_out, "q_out", dt, (batch, T, q_heads, dh), dev)
+    rp, rope_len, rot = None, 0, 0
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+            raise ValueError("rope must be [positions, rope_dim]")
+        rope_len, rot = rope.shape
+        rp = _dev_arg(rope, "rope", torch.float32, (rope_len, rot), dev)
+    args = (qp, kp, vp, _half_code(dt), batch, T, q_heads, kv_heads, dh, qs, ks, vs, rp, rope_len,
+            rot, 1 if interleaved else 0, _dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+            _maybe_arg(depths, "depths", torch.int32, (batch, T - 1), dev),
+            _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev), table, width, pages,
+            page_size, kc, vc, qo)
+    with _OnDevice(dev):
+        rc = lib().ddtree_append_kv(*args, _raw_stream(dev.index))
+    if rc:
+        _check("ddtree_append_kv", rc)
     return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_ws(*sizes) -> int:
+    return lib().ddtree_attention_workspace_size(*sizes)
 
 
 def ddtree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -603,43 +647,39 @@ def ddtree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     """Verified block's attention: q [batch, T, q_heads, dh] (bf16/f16) over one layer's caches
     [pages, kv_heads, page_size, dh] under the ancestor mask [batch, T, ceil(T/64)] (int64, as
     ddtree_mask's; None: a chain); scale defaults to dh ** -0.5. Returns out (and lse)."""
-    _arg(q, "q", _HALF)
-    if q.dim() != 4:
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [batch, T, q_heads, head_dim]")
+    dt = q.dtype
+    if dt not in _HALF:
+        raise TypeError(f"q must have dtype {' or '.join(map(str, _HALF))}, got {dt}")
     batch, T, q_heads, dh = q.shape
-    dev = q.device
-    pages, kv_heads, page_size, dc, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
-    if k_cache.dtype != q.dtype:
-        raise TypeError(f"k_cache must have dtype {q.dtype}, got {k_cache.dtype}")
+    kc, vc, table, shape, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
+    dev = k_cache.device
+    qp = _dev_arg(q, "q", dt, q.shape, dev)
+    if k_cache.dtype != dt:
+        raise TypeError(f"k_cache must have dtype {dt}, got {k_cache.dtype}")
+    pages, kv_heads, page_size, dc = shape
     if dc != dh:
         raise ValueError(f"the caches must have head_dim {dh}, got {dc}")
-    _arg(past_len, "past_len", _I32, (batch,))
-    if num_nodes is not None:
-        _arg(num_nodes, "num_nodes", _I32, (batch,))
-    if mask is not None:
-        _arg(mask, "mask", (torch.int64,), (batch, T, (T + 63) // 64))
     if out is None:
-        out = dict(out=torch.empty_like(q))
+        out = {"out": torch.empty_like(q)}
         if with_lse:
             out["lse"] = torch.empty((batch, T, q_heads), dtype=torch.float32, device=dev)
-    _arg(out["out"], "out", (q.dtype,), tuple(q.shape))
-    lse = out.get("lse")
-    if lse is not None:
-        _arg(lse, "lse", _F32, (batch, T, q_heads))
-    _on(dev, k_cache=k_cache, past_len=past_len, num_nodes=num_nodes, mask=mask, out=out["out"],
-        lse=lse, ws=ws)
-    with torch.cuda.device(dev):
-        if ws is None:
-            size = lib().ddtree_attention_workspace_size(batch, T, q_heads, kv_heads, dh, width,
-                                                         page_size)
-            ws = _scratch("attention", size, dev)
-        rc = lib().ddtree_attention(_ptr(q), _half_code(q), batch, T, q_heads, kv_heads, dh,
-                                    _ptr(k_cache), _ptr(v_cache), _ptr(page_table), width, pages,
-                                    page_size, _ptr(past_len), _ptr(num_nodes), _ptr(mask),
-                                    dh ** -0.5 if scale is None else float(scale),
-                                    _ptr(out["out"]), _ptr(lse), _ptr(ws), ws.numel(),
-                                    _stream(dev))
-    _check("ddtree_attention", rc)
+    args = (_dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+            _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev),
+            _maybe_arg(mask, "mask", torch.int64, (batch, T, (T + 63) // 64), dev),
+            dh ** -0.5 if scale is None else float(scale),
+            _dev_arg(out["out"], "out", dt, q.shape, dev),
+            _maybe_arg(out.get("lse"), "lse", torch.float32, (batch, T, q_heads), dev))
+    with _OnDevice(dev):
+        size = 0 if ws is not None else _attention_ws(batch, T, q_heads, kv_heads, dh, width,
+                                                      page_size)
+        wp, ws, size = _ws_arg("attention", size, ws, dev)
+        rc = lib().ddtree_attention(qp, _half_code(dt), batch, T, q_heads, kv_heads, dh, kc, vc,
+                                    table, width, pages, page_size, *args, wp, size,
+                                    _raw_stream(dev.index))
+    if rc:
+        _check("ddtree_attention", rc)
     return out
 
 
@@ -649,31 +689,47 @@ def ddtree_compact_kv_paged(k_cache: torch.Tensor, v_cache: torch.Tensor,
                             new_len: torch.Tensor | None = None) -> torch.Tensor:
     """In place: paged caches [layers, pages, heads, page_size, head_dim] keep the accepted
     path's rows (page_table [batch, width]); returns new_len [batch]."""
-    _arg(past_len, "past_len", _I32)
-    if past_len.dim() != 1:
+    if not isinstance(past_len, torch.Tensor) or past_len.dim() != 1:
         raise ValueError("past_len must be [batch]")
     batch = past_len.shape[0]
     if page_table is None:
         raise ValueError("page_table is required; ddtree_compact_kv takes contiguous caches")
-    pages, heads, page_size, dh, width = _paged_cache(k_cache, v_cache, page_table, batch, 5)
-    _arg(accepted_nodes, "accepted_nodes", _I32)
-    L = accepted_nodes.shape[-1]
-    _arg(accepted_nodes, "accepted_nodes", _I32, (batch, L))
-    _arg(accept_len, "accept_len", _I32, (batch,))
+    kc, vc, table, shape, width = _paged_cache(k_cache, v_cache, page_table, batch, 5)
     dev = k_cache.device
+    layers, pages, heads, page_size, dh = shape
+    if not isinstance(accepted_nodes, torch.Tensor) or accepted_nodes.dim() != 2:
+        raise ValueError("accepted_nodes must be [batch, L]")
+    L = accepted_nodes.shape[1]
     if new_len is None:
         new_len = torch.empty((batch,), dtype=torch.int32, device=dev)
-    _arg(new_len, "new_len", _I32, (batch,))
-    _on(dev, past_len=past_len, accepted_nodes=accepted_nodes, accept_len=accept_len,
-        new_len=new_len)
-    with torch.cuda.device(dev):
-        rc = lib().ddtree_compact_kv_paged(_ptr(k_cache), _ptr(v_cache), k_cache.shape[0], pages,
-                                           heads, page_size, dh * k_cache.element_size(),
-                                           _ptr(page_table), width, batch, _ptr(past_len),
-                                           _ptr(accepted_nodes), _ptr(accept_len), L,
-                                           _ptr(new_len), _stream(dev))
-    _check("ddtree_compact_kv_paged", rc)
+    args = (_dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+            _dev_arg(accepted_nodes, "accepted_nodes", torch.int32, (batch, L), dev),
+            _dev_arg(accept_len, "accept_len", torch.int32, (batch,), dev), L,
+            _dev_arg(new_len, "new_len", torch.int32, (batch,), dev))
+    with _OnDevice(dev):
+        rc = lib().ddtree_compact_kv_paged(kc, vc, layers, pages, heads, page_size,
+                                           dh * k_cache.element_size(), table, width, batch,
+                                           *args, _raw_stream(dev.index))
+    if rc:
+        _check("ddtree_compact_kv_paged", rc)
     return new_len
+
+
+@functools.lru_cache(maxsize=1024)
+def _accept_ws(*sizes) -> int:
+    return lib().ddtree_accept_sampled_workspace_size(*sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _chain_ws(*sizes) -> int:
+    return lib().dspark_accept_sampled_workspace_size(*sizes)
+
+
+def _rows_arg(t, name, batch):
+    """A [batch, n] tensor argument's n."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (batch is not None and t.shape[0] != batch):
+        raise ValueError(f"{name} must be [{'batch' if batch is None else batch}, n]")
+    return t.shape[1]
 
 
 def ddtree_accept_sampled(tree_tokens: torch.Tensor, parents: torch.Tensor,
@@ -683,53 +739,33 @@ def ddtree_accept_sampled(tree_tokens: torch.Tensor, parents: torch.Tensor,
     """Tree acceptance at a temperature: target_logits [batch, B+1, V] (bf16/f32), temperature
     [batch] (None: 1; 0: greedy), u [batch, L+1] uniforms -> accepted_nodes [batch, L],
     accept_len, next_token, logp [batch, L+1]."""
-    _arg(tree_tokens, "tree_tokens", _I32)
-    if tree_tokens.dim() != 2:
-        raise ValueError("tree_tokens must be [batch, B]")
-    batch, B = tree_tokens.shape
-    _arg(parents, "parents", _I32, (batch, B))
-    if num_nodes is not None:
-        _arg(num_nodes, "num_nodes", _I32, (batch,))
     _arg(target_logits, "target_logits", _LOGITS)
-    V = target_logits.shape[-1]
-    _arg(target_logits, "target_logits", _LOGITS, (batch, B + 1, V))
-    if temperature is not None:
-        _arg(temperature, "temperature", _F32, (batch,))
-    _arg(u, "u", _F32)
-    if u.dim() != 2 or u.shape[0] != batch:
-        raise ValueError(f"u must have shape ({batch}, L + 1), got {tuple(u.shape)}")
-    L = u.shape[1] - 1
-    dev = target_logits.device
-    dt = _dtype_code(target_logits)
+    B = _rows_arg(tree_tokens, "tree_tokens", None)
+    batch, V, dev = tree_tokens.shape[0], target_logits.shape[-1], target_logits.device
+    L = _rows_arg(u, "u", batch) - 1
+    dt = DDT_BF16 if target_logits.dtype == torch.bfloat16 else DDT_F32
     if out is None:
-        out = dict(accepted_nodes=torch.empty((batch, L), dtype=torch.int32, device=dev),
-                   accept_len=torch.empty((batch,), dtype=torch.int32, device=dev),
-                   next_token=torch.empty((batch,), dtype=torch.int32, device=dev),
+        i32 = torch.empty((max(L, 0) + 2, batch), dtype=torch.int32, device=dev)
+        out = dict(accepted_nodes=i32[2:].view(batch, max(L, 0)), accept_len=i32[0],
+                   next_token=i32[1],
                    logp=torch.empty((batch, L + 1), dtype=torch.float32, device=dev))
-    _accepted_out(out, dev, batch, L)
-    _arg(out["accepted_nodes"], "accepted_nodes", _I32, (batch, L))
-    _on(dev, tree_tokens=tree_tokens, parents=parents, num_nodes=num_nodes,
-        temperature=temperature, u=u, ws=ws, accepted_nodes=out["accepted_nodes"])
-    with torch.cuda.device(dev):
-        if ws is None:
-            size = lib().ddtree_accept_sampled_workspace_size(batch, B, L, V, dt)
-            ws = _scratch("accept_sampled", size, dev)
-        rc = lib().ddtree_accept_sampled(_ptr(tree_tokens), _ptr(parents), _ptr(num_nodes),
-                                         _ptr(target_logits), dt, _ptr(temperature), _ptr(u),
-                                         batch, B, L, V, _ptr(out["accepted_nodes"]),
-                                         _ptr(out["accept_len"]), _ptr(out["next_token"]),
-                                         _ptr(out.get("logp")), _ptr(ws), ws.numel(),
-                                         _stream(dev))
-    _check("ddtree_accept_sampled", rc)
+    args = (_dev_arg(tree_tokens, "tree_tokens", torch.int32, (batch, B), dev),
+            _dev_arg(parents, "parents", torch.int32, (batch, B), dev),
+            _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev),
+            _dev_arg(target_logits, "target_logits", target_logits.dtype, (batch, B + 1, V), dev),
+            dt, _maybe_arg(temperature, "temperature", torch.float32, (batch,), dev),
+            _dev_arg(u, "u", torch.float32, (batch, L + 1), dev), batch, B, L, V,
+            _dev_arg(out["accepted_nodes"], "accepted_nodes", torch.int32, (batch, L), dev),
+            _dev_arg(out["accept_len"], "accept_len", torch.int32, (batch,), dev),
+            _dev_arg(out["next_token"], "next_token", torch.int32, (batch,), dev),
+            _maybe_arg(out.get("logp"), "logp", torch.float32, (batch, L + 1), dev))
+    with _OnDevice(dev):
+        size = 0 if ws is not None else _accept_ws(batch, B, L, V, dt)
+        wp, ws, size = _ws_arg("accept_sampled", size, ws, dev)
+        rc = lib().ddtree_accept_sampled(*args, wp, size, _raw_stream(dev.index))
+    if rc:
+        _check("ddtree_accept_sampled", rc)
     return out
-
-
-def _accepted_out(out, dev, batch, L):
-    _arg(out["accept_len"], "accept_len", _I32, (batch,))
-    _arg(out["next_token"], "next_token", _I32, (batch,))
-    if out.get("logp") is not None:
-        _arg(out["logp"], "logp", _F32, (batch, L + 1))
-    _on(dev, accept_len=out["accept_len"], next_token=out["next_token"], logp=out.get("logp"))
 
 
 def dspark_accept_sampled(tokens: torch.Tensor, target_logits: torch.Tensor,
@@ -739,36 +775,27 @@ def dspark_accept_sampled(tokens: torch.Tensor, target_logits: torch.Tensor,
     """Verification of a sampled chain: tokens [batch, P], target_logits [batch, P+1, V],
     draft_logits [batch, P, V] (bf16/f32), temperature [batch] (None: 1; 0: greedy), u
     [batch, P+1] uniforms, keep [batch] -> accept_len, next_token, logp [batch, P+1]."""
-    _arg(tokens, "tokens", _I32)
-    if tokens.dim() != 2:
-        raise ValueError("tokens must be [batch, P]")
-    batch, P = tokens.shape
     _arg(target_logits, "target_logits", _LOGITS)
-    V = target_logits.shape[-1]
-    _arg(target_logits, "target_logits", _LOGITS, (batch, P + 1, V))
-    _arg(draft_logits, "draft_logits", (target_logits.dtype,), (batch, P, V))
-    if temperature is not None:
-        _arg(temperature, "temperature", _F32, (batch,))
-    _arg(u, "u", _F32, (batch, P + 1))
-    if keep is not None:
-        _arg(keep, "keep", _I32, (batch,))
-    dev = target_logits.device
-    dt = _dtype_code(target_logits)
+    P = _rows_arg(tokens, "tokens", None)
+    batch, V, dev = tokens.shape[0], target_logits.shape[-1], target_logits.device
+    dt = DDT_BF16 if target_logits.dtype == torch.bfloat16 else DDT_F32
     if out is None:
-        out = dict(accept_len=torch.empty((batch,), dtype=torch.int32, device=dev),
-                   next_token=torch.empty((batch,), dtype=torch.int32, device=dev),
+        i32 = torch.empty((2, batch), dtype=torch.int32, device=dev)
+        out = dict(accept_len=i32[0], next_token=i32[1],
                    logp=torch.empty((batch, P + 1), dtype=torch.float32, device=dev))
-    _accepted_out(out, dev, batch, P)
-    _on(dev, tokens=tokens, draft_logits=draft_logits, temperature=temperature, u=u, keep=keep,
-        ws=ws)
-    with torch.cuda.device(dev):
-        if ws is None:
-            size = lib().dspark_accept_sampled_workspace_size(batch, P, V, dt)
-            ws = _scratch("chain_accept_sampled", size, dev)
-        rc = lib().dspark_accept_sampled(_ptr(tokens), _ptr(keep), _ptr(target_logits),
-                                         _ptr(draft_logits), dt, _ptr(temperature), _ptr(u), batch,
-                                         P, V, _ptr(out["accept_len"]), _ptr(out["next_token"]),
-                                         _ptr(out.get("logp")), _ptr(ws), ws.numel(),
-                                         _stream(dev))
-    _check("dspark_accept_sampled", rc)
+    args = (_dev_arg(tokens, "tokens", torch.int32, (batch, P), dev),
+            _maybe_arg(keep, "keep", torch.int32, (batch,), dev),
+            _dev_arg(target_logits, "target_logits", target_logits.dtype, (batch, P + 1, V), dev),
+            _dev_arg(draft_logits, "draft_logits", target_logits.dtype, (batch, P, V), dev), dt,
+            _maybe_arg(temperature, "temperature", torch.float32, (batch,), dev),
+            _dev_arg(u, "u", torch.float32, (batch, P + 1), dev), batch, P, V,
+            _dev_arg(out["accept_len"], "accept_len", torch.int32, (batch,), dev),
+            _dev_arg(out["next_token"], "next_token", torch.int32, (batch,), dev),
+            _maybe_arg(out.get("logp"), "logp", torch.float32, (batch, P + 1), dev))
+    with _OnDevice(dev):
+        size = 0 if ws is not None else _chain_ws(batch, P, V, dt)
+        wp, ws, size = _ws_arg("chain_accept_sampled", size, ws, dev)
+        rc = lib().dspark_accept_sampled(*args, wp, size, _raw_stream(dev.index))
+    if rc:
+        _check("dspark_accept_sampled", rc)
     return out

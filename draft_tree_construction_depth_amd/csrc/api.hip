@@ -511,8 +511,10 @@ AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_he
   const int64_t most = batch * units * ((steps + pl.least - 1) / pl.least);
   if (steps <= pl.least) slots = 0;
   else if (most < slots) slots = most;
-  pl.merge = slots > 0 ? batch * units * pl.QW : 0;
-  size_t o = align_up((size_t)batch * sizeof(ddt::AttnPlace));
+  // a split request has two slots or more for each of its units
+  const int64_t split = slots / (2 * units) < batch ? slots / (2 * units) : batch;
+  pl.merge = split * units * pl.QW;
+  size_t o = align_up((size_t)(split + 1) * sizeof(ddt::AttnPlace));
   pl.part = o;
   o = align_up(o + (size_t)slots * pl.QW * 32 * head_dim * sizeof(float));
   pl.ml = o;
@@ -1000,6 +1002,7 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   if (chk2 == DDT_EINVAL) return chk2;
   if (chk != DDT_OK || chk2 != DDT_OK) return DDT_ENOTSUP;
   const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap);
+  if (ap.rows.cap > (1 << 27)) return DDT_ENOTSUP;  // the plan counts steps in 32 bits
   if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
   ap.q = q;
   ap.k_cache = k_cache;

@@ -59,7 +59,8 @@ struct AttnTile {
 };
 
 struct AttnPlace {
-  int32_t slot, splits;  // first workspace slot of a request, its pieces
+  int32_t b, slot, splits;  // a split request, its first workspace slot, its pieces
+  int32_t count;            // entry 0: split requests
 };
 
 struct AttnParams {
@@ -79,7 +80,7 @@ struct AttnParams {
   float scale2;  // scale * log2(e)
   void* out;     // [batch][T][q_heads][head_dim]
   float* lse;    // [batch][T][q_heads], may be null
-  AttnPlace* place;  // [batch]
+  AttnPlace* place;  // split requests, in order
   float* part;       // [slot][QW] of OQ x 64 lanes x 4 floats
   float* part_ml;    // [slot][QW][64 lanes][2]: running maximum (log2) and sum
 };
@@ -127,7 +128,7 @@ __device__ bool attn_plan(const AttnParams& p, AttnWork& w) {
     const int per = (total + 7) >> 3, l = (id & 7) * per + (id >> 3);
     if ((id >> 3) >= per || l >= total) return false;
     w = AttnWork{0, l % units, l / units, splits, splits > 1 ? l : -1, len, past, nodes, steps};
-    if (l == 0 && tid == 0) p.place[0] = AttnPlace{0, splits};
+    if (l == 0 && tid == 0) p.place[0] = AttnPlace{0, 0, splits, splits > 1};
     return true;
   }
   int64_t sum = 0;
@@ -143,7 +144,10 @@ __device__ bool attn_plan(const AttnParams& p, AttnWork& w) {
   }
   int64_t c = (sum * units + p.target - 1) / p.target;
   c = c < p.least ? p.least : c;
-  int total = 0;
+  // split requests and their workspace slots are counted in one number: slots
+  // are fewer than 2^20, split requests fewer than half the slots
+  constexpr int kOne = 1 << 20;
+  int total = 0, split = 0;
   for (int64_t b0 = 0; b0 < p.batch; b0 += kAtThreads) {
     int x = 0, t;
     if (b0 + tid < p.batch) {
@@ -152,8 +156,13 @@ __device__ bool attn_plan(const AttnParams& p, AttnWork& w) {
     }
     block_excl_scan_reg<kAtThreads>(x, s_sum, t);
     total += t;
+    if (blockIdx.x == 0) {
+      block_excl_scan_reg<kAtThreads>(x > units ? 1 : 0, s_sum2, t);
+      split += t;
+    }
     __syncthreads();
   }
+  if (blockIdx.x == 0 && tid == 0) p.place[0].count = split;
   const int per = (total + 7) >> 3, l = (id & 7) * per + (id >> 3);
   if ((id >> 3) >= per || l >= total) return false;
   int at = 0, slots = 0;
@@ -163,7 +172,7 @@ __device__ bool attn_plan(const AttnParams& p, AttnWork& w) {
       attn_lengths(p, (int)(b0 + tid), past, nodes, len);
       x = (int)((attn_steps<TR>(len) + c - 1) / c) * units;
     }
-    const int y = x > units ? x : 0;  // only split requests use the workspace
+    const int y = x > units ? x + kOne : 0;  // only split requests use the workspace
     const int first = at + block_excl_scan_reg<kAtThreads>(x, s_sum, t);
     const int slot = slots + block_excl_scan_reg<kAtThreads>(y, s_sum2, t2);
     if (l >= first && l < first + x) {
@@ -182,10 +191,15 @@ __device__ bool attn_plan(const AttnParams& p, AttnWork& w) {
   const int r = l - s_hit[1];
   w.piece = r / units;
   w.u = r - w.piece * units;
-  w.slot = w.splits > 1 ? s_hit[2] + r : -1;
+  w.slot = w.splits > 1 ? (s_hit[2] & (kOne - 1)) + r : -1;
   attn_lengths(p, w.b, w.past, w.nodes, w.len);
   w.steps = attn_steps<TR>(w.len);
-  if (r == 0 && tid == 0) p.place[w.b] = AttnPlace{s_hit[2], w.splits};
+  if (r == 0 && tid == 0 && w.splits > 1) {
+    AttnPlace* e = p.place + s_hit[2] / kOne;
+    e->b = w.b;
+    e->slot = s_hit[2] & (kOne - 1);
+    e->splits = w.splits;
+  }
   return true;
 }
 
@@ -232,10 +246,16 @@ __device__ __forceinline__ bool attn_not_finite(uint32_t two) {
 template <typename H>
 __device__ __forceinline__ uint32_t attn_finite_only(uint32_t two) {
   constexpr uint32_t e = __is_same(H, __bf16) ? 0x7F80u : 0x7C00u;
-  if ((two & e) == e) two &= 0xFFFF0000u;
-  if ((two >> 16 & e) == e) two &= 0xFFFFu;
-  return two;
+  two = (two & e) == e ? two & 0xFFFF0000u : two;
+  return (two >> 16 & e) == e ? two & 0xFFFFu : two;
 }
+
+struct AttnFalse {
+  static constexpr bool value = false;
+};
+struct AttnTrue {
+  static constexpr bool value = true;
+};
 
 // A wave's running softmax over its 32 queries: lane l has query l % 32; the
 // halves hold different rows of S^T and O^T.
@@ -270,11 +290,11 @@ __device__ __forceinline__ uint64_t attn_visible(const AttnParams& p, const Attn
   return v & held;
 }
 
-// One staged tile. k, v: its rows in LDS; masked: vis says which are seen.
-template <typename H, int DH, int KT>
+// One staged tile. k, v: its rows in LDS; MASKED: vis says which are seen.
+template <typename H, int DH, int KT, bool MASKED>
 __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned char* v,
-                                          const at_u32x4 (&q)[DH / 16], float scale2, bool masked,
-                                          uint64_t vis, AttnState<DH>& st) {
+                                          const at_u32x4 (&q)[DH / 16], float scale2, uint64_t vis,
+                                          AttnState<DH>& st) {
   constexpr int NB = KT / 32, ROW = DH * 2, CPR = DH / 8;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   at_f32x16 s[NB];
@@ -290,13 +310,16 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
       s[t] = attn_mfma<H>(a, q[c], s[t]);
     }
   }
-  if (masked) {
+  if (MASKED) {
 #pragma unroll
     for (int t = 0; t < NB; ++t) {
       const uint32_t bits = (uint32_t)(vis >> (32 * t)) >> (4 * h);
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        s[t][r] = bits >> ((r >> 2) * 8 + (r & 3)) & 1 ? s[t][r] : -INFINITY;
+      for (int r = 0; r < 16; ++r) {  // a clear bit: -inf
+        const int k = (r >> 2) * 8 + (r & 3);
+        const uint32_t on = (uint32_t)((int32_t)(bits << (31 - k)) >> 31);
+        s[t][r] = __uint_as_float((on & __float_as_uint(s[t][r])) | (~on & 0xFF800000u));
+      }
     }
   }
   float top = s[0][0];
@@ -330,12 +353,11 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
   // Rows that a query does not see have weight 0, but 0 times a NaN or an
   // infinity among their values is no 0: such values (garbage behind the
   // block, on unmapped pages, or in other nodes' rows) are taken out of the
-  // product and added by hand for the queries that do see them.
+  // product and added by themselves for the queries that do see them.
   uint64_t dirty = 0;
-  if (masked) {
+  if (MASKED) {
     bool bad = false;
     if (lane < KT)
-#pragma unroll
       for (int c = 0; c < CPR; ++c) {
         const at_u32x4 x = *(const at_u32x4*)(v + lane * ROW + c * 16);
         bad |= attn_not_finite<H>(x[0]) || attn_not_finite<H>(x[1]) || attn_not_finite<H>(x[2]) ||
@@ -360,33 +382,32 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
       f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (16 * u) * ROW + at));
       f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (16 * u + 8) * ROW + at));
       at_u32x4 a = __builtin_bit_cast(at_u32x4, f);
-      if (dirty)
+      if (MASKED && dirty)
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = attn_finite_only<H>(a[i]);
       st.o[d] = attn_mfma<H>(a, pb, st.o[d]);
     }
   }
-  while (dirty) {  // uniform
+  while (MASKED && dirty) {  // uniform
     const int row = __builtin_ctzll(dirty);
     dirty &= dirty - 1;
-    // the weight of that row: register and half by the accumulator layout
-    const int reg = ((row >> 3) & 3) * 4 + (row & 3), half = (row >> 2) & 1;
-    float wt = 0.0f;
-#pragma unroll
-    for (int t = 0; t < NB; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) wt = row >> 5 == t && reg == r ? s[t][r] : wt;
-    wt = __shfl(wt, (lane & 31) + 32 * half);
     if (vis >> row & 1) {
 #pragma unroll
-      for (int d = 0; d < DH / 32; ++d)
+      for (int d = 0; d < DH / 32; ++d) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int e = 32 * d + (r >> 2) * 8 + 4 * h + (r & 3);
-          const float x =
-              (float)*(const H*)(v + row * ROW + attn_v_chunk<DH>(row, e >> 3) * 16 + (e & 7) * 2);
-          if (!(fabsf(x) < INFINITY)) st.o[d][r] = fmaf(wt, x, st.o[d][r]);
+        for (int r = 0; r < 16; r += 4) {
+          const int e = 32 * d + 2 * r + 4 * h;
+          const uint2 x =
+              *(const uint2*)(v + row * ROW + attn_v_chunk<DH>(row, e >> 3) * 16 + (e & 7) * 2);
+          // what is not finite, times any weight; 0 elsewhere
+          const uint32_t two[2] = {x.x ^ attn_finite_only<H>(x.x), x.y ^ attn_finite_only<H>(x.y)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            st.o[d][r + k] +=
+                (float)__builtin_bit_cast(H, (uint16_t)(two[k >> 1] >> (16 * (k & 1))));
         }
+        asm volatile("" ::: "memory");  // a few elements at a time
+      }
     }
   }
 }
@@ -439,11 +460,24 @@ __device__ __forceinline__ void attn_store(const AttnParams& p, int64_t row, int
     p.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// Whether cache rows [r0, r1) of request b lie on pages of the pool; every
+// thread calls it.
+__device__ __forceinline__ bool attn_mapped(const PagedRows& p, int b, int r0, int r1, int* s_any) {
+  if (!p.table) return true;
+  bool bad = false;
+  for (int g = (r0 >> p.shift) + (int)threadIdx.x; g <= (r1 - 1) >> p.shift; g += kAtThreads)
+    bad |= page_of(p, b, g << p.shift) < 0;
+  const uint64_t any = __ballot(bad);
+  if ((threadIdx.x & 63) == 0) s_any[threadIdx.x >> 6] = any != 0;
+  __syncthreads();
+  return !(s_any[0] | s_any[1] | s_any[2] | s_any[3]);
+}
+
 template <typename H, int DH, int QW>
 __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(AttnParams p) {
   using C = AttnTile<DH, QW>;
   __shared__ __align__(256) unsigned char lds[C::LDS];
-  __shared__ int s_bad[C::NG][C::NBUF];  // step whose tile has rows on no page
+  __shared__ int s_any[kAtWaves];
   AttnWork w;
   if (!attn_plan<C::TR>(p, w)) return;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -471,17 +505,19 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
 #pragma unroll
     for (int r = 0; r < 16; ++r) st.o[d][r] = 0.0f;
 
-  // the piece's steps
+  // the piece's steps [t0, t1); those before tm see every row they hold
   const int each = (w.steps + w.splits - 1) / w.splits;
   const int t0 = w.piece * each;
   const int t1 = w.len == 0 ? t0 : (t0 + each < w.steps ? t0 + each : w.steps);
   // this thread's chunks of a tile: row ld_row + k * STEP, chunk ld_c
   constexpr int STEP = QW * kWave / C::CPR;
   const int gt = wq * kWave + lane, ld_row = gt / C::CPR, ld_c = gt % C::CPR;
-  unsigned char* tiles = lds + g * C::NBUF * 2 * C::TILE;
-  if (tid < C::NG * C::NBUF) s_bad[tid / C::NBUF][tid % C::NBUF] = -1;
+  unsigned char* const tiles = lds + g * C::NBUF * 2 * C::TILE;
   at_u32x4 kr[C::LOADS], vr[C::LOADS];
   int page[C::LOADS];
+  const int64_t page_rows = (int64_t)p.kv_heads * p.rows.page_size;
+  const H* const k0 = (const H*)p.k_cache + (int64_t)head * p.rows.page_size * DH + ld_c * 8;
+  const H* const v0 = (const H*)p.v_cache + (int64_t)head * p.rows.page_size * DH + ld_c * 8;
   auto row_of = [&](int t, int k) {  // the cache row that chunk k is of, clamped into the request
     const int r = t * C::TR + g * C::KT + ld_row + k * STEP;
     return r < w.len ? r : w.len - 1;
@@ -490,37 +526,38 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
 #pragma unroll
     for (int k = 0; k < C::LOADS; ++k) page[k] = page_of(p.rows, w.b, row_of(t, k));
   };
-  bool bad = false;
   auto fetch = [&](int t) {
-    bad = false;
 #pragma unroll
     for (int k = 0; k < C::LOADS; ++k) {
-      const int r = row_of(t, k);
-      bad |= page[k] < 0;
+      // rows on no page: some row's values, taken out by the mask
       const int64_t pg = page[k] < 0 ? 0 : page[k];
-      const int rp = page[k] < 0 ? 0 : row_in_page(p.rows, r);
-      const int64_t at = ((pg * p.kv_heads + head) * p.rows.page_size + rp) * DH + ld_c * 8;
-      kr[k] = *(const at_u32x4*)((const H*)p.k_cache + at);
-      vr[k] = *(const at_u32x4*)((const H*)p.v_cache + at);
+      const int rp = page[k] < 0 ? 0 : row_in_page(p.rows, row_of(t, k));
+      const int64_t at = (pg * page_rows + rp) * DH;
+      kr[k] = *(const at_u32x4*)(k0 + at);
+      vr[k] = *(const at_u32x4*)(v0 + at);
     }
   };
+  int tm = t0;
   if (t0 < t1) {
     find(t0);
     fetch(t0);
     if (t0 + 1 < t1) find(t0 + 1);
+    const int end = t1 * C::TR < w.len ? t1 * C::TR : w.len;
+    if (attn_mapped(p.rows, w.b, t0 * C::TR, end, s_any)) {
+      tm = w.past / C::TR;
+      tm = tm < t0 ? t0 : (tm > t1 ? t1 : tm);
+    }
   }
-  __syncthreads();  // s_bad
-  for (int t = t0; t < t1; ++t) {
-    const int buf = C::NBUF == 2 ? t & 1 : 0;
-    unsigned char* kt = tiles + buf * 2 * C::TILE;
-    unsigned char* vt = kt + C::TILE;
+  auto step = [&](int t, auto is_masked) {
+    constexpr bool MASKED = decltype(is_masked)::value;
+    unsigned char* const kt = tiles + (C::NBUF == 2 ? (t & 1) * 2 * C::TILE : 0);
+    unsigned char* const vt = kt + C::TILE;
 #pragma unroll
     for (int k = 0; k < C::LOADS; ++k) {
       const int row = ld_row + k * STEP;
       *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, ld_c) * 16) = kr[k];
       *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, ld_c) * 16) = vr[k];
     }
-    if (__ballot(bad) && lane == 0) s_bad[g][buf] = t;
     if (QW > 1) {
       __syncthreads();
     } else {  // the tile is the wave's own: its LDS operations take effect in order
@@ -533,22 +570,24 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
       if (t + 2 < t1) find(t + 2);
     }
     const int r0 = t * C::TR + g * C::KT;
-    if (busy && r0 < w.len) {
-      const bool masked = r0 + C::KT > w.past || r0 + C::KT > w.len || s_bad[g][buf] == t;
+    if (busy && (!MASKED || r0 < w.len)) {
       uint64_t vis = 0;
-      if (masked) {
+      if (MASKED) {
         const int r = r0 + lane;
         const bool held = lane < C::KT && r < w.len && page_of(p.rows, w.b, r) >= 0;
         vis = attn_visible<C::KT>(p, w, r0, i, live, __ballot(held));
       }
-      attn_tile<H, DH, C::KT>(kt, vt, q, p.scale2, masked, vis, st);
+      attn_tile<H, DH, C::KT, MASKED>(kt, vt, q, p.scale2, vis, st);
     }
     if (QW == 1) {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-  }
+  };
+  int t = t0;
+  for (; t < tm; ++t) step(t, AttnFalse{});
+  for (; t < t1; ++t) step(t, AttnTrue{});
   st.l = attn_sum_halves(st.l);
 
   // merge the groups
@@ -599,12 +638,11 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
 template <typename H, int DH, int QW>
 __global__ __launch_bounds__(DH * 2) void attn_merge_kernel(AttnParams p) {
   const int units = p.kv_heads * p.MT;
-  const int64_t id = blockIdx.x;  // request, unit, query wave
-  const int wq = (int)(id % QW);
-  const int64_t bu = id / QW;
-  const int b = (int)(bu / units), u = (int)(bu - (int64_t)b * units);
-  const AttnPlace pl = p.place[b];
-  if (pl.splits <= 1) return;
+  const int id = (int)blockIdx.x;  // split request, unit, query wave
+  const int wq = id % QW, k = id / QW / units, u = id / QW - k * units;
+  if (k >= p.place[0].count) return;
+  const AttnPlace pl = p.place[k];
+  const int b = pl.b;
   int past, nodes, len;
   attn_lengths(p, b, past, nodes, len);
   const int lane = threadIdx.x & 63, d = threadIdx.x >> 6;

@@ -481,66 +481,64 @@ void launch_append(const ddt::AppendParams& ap, int64_t blocks, int interleaved,
 
 // ---- attention: waves along the queries, workgroups, workspace -------------------
 struct AttnPlan {
-  int QW, MT;
-  int64_t target, least, grid, merge;  // workgroups of the launches; merge 0: nothing to merge
+  int NQ, QW;  // queries of a wave, waves side by side
+  int64_t groups, least;
+  bool merge;  // a unit can be cut
   size_t part, ml, end;
 };
-
-// Waves side by side: as many as the query rows of a key/value head fill.
-int attn_waves(int32_t T, int32_t G, int32_t head_dim) {
-  const int64_t M = (int64_t)T * G;
-  const int qw = M <= 32 ? 1 : (M <= 64 ? 2 : 4);
-  return head_dim == 256 && qw == 1 ? 2 : qw;  // four groups' tiles would fill the LDS
-}
 
 AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
                         int32_t head_dim, int64_t cap) {
   AttnPlan pl;
   const int G = q_heads / kv_heads;
-  pl.QW = attn_waves(T, G, head_dim);
-  pl.MT = (int)(((int64_t)T * G + 32 * pl.QW - 1) / (32 * pl.QW));
-  const int64_t units = (int64_t)kv_heads * pl.MT;
+  // up to 64 query rows of a key/value head: 16 to a wave, as many waves side
+  // by side as they fill (at head_dim 256 two or more: four groups' tiles
+  // would not leave registers for the next ones); more: 32 to a wave
+  const int64_t M = (int64_t)T * G;
+  pl.NQ = M <= 64 ? 16 : 32;
+  pl.QW = M <= 16 && head_dim < 256 ? 1 : (M <= 32 ? 2 : 4);
   const int rows = pl.QW == 4 ? (head_dim <= 128 ? 64 : 32) : 32 * (4 / pl.QW);  // AttnTile::TR
-  pl.target = 512;  // two workgroups on each of 256 CUs
-  pl.least = 2;
-  pl.grid = (pl.target + batch * units + 7) & ~(int64_t)7;
   const int64_t steps = (cap + rows - 1) / rows;
-  // split requests take at most twice the target's pieces (each has two or
-  // more, none of which but the last is shorter than the common size)
-  int64_t slots = 2 * pl.target;
-  const int64_t most = batch * units * ((steps + pl.least - 1) / pl.least);
-  if (steps <= pl.least) slots = 0;
-  else if (most < slots) slots = most;
-  // a split request has two slots or more for each of its units
-  const int64_t split = slots / (2 * units) < batch ? slots / (2 * units) : batch;
-  pl.merge = split * units * pl.QW;
-  size_t o = align_up((size_t)(split + 1) * sizeof(ddt::AttnPlace));
+  const int64_t tiles = (M + pl.NQ * pl.QW - 1) / (pl.NQ * pl.QW);
+  pl.least = 2;
+  // two workgroups on each of 256 CUs (one where a tile fills the LDS or the
+  // registers), fewer for little work
+  pl.groups = head_dim == 256 ? 256 : 512;
+  const int64_t axis = steps > ((int64_t)1 << 31) / (kv_heads * tiles) / batch
+                           ? (int64_t)1 << 31
+                           : batch * kv_heads * tiles * steps;
+  const int64_t want = ((axis + pl.least - 1) / pl.least + 7) & ~(int64_t)7;
+  if (want < pl.groups) pl.groups = want;
+  pl.merge = steps > 1;
+  const int64_t slots = pl.merge ? 2 * pl.groups : 0;
+  size_t o = align_up((size_t)pl.groups * sizeof(ddt::AttnPlace));
   pl.part = o;
-  o = align_up(o + (size_t)slots * pl.QW * 32 * head_dim * sizeof(float));
+  o = align_up(o + (size_t)slots * pl.QW * pl.NQ * head_dim * sizeof(float));
   pl.ml = o;
   o = align_up(o + (size_t)slots * pl.QW * 64 * 2 * sizeof(float));
   pl.end = o;
   return pl;
 }
 
-template <typename H, int DH, int QW>
+template <typename H, int DH, int NQ, int QW>
 int launch_attn_tile(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
-  hipLaunchKernelGGL((ddt::attn_kernel<H, DH, QW>), dim3((unsigned)pl.grid), dim3(ddt::kAtThreads),
-                     0, st, ap);
+  hipLaunchKernelGGL((ddt::attn_kernel<H, DH, NQ, QW>), dim3((unsigned)pl.groups),
+                     dim3(ddt::kAtThreads), 0, st, ap);
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
-  if (pl.merge == 0) return DDT_OK;
-  hipLaunchKernelGGL((ddt::attn_merge_kernel<H, DH, QW>), dim3((unsigned)pl.merge), dim3(DH * 2),
-                     0, st, ap);
+  if (!pl.merge) return DDT_OK;
+  hipLaunchKernelGGL((ddt::attn_merge_kernel<H, DH, NQ, QW>), dim3((unsigned)(pl.groups * QW)),
+                     dim3(ddt::AttnTile<DH, NQ, QW>::PIECES * 32), 0, st, ap);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
 }
 
 template <typename H, int DH>
 int launch_attn_waves(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
+  if (pl.NQ == 32) return launch_attn_tile<H, DH, 32, 4>(ap, pl, st);
+  if (pl.QW == 4) return launch_attn_tile<H, DH, 16, 4>(ap, pl, st);
   if constexpr (DH < 256) {
-    if (pl.QW == 1) return launch_attn_tile<H, DH, 1>(ap, pl, st);
+    if (pl.QW == 1) return launch_attn_tile<H, DH, 16, 1>(ap, pl, st);
   }
-  if (pl.QW == 2) return launch_attn_tile<H, DH, 2>(ap, pl, st);
-  return launch_attn_tile<H, DH, 4>(ap, pl, st);
+  return launch_attn_tile<H, DH, 16, 2>(ap, pl, st);
 }
 
 template <typename H>
@@ -1012,8 +1010,7 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   ap.q_heads = q_heads;
   ap.kv_heads = kv_heads;
   ap.G = q_heads / kv_heads;
-  ap.MT = pl.MT;
-  ap.target = (int32_t)pl.target;
+  ap.groups = (int32_t)pl.groups;
   ap.least = (int32_t)pl.least;
   ap.past_len = past_len;
   ap.num_nodes = num_nodes;

@@ -9,25 +9,31 @@
 //
 // One pass over the cache with the running maximum and sum of the softmax.
 // The T * G query rows that share a key/value head form the columns of the
-// products: a wave owns 32 of them and forms S^T = K Q^T (32x32x16 MFMA, K
-// fragments from LDS, Q fragments in registers), so that a lane holds scores
-// of one query only: maximum, sum and rescaling need no reduction across
-// lanes beyond one exchange between the wave's halves, and the weights leave
-// the accumulator layout as the B operand of O^T += V^T P^T as they are. The
-// accumulator's row order (4-row pieces alternating between the halves) is
-// the order in which V^T's columns are read; V's fragments come transposed
-// out of row-major LDS (ds_read_b64_tr_b16).
+// products: a wave owns NQ = 32 of them (or 16) and forms S^T = K Q^T
+// (32x32x16 MFMA, or 16x16x32; K fragments from LDS, Q fragments in
+// registers), so that a lane holds scores of one query only: maximum, sum and
+// rescaling need no reduction across lanes beyond an exchange between the
+// wave's halves (quarters), and the weights leave the accumulator layout as
+// the B operand of O^T += V^T P^T as they are. The accumulator's row order
+// (4-row pieces dealt to the halves or quarters in turn) is the order in
+// which V^T's columns are read; V's fragments come transposed out of
+// row-major LDS (ds_read_b64_tr_b16).
 //
-// A workgroup is four waves: QW of them side by side over 32 QW queries, NG =
+// A workgroup is four waves: QW of them side by side over NQ QW queries, NG =
 // 4 / QW groups of those over different cache rows, merged at the end. Few
-// queries (plain decoding, short chains) are bound by the cache's bytes, so
-// all four waves take rows (QW = 1); many (trees) by the products and the
-// LDS reads that feed them, so all four share one staged tile (QW = 4).
+// queries (plain decoding, short chains) are bound by the cache's bytes: up to
+// 64 rows share a key/value head's pass, 16 to a wave (half the registers of
+// 32), and as many waves as are left take other rows. More (trees) are bound
+// by the products and the LDS reads that feed them, so all four waves share
+// one staged tile, and 32 queries to a wave halve the LDS reads per product.
 //
 // The next tile's rows are in flight (global to registers) while the present
-// one is worked on. The cache's rows are split over workgroups in pieces of
-// about one size for all requests, from the lengths on the device (attn_plan);
-// the pieces' results go through the workspace and attn_merge_kernel.
+// one is worked on. Work is cut evenly: all steps of all units (a unit: one
+// request's, key/value head's and query tile's pass over the cache) lie on one
+// axis, and each of the workgroups that the card holds at once takes an equal
+// stretch of it, from the lengths on the device (attn_plan). A unit cut by a
+// stretch's end leaves partial results in the workspace for
+// attn_merge_kernel.
 #pragma once
 
 #include "paged.hpp"
@@ -43,9 +49,9 @@ typedef short at_s16x4 __attribute__((ext_vector_type(4)));
 typedef float at_f32x4 __attribute__((ext_vector_type(4)));
 typedef float at_f32x16 __attribute__((ext_vector_type(16)));
 
-template <int DH_, int QW_>
+template <int DH_, int NQ_, int QW_>
 struct AttnTile {
-  static constexpr int DH = DH_, QW = QW_;
+  static constexpr int DH = DH_, NQ = NQ_, QW = QW_;
   static constexpr int NG = kAtWaves / QW;                 // groups over cache rows
   static constexpr int KT = QW == 4 && DH <= 128 ? 64 : 32;  // rows of a group's tile
   static constexpr int TR = NG * KT;                       // rows of a workgroup's step
@@ -55,12 +61,14 @@ struct AttnTile {
   static constexpr int NBUF = QW == 1 ? 1 : 2;             // one wave needs no second buffer
   static constexpr int TILE = KT * ROW;                    // bytes of K (or V) of a tile
   static constexpr int LDS = NG * NBUF * 2 * TILE;
-  static constexpr int OQ = DH / 8;                        // 4-float pieces of O per lane
+  static constexpr int PIECES = DH * NQ / (4 * kWave);     // 4-float pieces of O per lane
 };
 
+// What a workgroup's stretch leaves to merge: the unit that it begins and does
+// not end (slot 2 w + 1; b < 0: none), and whether its first piece (slot 2 w),
+// the continuation of the unit before, ends that unit.
 struct AttnPlace {
-  int32_t b, slot, splits;  // a split request, its first workspace slot, its pieces
-  int32_t count;            // entry 0: split requests
+  int32_t b, u, ends, pad;
 };
 
 struct AttnParams {
@@ -69,9 +77,8 @@ struct AttnParams {
   const void* v_cache;
   int64_t batch;
   int32_t T, q_heads, kv_heads, G;
-  int32_t MT;       // query tiles of a (request, key/value head)
-  int32_t target;   // workgroups to split the rows over
-  int32_t least;    // fewest steps of a piece
+  int32_t groups;  // workgroups that share the work
+  int32_t least;   // fewest steps for a workgroup of its own
   PagedRows rows;
   const int32_t* past_len;
   const int32_t* num_nodes;  // [batch], may be null: T - 1
@@ -80,150 +87,187 @@ struct AttnParams {
   float scale2;  // scale * log2(e)
   void* out;     // [batch][T][q_heads][head_dim]
   float* lse;    // [batch][T][q_heads], may be null
-  AttnPlace* place;  // split requests, in order
-  float* part;       // [slot][QW] of OQ x 64 lanes x 4 floats
+  AttnPlace* place;  // [groups]
+  float* part;       // [slot][QW] of PIECES x 64 lanes x 4 floats, two slots a workgroup
   float* part_ml;    // [slot][QW][64 lanes][2]: running maximum (log2) and sum
 };
 
-struct AttnWork {
-  int b, u, piece, splits, slot;  // slot: of this workgroup, -1 for the only piece
-  int len, past, nodes, steps;
+// One request's work: rows [0, rows) of its block see anything (0: the
+// request is taken out); its waves of NQ query rows per key/value head are
+// dealt evenly to `tiles` query tiles.
+struct AttnReq {
+  int past, rows, len, steps, waves, tiles;
 };
 
-__device__ __forceinline__ void attn_lengths(const AttnParams& p, int b, int& past, int& nodes,
-                                             int& len) {
-  past = p.past_len[b];
-  nodes = p.num_nodes ? p.num_nodes[b] : p.T - 1;
+template <class C>
+__device__ __forceinline__ AttnReq attn_request(const AttnParams& p, int64_t b) {
+  AttnReq r;
+  r.past = p.past_len[b];
+  int nodes = p.num_nodes ? p.num_nodes[b] : p.T - 1;
   nodes = nodes < 0 ? 0 : (nodes > p.T - 1 ? p.T - 1 : nodes);
-  int64_t n = past < 0 ? 0 : (int64_t)past + nodes + 1;
-  len = (int)(n < p.rows.cap ? n : p.rows.cap);
+  r.rows = r.past < 0 ? 0 : nodes + 1;
+  const int64_t n = (int64_t)r.past + r.rows;
+  r.len = r.past < 0 ? 0 : (int)(n < p.rows.cap ? n : p.rows.cap);
+  // one step for an empty request: its rows are cleared
+  r.steps = r.len > C::TR ? (r.len + C::TR - 1) / C::TR : 1;
+  r.waves = (r.rows * p.G + C::NQ - 1) / C::NQ;
+  r.tiles = r.waves > C::QW ? (r.waves + C::QW - 1) / C::QW : 1;
+  return r;
 }
 
-template <int TR>
-__device__ __forceinline__ int attn_steps(int len) {
-  return len > TR ? (len + TR - 1) / TR : 1;  // one for an empty request: its rows are cleared
+// Inclusive scan of one 64-bit number per lane.
+__device__ __forceinline__ int64_t attn_wave_scan(int64_t x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
 }
 
-// Which piece of which request this workgroup takes; false: none. Every
-// request's rows are cut into pieces of at most c steps, c the same for all,
-// such that about p.target pieces result; logical order is request, piece,
-// unit (key/value head, then query tile), and consecutive workgroups of one
-// XCD (ids 8 apart) take consecutive ones, so that a piece's query tiles read
-// its rows from one L2.
-template <int TR>
-__device__ bool attn_plan(const AttnParams& p, AttnWork& w) {
-  __shared__ __align__(16) int s_sum[kAtWaves];
-  __shared__ __align__(16) int s_sum2[kAtWaves];
-  __shared__ int s_hit[4];
-  const int tid = threadIdx.x;
-  const int units = p.kv_heads * p.MT;
-  const int id = (int)blockIdx.x;
-  int past, nodes, len;
+// A position on the axis of steps: request, unit of the request (key/value
+// head, then query tile) and step.
+struct AttnPos {
+  int64_t x;  // steps before it
+  int b, u, s;
+};
+
+__device__ __forceinline__ AttnPos attn_uniform(const AttnPos& a) {
+  const uint64_t x = (uint64_t)a.x;
+  return AttnPos{
+      (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)x)),
+      __builtin_amdgcn_readfirstlane(a.b), __builtin_amdgcn_readfirstlane(a.u),
+      __builtin_amdgcn_readfirstlane(a.s)};
+}
+
+// The stretch [from, to) of workgroup w of `groups`; false: none. The axis is
+// request after request, each tiles * kv_heads units of `steps`. An end that
+// falls close to a unit's is moved there (by up to an eighth of a stretch), so
+// that short units are not cut at all.
+template <class C>
+__device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnPos& from, AttnPos& to) {
+  __shared__ int64_t s_part[kAtWaves];
+  __shared__ AttnPos s_pos[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto axis = [&](int64_t b) -> int64_t {
+    if (b >= p.batch) return 0;
+    const AttnReq r = attn_request<C>(p, b);
+    return (int64_t)r.tiles * p.kv_heads * r.steps;
+  };
+  int64_t total = 0;
   if (p.batch == 1) {
-    attn_lengths(p, 0, past, nodes, len);
-    const int steps = attn_steps<TR>(len);
-    int64_t c = ((int64_t)steps * units + p.target - 1) / p.target;
-    c = c < p.least ? p.least : c;
-    const int splits = (int)((steps + c - 1) / c), total = splits * units;
-    const int per = (total + 7) >> 3, l = (id & 7) * per + (id >> 3);
-    if ((id >> 3) >= per || l >= total) return false;
-    w = AttnWork{0, l % units, l / units, splits, splits > 1 ? l : -1, len, past, nodes, steps};
-    if (l == 0 && tid == 0) p.place[0] = AttnPlace{0, 0, splits, splits > 1};
-    return true;
-  }
-  int64_t sum = 0;
-  for (int64_t b0 = 0; b0 < p.batch; b0 += kAtThreads) {
-    int x = 0, t;
-    if (b0 + tid < p.batch) {
-      attn_lengths(p, (int)(b0 + tid), past, nodes, len);
-      x = attn_steps<TR>(len);
-    }
-    block_excl_scan_reg<kAtThreads>(x, s_sum, t);
-    sum += t;
+    total = axis(0);
+  } else {
+    int64_t sum = 0;
+    for (int64_t b = tid; b < p.batch; b += kAtThreads) sum += axis(b);
+    sum = attn_wave_scan(sum);
+    if (lane == 63) s_part[wave] = sum;
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAtWaves; ++i) total += s_part[i];
   }
-  int64_t c = (sum * units + p.target - 1) / p.target;
-  c = c < p.least ? p.least : c;
-  // split requests and their workspace slots are counted in one number: slots
-  // are fewer than 2^20, split requests fewer than half the slots
-  constexpr int kOne = 1 << 20;
-  int total = 0, split = 0;
-  for (int64_t b0 = 0; b0 < p.batch; b0 += kAtThreads) {
-    int x = 0, t;
-    if (b0 + tid < p.batch) {
-      attn_lengths(p, (int)(b0 + tid), past, nodes, len);
-      x = (int)((attn_steps<TR>(len) + c - 1) / c) * units;
+  const int64_t want = (total + p.least - 1) / p.least;
+  const int n = want < p.groups ? (int)want : p.groups;
+  // consecutive workgroups of one XCD (ids 8 apart) take consecutive
+  // stretches: query tiles of one unit read its rows from one L2
+  const int per = (n + 7) >> 3;
+  if ((w >> 3) >= per) {  // the ids left over take the numbers from 8 per on
+    k = w;
+    return false;
+  }
+  k = (w & 7) * per + (w >> 3);
+  if (k >= n) return false;
+  const int64_t slack = (total / n) >> 3;
+  // end number e of the stretches, as a position in the request that holds it
+  auto place = [&](int64_t e, int64_t before, int b, AttnPos& at) {
+    const AttnReq r = attn_request<C>(p, b);
+    const int64_t x = total * e / n - before;
+    int64_t u = x / r.steps, s = x - u * r.steps;
+    if (e > 0 && e < n) {
+      if (s <= slack && s <= r.steps - s) {
+        s = 0;
+      } else if (r.steps - s <= slack) {
+        s = 0;
+        ++u;
+      }
     }
-    block_excl_scan_reg<kAtThreads>(x, s_sum, t);
-    total += t;
-    if (blockIdx.x == 0) {
-      block_excl_scan_reg<kAtThreads>(x > units ? 1 : 0, s_sum2, t);
-      split += t;
+    at = AttnPos{before + u * r.steps + s, b, (int)u, (int)s};
+  };
+  if (p.batch == 1) {
+    place(k, 0, 0, from);
+    place(k + 1, 0, 0, to);
+  } else {
+    const int64_t x0 = total * k / n, x1 = total * (k + 1) / n;
+    int64_t base = 0;
+    for (int64_t b0 = 0; b0 < p.batch; b0 += kAtThreads) {
+      const int64_t b = b0 + tid, mine = axis(b);
+      int64_t incl = attn_wave_scan(mine);
+      __syncthreads();  // s_part's readers before this round
+      if (lane == 63) s_part[wave] = incl;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int i = 0; i < kAtWaves; ++i) {
+        incl += i < wave ? s_part[i] : 0;
+        all += s_part[i];
+      }
+      const int64_t before = base + incl - mine;
+      if (x0 >= before && x0 < before + mine) place(k, before, (int)b, s_pos[0]);
+      // (the axis' own end belongs to the last request)
+      if (x1 > before && x1 <= before + mine) place(k + 1, before, (int)b, s_pos[1]);
+      base += all;
+      if (base >= x1) break;  // uniform
     }
     __syncthreads();
-  }
-  if (blockIdx.x == 0 && tid == 0) p.place[0].count = split;
-  const int per = (total + 7) >> 3, l = (id & 7) * per + (id >> 3);
-  if ((id >> 3) >= per || l >= total) return false;
-  int at = 0, slots = 0;
-  for (int64_t b0 = 0; b0 < p.batch; b0 += kAtThreads) {
-    int x = 0, t, t2;
-    if (b0 + tid < p.batch) {
-      attn_lengths(p, (int)(b0 + tid), past, nodes, len);
-      x = (int)((attn_steps<TR>(len) + c - 1) / c) * units;
-    }
-    const int y = x > units ? x + kOne : 0;  // only split requests use the workspace
-    const int first = at + block_excl_scan_reg<kAtThreads>(x, s_sum, t);
-    const int slot = slots + block_excl_scan_reg<kAtThreads>(y, s_sum2, t2);
-    if (l >= first && l < first + x) {
-      s_hit[0] = (int)b0 + tid;
-      s_hit[1] = first;
-      s_hit[2] = slot;
-      s_hit[3] = x / units;
-    }
-    __syncthreads();
-    at += t;
-    slots += t2;
-    if (at > l) break;  // uniform
-  }
-  w.b = s_hit[0];
-  w.splits = s_hit[3];
-  const int r = l - s_hit[1];
-  w.piece = r / units;
-  w.u = r - w.piece * units;
-  w.slot = w.splits > 1 ? (s_hit[2] & (kOne - 1)) + r : -1;
-  attn_lengths(p, w.b, w.past, w.nodes, w.len);
-  w.steps = attn_steps<TR>(w.len);
-  if (r == 0 && tid == 0 && w.splits > 1) {
-    AttnPlace* e = p.place + s_hit[2] / kOne;
-    e->b = w.b;
-    e->slot = s_hit[2] & (kOne - 1);
-    e->splits = w.splits;
+    from = attn_uniform(s_pos[0]);
+    to = attn_uniform(s_pos[1]);
   }
   return true;
 }
 
 template <typename H>
 __device__ __forceinline__ at_f32x16 attn_mfma(at_u32x4 a, at_u32x4 b, at_f32x16 c) {
-  if constexpr (__is_same(H, __bf16)) {
-    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  typedef H v8 __attribute__((ext_vector_type(8)));
+  if constexpr (__is_same(H, __bf16))
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a),
                                                    __builtin_bit_cast(v8, b), c, 0, 0, 0);
-  } else {
-    typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  else
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a),
                                                   __builtin_bit_cast(v8, b), c, 0, 0, 0);
-  }
+}
+template <typename H>
+__device__ __forceinline__ at_f32x4 attn_mfma(at_u32x4 a, at_u32x4 b, at_f32x4 c) {
+  typedef H v8 __attribute__((ext_vector_type(8)));
+  if constexpr (__is_same(H, __bf16))
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a),
+                                                   __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a),
+                                                  __builtin_bit_cast(v8, b), c, 0, 0, 0);
 }
 
-// The other half's value of this lane's query, with this one's.
-__device__ __forceinline__ float attn_max_halves(float x) {
+// Over the lanes that hold the same query: l and l + 32, or l % 16 in all
+// four quarters.
+template <int NQ, typename Op>
+__device__ __forceinline__ float attn_across(float x, Op op) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  x = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  if constexpr (NQ == 16) {
+    const auto t =
+        __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = op(__uint_as_float(t[0]), __uint_as_float(t[1]));
+  }
+  return x;
 }
-__device__ __forceinline__ float attn_sum_halves(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+template <int NQ>
+__device__ __forceinline__ float attn_max_across(float x) {
+  return attn_across<NQ>(x, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int NQ>
+__device__ __forceinline__ float attn_sum_across(float x) {
+  return attn_across<NQ>(x, [](float a, float b) { return a + b; });
 }
 
 // Places of a 16-byte chunk in a staged tile. K is read 32 rows at a time at
@@ -257,24 +301,51 @@ struct AttnTrue {
   static constexpr bool value = true;
 };
 
-// A wave's running softmax over its 32 queries: lane l has query l % 32; the
-// halves hold different rows of S^T and O^T.
+// A wave's running softmax over its NQ queries: lane l has query l % NQ; the
+// lanes with one query hold different rows of S^T and O^T.
+template <int DH, int NQ>
+struct AttnState;
+
 template <int DH>
-struct AttnState {
+struct AttnState<DH, 32> {
+  static constexpr int PIECES = DH / 8, R = 16;  // registers of an accumulator
   float m, mref, l;  // maximum in use (log2), the same or 0 while it is -inf, sum of weights
   at_f32x16 o[DH / 32];
+  __device__ __forceinline__ at_f32x4 get(int j) const {
+    const at_f32x16& x = o[j >> 2];
+    const int r = 4 * (j & 3);
+    return at_f32x4{x[r], x[r + 1], x[r + 2], x[r + 3]};
+  }
+  __device__ __forceinline__ void set(int j, at_f32x4 v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j >> 2][4 * (j & 3) + e] = v[e];
+  }
+  // first of the four head elements of piece j
+  static __device__ __forceinline__ int element(int j, int lane) {
+    return 32 * (j >> 2) + 8 * (j & 3) + 4 * (lane >> 5);
+  }
+};
+
+template <int DH>
+struct AttnState<DH, 16> {
+  static constexpr int PIECES = DH / 16, R = 4;
+  float m, mref, l;
+  at_f32x4 o[DH / 16];
+  __device__ __forceinline__ at_f32x4 get(int j) const { return o[j]; }
+  __device__ __forceinline__ void set(int j, at_f32x4 v) { o[j] = v; }
+  static __device__ __forceinline__ int element(int j, int lane) { return 16 * j + 4 * (lane >> 4); }
 };
 
 // Rows of the group's tile that this lane's query sees, as bits.
 template <int KT>
-__device__ __forceinline__ uint64_t attn_visible(const AttnParams& p, const AttnWork& w, int r0,
+__device__ __forceinline__ uint64_t attn_visible(const AttnParams& p, int64_t b, int past, int r0,
                                                  int i, bool live, uint64_t held) {
   if (!live) return 0;
-  const int a = w.past - r0;  // rows of the tile before the block
+  const int a = past - r0;  // rows of the tile before the block
   uint64_t v = a >= 64 ? ~0ull : (a > 0 ? (1ull << a) - 1 : 0ull);
   if (a < 64) {
     if (p.mask) {
-      const uint64_t* words = p.mask + ((int64_t)w.b * p.T + i) * p.W;
+      const uint64_t* words = p.mask + (b * p.T + i) * p.W;
       if (a >= 0) {
         v |= words[0] << a;
       } else {
@@ -291,33 +362,35 @@ __device__ __forceinline__ uint64_t attn_visible(const AttnParams& p, const Attn
 }
 
 // One staged tile. k, v: its rows in LDS; MASKED: vis says which are seen.
-template <typename H, int DH, int KT, bool MASKED>
+template <typename H, int DH, int NQ, int KT, bool MASKED>
 __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned char* v,
-                                          const at_u32x4 (&q)[DH / 16], float scale2, uint64_t vis,
-                                          AttnState<DH>& st) {
-  constexpr int NB = KT / 32, ROW = DH * 2, CPR = DH / 8;
-  const int lane = threadIdx.x & 63, h = lane >> 5;
-  at_f32x16 s[NB];
+                                          const at_u32x4 (&q)[DH * NQ / 512], float scale2,
+                                          uint64_t vis, AttnState<DH, NQ>& st, int lane) {
+  typedef AttnState<DH, NQ> State;
+  constexpr int NB = KT / NQ, R = State::R, ROW = DH * 2, CPR = DH / 8;
+  constexpr int Z = kWave / NQ;  // lanes with one query
+  const int z = lane / NQ;
+  decltype(st.o[0] + st.o[0]) s[NB];
 #pragma unroll
   for (int t = 0; t < NB; ++t) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
-    const int row = 32 * t + (lane & 31);
+    for (int r = 0; r < R; ++r) s[t][r] = 0.0f;
+    const int row = NQ * t + lane % NQ;
 #pragma unroll
-    for (int c = 0; c < DH / 16; ++c) {
-      const at_u32x4 a =
-          *(const at_u32x4*)(k + row * ROW + attn_k_chunk<DH>(row, 2 * c + h) * 16);
+    for (int c = 0; c < CPR / Z; ++c) {
+      const at_u32x4 a = *(const at_u32x4*)(k + row * ROW + attn_k_chunk<DH>(row, Z * c + z) * 16);
       s[t] = attn_mfma<H>(a, q[c], s[t]);
     }
   }
+  // s[t][r] is row NQ t + 4 Z (r / 4) + 4 z + r % 4
   if (MASKED) {
 #pragma unroll
     for (int t = 0; t < NB; ++t) {
-      const uint32_t bits = (uint32_t)(vis >> (32 * t)) >> (4 * h);
+      const uint32_t bits = (uint32_t)(vis >> (NQ * t)) >> (4 * z);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {  // a clear bit: -inf
-        const int k = (r >> 2) * 8 + (r & 3);
-        const uint32_t on = (uint32_t)((int32_t)(bits << (31 - k)) >> 31);
+      for (int r = 0; r < R; ++r) {  // a clear bit: -inf
+        const int b = (r >> 2) * 4 * Z + (r & 3);
+        const uint32_t on = (uint32_t)((int32_t)(bits << (31 - b)) >> 31);
         s[t][r] = __uint_as_float((on & __float_as_uint(s[t][r])) | (~on & 0xFF800000u));
       }
     }
@@ -326,17 +399,17 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
 #pragma unroll
   for (int t = 0; t < NB; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-  top = attn_max_halves(top) * scale2;
+    for (int r = 0; r < R; ++r) top = fmaxf(top, s[t][r]);
+  top = attn_max_across<NQ>(top) * scale2;
   // The maximum moves only when a score passes it by 2^8: weights up to 256
   // keep their relative precision in either type.
   if (__ballot(top > st.m + kAtSlack) != 0) {
     const float m = top > st.m + kAtSlack ? top : st.m;
     const float keep = m > st.m ? __builtin_amdgcn_exp2f(st.m - m) : 1.0f;
 #pragma unroll
-    for (int d = 0; d < DH / 32; ++d)
+    for (int d = 0; d < DH / NQ; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) st.o[d][r] *= keep;
+      for (int r = 0; r < R; ++r) st.o[d][r] *= keep;
     st.l *= keep;
     st.m = m;
     st.mref = m > -INFINITY ? m : 0.0f;
@@ -345,7 +418,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
 #pragma unroll
   for (int t = 0; t < NB; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
+    for (int r = 0; r < R; ++r) {
       s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], scale2, -st.mref));
       sum += s[t][r];
     }
@@ -365,22 +438,26 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
       }
     dirty = __ballot(bad);
   }
-  const int ls = lane & 15, vrow = 4 * h + (ls >> 2), vc = ((lane >> 4) & 1) * 2 + ((ls & 3) >> 1);
+  // a product takes 8 Z rows: two 4-row pieces of each lane, 4 Z rows apart
+  const int ls = lane & 15, vrow = 4 * z + (ls >> 2);
+  const int vc = (NQ == 32 ? ((lane >> 4) & 1) * 2 : 0) + ((ls & 3) >> 1);
   typedef __attribute__((address_space(3))) at_s16x4 lds_s16x4;
 #pragma unroll
-  for (int u = 0; u < KT / 16; ++u) {
+  for (int u = 0; u < KT / (8 * Z); ++u) {
     H w8[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w8[i] = (H)s[u >> 1][8 * (u & 1) + i];
+    for (int i = 0; i < 8; ++i)
+      w8[i] = NQ == 32 ? (H)s[u >> 1][8 * (u & 1) + i] : (H)s[2 * u + (i >> 2)][i & 3];
     const at_u32x4 pb = __builtin_bit_cast(at_u32x4, w8);
 #pragma unroll
-    for (int d = 0; d < DH / 32; ++d) {
-      const int at = vrow * ROW + attn_v_chunk<DH>(vrow, 4 * d + vc) * 16 + (ls & 1) * 8;
+    for (int d = 0; d < DH / NQ; ++d) {
+      const int at = vrow * ROW + attn_v_chunk<DH>(vrow, NQ / 8 * d + vc) * 16 + (ls & 1) * 8;
       struct {
         at_s16x4 lo, hi;
       } f;
-      f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (16 * u) * ROW + at));
-      f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (16 * u + 8) * ROW + at));
+      f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (8 * Z * u) * ROW + at));
+      f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(v + (8 * Z * u + 4 * Z) * ROW + at));
       at_u32x4 a = __builtin_bit_cast(at_u32x4, f);
       if (MASKED && dirty)
 #pragma unroll
@@ -393,28 +470,26 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     dirty &= dirty - 1;
     if (vis >> row & 1) {
 #pragma unroll
-      for (int d = 0; d < DH / 32; ++d) {
+      for (int j = 0; j < State::PIECES; ++j) {
+        const int e = State::element(j, lane);
+        const uint2 x =
+            *(const uint2*)(v + row * ROW + attn_v_chunk<DH>(row, e >> 3) * 16 + (e & 7) * 2);
+        // what is not finite, times any weight; 0 elsewhere
+        const uint32_t two[2] = {x.x ^ attn_finite_only<H>(x.x), x.y ^ attn_finite_only<H>(x.y)};
+        at_f32x4 o = st.get(j);
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const int e = 32 * d + 2 * r + 4 * h;
-          const uint2 x =
-              *(const uint2*)(v + row * ROW + attn_v_chunk<DH>(row, e >> 3) * 16 + (e & 7) * 2);
-          // what is not finite, times any weight; 0 elsewhere
-          const uint32_t two[2] = {x.x ^ attn_finite_only<H>(x.x), x.y ^ attn_finite_only<H>(x.y)};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            st.o[d][r + k] +=
-                (float)__builtin_bit_cast(H, (uint16_t)(two[k >> 1] >> (16 * (k & 1))));
-        }
-        asm volatile("" ::: "memory");  // a few elements at a time
+        for (int i = 0; i < 4; ++i)
+          o[i] += (float)__builtin_bit_cast(H, (uint16_t)(two[i >> 1] >> (16 * (i & 1))));
+        st.set(j, o);
+        if (j & 1) asm volatile("" ::: "memory");  // a few elements at a time
       }
     }
   }
 }
 
 // Takes another state of the same queries into this one.
-template <int DH>
-__device__ __forceinline__ void attn_join(AttnState<DH>& st, float m, float l,
+template <int DH, int NQ>
+__device__ __forceinline__ void attn_join(AttnState<DH, NQ>& st, float m, float l,
                                           const at_f32x4* o, int stride) {
   const float top = fmaxf(st.m, m);
   const float a = st.m > -INFINITY ? __builtin_amdgcn_exp2f(st.m - top) : 0.0f;
@@ -422,41 +497,53 @@ __device__ __forceinline__ void attn_join(AttnState<DH>& st, float m, float l,
   st.m = top;
   st.l = st.l * a + l * b;
 #pragma unroll
-  for (int d = 0; d < DH / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      const at_f32x4 x = o[(d * 4 + (r >> 2)) * stride];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st.o[d][r + e] = st.o[d][r + e] * a + x[e] * b;
-    }
+  for (int j = 0; j < AttnState<DH, NQ>::PIECES; ++j) st.set(j, st.get(j) * a + o[j * stride] * b);
 }
 
-// Query row `col` of unit u of request b: block row i and query head; false
-// past the last.
-__device__ __forceinline__ bool attn_query(const AttnParams& p, int u, int col, int& i, int& hq) {
-  const int head = u / p.MT;
-  i = col / p.G;
-  hq = head * p.G + (col - i * p.G);
-  return i < p.T;
+// The thread's number, not known to the compiler as one value: what is derived
+// from it for a piece's start or end is formed there, and not kept in
+// registers over the steps.
+__device__ __forceinline__ int attn_tid() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
 }
 
-template <typename H, int ND>
-__device__ __forceinline__ void attn_store(const AttnParams& p, int64_t row, int d0, float m,
-                                           float l, bool seen, const at_f32x16 (&o)[ND], int DH) {
-  const int h = (threadIdx.x & 63) >> 5;
-  const float inv = seen && l > 0.0f ? 1.0f / l : 0.0f;
-  const bool none = !seen || l == 0.0f;
+// A lane's query: a wave of unit u's query tile holds NQ consecutive query
+// rows of the unit's key/value head, query head by query head for each block row.
+struct AttnQuery {
+  int i, hq;  // block row and query head
+  bool live;  // it takes part
+};
+
+template <int NQ>
+__device__ __forceinline__ AttnQuery attn_query(const AttnParams& p, const AttnReq& r, int u, int wq,
+                                                int lane) {
+  const int head = u / r.tiles, tile = u - head * r.tiles;
+  const int w0 = tile * r.waves / r.tiles, w1 = (tile + 1) * r.waves / r.tiles;
+  const int col = (w0 + wq) * NQ + lane % NQ;
+  AttnQuery q;
+  q.i = col / p.G;
+  q.hq = head * p.G + (col - q.i * p.G);
+  q.live = w0 + wq < w1 && q.i < r.rows;
+  return q;
+}
+
+// Pieces [j0, j0 + NP) of an output row.
+template <typename H, int DH, int NQ, int NP>
+__device__ __forceinline__ void attn_store(const AttnParams& p, int64_t row, int j0, float m,
+                                           float l, const at_f32x4 (&o)[NP], int lane) {
+  const bool none = l == 0.0f;  // (a NaN stays one)
+  const float inv = none ? 0.0f : 1.0f / l;
   H* out = (H*)p.out + row * DH;
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
+  for (int j = 0; j < NP; ++j) {
+    H x[4];
 #pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      H x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = none ? (H)0.0f : (H)(o[d][r + e] * inv);
-      *(uint64_t*)(out + 32 * (d0 + d) + (r >> 2) * 8 + 4 * h) = __builtin_bit_cast(uint64_t, x);
-    }
-  if (p.lse && h == 0 && d0 == 0)
+    for (int e = 0; e < 4; ++e) x[e] = none ? (H)0.0f : (H)(o[j][e] * inv);
+    *(uint64_t*)(out + AttnState<DH, NQ>::element(j0 + j, lane)) = __builtin_bit_cast(uint64_t, x);
+  }
+  if (p.lse && lane < NQ && j0 == 0)
     p.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -473,42 +560,53 @@ __device__ __forceinline__ bool attn_mapped(const PagedRows& p, int b, int r0, i
   return !(s_any[0] | s_any[1] | s_any[2] | s_any[3]);
 }
 
-template <typename H, int DH, int QW>
-__global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(AttnParams p) {
-  using C = AttnTile<DH, QW>;
-  __shared__ __align__(256) unsigned char lds[C::LDS];
-  __shared__ int s_any[kAtWaves];
-  AttnWork w;
-  if (!attn_plan<C::TR>(p, w)) return;
-  const int tid = threadIdx.x, lane = tid & 63;
+// Clears the rows of request b that see nothing, for one key/value head.
+template <typename H, int DH>
+__device__ __forceinline__ void attn_clear(const AttnParams& p, int64_t b, int rows, int head) {
+  const int per = p.G * DH / 8;  // 16-byte pieces of a block row's heads
+  for (int k = threadIdx.x; k < (p.T - rows) * per; k += kAtThreads) {
+    const int row = k / per, c = k - row * per;
+    const int64_t at = ((b * p.T + rows + row) * p.q_heads + (int64_t)head * p.G) * DH + c * 8;
+    *(at_u32x4*)((H*)p.out + at) = at_u32x4{0, 0, 0, 0};
+  }
+  if (p.lse)
+    for (int k = threadIdx.x; k < (p.T - rows) * p.G; k += kAtThreads) {
+      const int row = k / p.G;
+      p.lse[(b * p.T + rows + row) * p.q_heads + head * p.G + (k - row * p.G)] = -INFINITY;
+    }
+}
+
+// Steps [t0, t1) of unit u of request b, into the output or workspace slot
+// `slot` (-1: the output).
+template <typename H, class C>
+__device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* lds, int* s_any,
+                                           int b, int u, const AttnReq& rq, int t0, int t1,
+                                           int slot) {
+  constexpr int DH = C::DH, NQ = C::NQ, QW = C::QW;
+  const int tid = attn_tid(), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = wave / QW, wq = wave % QW;
-  const int head = w.u / p.MT;
-  // this lane's query
-  const int col = ((w.u - head * p.MT) * QW + wq) * 32 + (lane & 31);
-  int i, hq;
-  const bool in = attn_query(p, w.u, col, i, hq);
-  const bool live = in && i <= w.nodes && w.past >= 0;
-  const bool busy = __ballot(live) != 0;  // waves past the last node only carry rows
-  at_u32x4 q[DH / 16];
+  const int head = u / rq.tiles;
+  const AttnQuery me = attn_query<NQ>(p, rq, u, wq, lane);
+  const int i = me.i;
+  const bool live = me.live;
+  const bool busy = __ballot(live) != 0;  // a wave without queries only carries rows
+  if (rq.len == 0) t1 = t0;
+  constexpr int NF = DH * NQ / 512;  // Q fragments of 16 bytes
+  at_u32x4 q[NF];
   {
-    const H* src = (const H*)p.q + (((int64_t)w.b * p.T + i) * p.q_heads + hq) * DH + (lane >> 5) * 8;
+    const H* src =
+        (const H*)p.q + (((int64_t)b * p.T + i) * p.q_heads + me.hq) * DH + lane / NQ * 8;
 #pragma unroll
-    for (int c = 0; c < DH / 16; ++c)
-      q[c] = live ? *(const at_u32x4*)(src + 16 * c) : at_u32x4{0, 0, 0, 0};
+    for (int c = 0; c < NF; ++c)
+      q[c] = live ? *(const at_u32x4*)(src + DH / NF * c) : at_u32x4{0, 0, 0, 0};
   }
-  AttnState<DH> st;
+  AttnState<DH, NQ> st;
   st.m = -INFINITY;
   st.mref = st.l = 0.0f;
 #pragma unroll
-  for (int d = 0; d < DH / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) st.o[d][r] = 0.0f;
+  for (int j = 0; j < C::PIECES; ++j) st.set(j, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 
-  // the piece's steps [t0, t1); those before tm see every row they hold
-  const int each = (w.steps + w.splits - 1) / w.splits;
-  const int t0 = w.piece * each;
-  const int t1 = w.len == 0 ? t0 : (t0 + each < w.steps ? t0 + each : w.steps);
   // this thread's chunks of a tile: row ld_row + k * STEP, chunk ld_c
   constexpr int STEP = QW * kWave / C::CPR;
   const int gt = wq * kWave + lane, ld_row = gt / C::CPR, ld_c = gt % C::CPR;
@@ -520,11 +618,11 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
   const H* const v0 = (const H*)p.v_cache + (int64_t)head * p.rows.page_size * DH + ld_c * 8;
   auto row_of = [&](int t, int k) {  // the cache row that chunk k is of, clamped into the request
     const int r = t * C::TR + g * C::KT + ld_row + k * STEP;
-    return r < w.len ? r : w.len - 1;
+    return r < rq.len ? r : rq.len - 1;
   };
   auto find = [&](int t) {
 #pragma unroll
-    for (int k = 0; k < C::LOADS; ++k) page[k] = page_of(p.rows, w.b, row_of(t, k));
+    for (int k = 0; k < C::LOADS; ++k) page[k] = page_of(p.rows, b, row_of(t, k));
   };
   auto fetch = [&](int t) {
 #pragma unroll
@@ -537,17 +635,19 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
       vr[k] = *(const at_u32x4*)(v0 + at);
     }
   };
+  // steps before tm see every row they hold
   int tm = t0;
   if (t0 < t1) {
     find(t0);
     fetch(t0);
     if (t0 + 1 < t1) find(t0 + 1);
-    const int end = t1 * C::TR < w.len ? t1 * C::TR : w.len;
-    if (attn_mapped(p.rows, w.b, t0 * C::TR, end, s_any)) {
-      tm = w.past / C::TR;
+    const int end = t1 * C::TR < rq.len ? t1 * C::TR : rq.len;
+    if (attn_mapped(p.rows, b, t0 * C::TR, end, s_any)) {
+      tm = rq.past / C::TR;
       tm = tm < t0 ? t0 : (tm > t1 ? t1 : tm);
     }
   }
+  __syncthreads();  // the piece before is done with the LDS
   auto step = [&](int t, auto is_masked) {
     constexpr bool MASKED = decltype(is_masked)::value;
     unsigned char* const kt = tiles + (C::NBUF == 2 ? (t & 1) * 2 * C::TILE : 0);
@@ -570,14 +670,14 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
       if (t + 2 < t1) find(t + 2);
     }
     const int r0 = t * C::TR + g * C::KT;
-    if (busy && (!MASKED || r0 < w.len)) {
+    if (busy && (!MASKED || r0 < rq.len)) {
       uint64_t vis = 0;
       if (MASKED) {
         const int r = r0 + lane;
-        const bool held = lane < C::KT && r < w.len && page_of(p.rows, w.b, r) >= 0;
-        vis = attn_visible<C::KT>(p, w, r0, i, live, __ballot(held));
+        const bool held = lane < C::KT && r < rq.len && page_of(p.rows, b, r) >= 0;
+        vis = attn_visible<C::KT>(p, b, rq.past, r0, i, live, __ballot(held));
       }
-      attn_tile<H, DH, C::KT, MASKED>(kt, vt, q, p.scale2, vis, st);
+      attn_tile<H, DH, NQ, C::KT, MASKED>(kt, vt, q, p.scale2, vis, st, lane);
     }
     if (QW == 1) {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -588,83 +688,122 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
   int t = t0;
   for (; t < tm; ++t) step(t, AttnFalse{});
   for (; t < t1; ++t) step(t, AttnTrue{});
-  st.l = attn_sum_halves(st.l);
+  st.l = attn_sum_across<NQ>(st.l);
+  const int out_lane = attn_tid() & 63;
 
   // merge the groups
   if constexpr (C::NG > 1) {
-    constexpr int BLOCK = C::OQ * kWave * 16 + kWave * 8;  // bytes of a wave's state
+    constexpr int BLOCK = C::PIECES * kWave * 16 + kWave * 8;  // bytes of a wave's state
     static_assert(C::NG / 2 * QW * BLOCK <= C::LDS, "states fit the tiles' LDS");
 #pragma unroll
     for (int half = C::NG / 2; half >= 1; half /= 2) {
       __syncthreads();
       unsigned char* at = lds + ((g >= half ? g - half : g) * QW + wq) * BLOCK;
-      at_f32x4* o = (at_f32x4*)at + lane;
-      float* ml = (float*)(at + C::OQ * kWave * 16) + 2 * lane;
+      at_f32x4* o = (at_f32x4*)at + out_lane;
+      float* ml = (float*)(at + C::PIECES * kWave * 16) + 2 * out_lane;
       if (g >= half && g < 2 * half) {
 #pragma unroll
-        for (int d = 0; d < DH / 32; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; r += 4)
-            o[(d * 4 + (r >> 2)) * kWave] =
-                at_f32x4{st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
+        for (int j = 0; j < C::PIECES; ++j) o[j * kWave] = st.get(j);
         ml[0] = st.m;
         ml[1] = st.l;
       }
       __syncthreads();
-      if (g < half) attn_join<DH>(st, ml[0], ml[1], o, kWave);
+      if (g < half) attn_join<DH, NQ>(st, ml[0], ml[1], o, kWave);
     }
     if (g > 0) return;
   }
-  if (w.slot < 0) {
-    if (in)
-      attn_store<H, DH / 32>(p, ((int64_t)w.b * p.T + i) * p.q_heads + hq, 0, st.m, st.l, live, st.o,
-                             DH);
+  at_f32x4 o[C::PIECES];
+#pragma unroll
+  for (int j = 0; j < C::PIECES; ++j) o[j] = st.get(j);
+  if (slot < 0) {
+    const AttnQuery to = attn_query<NQ>(p, rq, u, wq, out_lane);
+    if (to.live)
+      attn_store<H, DH, NQ>(p, ((int64_t)b * p.T + to.i) * p.q_heads + to.hq, 0, st.m, st.l, o,
+                            out_lane);
     return;
   }
-  at_f32x4* o = (at_f32x4*)p.part + ((int64_t)w.slot * QW + wq) * C::OQ * kWave + lane;
+  at_f32x4* part = (at_f32x4*)p.part + ((int64_t)slot * QW + wq) * C::PIECES * kWave + out_lane;
 #pragma unroll
-  for (int d = 0; d < DH / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; r += 4)
-      o[(d * 4 + (r >> 2)) * kWave] =
-          at_f32x4{st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
-  float* ml = p.part_ml + (((int64_t)w.slot * QW + wq) * kWave + lane) * 2;
+  for (int j = 0; j < C::PIECES; ++j) part[j * kWave] = o[j];
+  float* ml = p.part_ml + (((int64_t)slot * QW + wq) * kWave + out_lane) * 2;
   ml[0] = st.m;
   ml[1] = st.l;
 }
 
-// Merges the pieces of split requests: a wave per 32 queries and 32 elements
-// of the head.
-template <typename H, int DH, int QW>
-__global__ __launch_bounds__(DH * 2) void attn_merge_kernel(AttnParams p) {
-  const int units = p.kv_heads * p.MT;
-  const int id = (int)blockIdx.x;  // split request, unit, query wave
-  const int wq = id % QW, k = id / QW / units, u = id / QW - k * units;
-  if (k >= p.place[0].count) return;
-  const AttnPlace pl = p.place[k];
-  const int b = pl.b;
-  int past, nodes, len;
-  attn_lengths(p, b, past, nodes, len);
-  const int lane = threadIdx.x & 63, d = threadIdx.x >> 6;
-  const int col = ((u - u / p.MT * p.MT) * QW + wq) * 32 + (lane & 31);
-  int i, hq;
-  const bool in = attn_query(p, u, col, i, hq);
-  const bool live = in && i <= nodes;
-  constexpr int OQ = AttnTile<DH, QW>::OQ;
-  AttnState<32> st;
-  st.m = -INFINITY;
-  st.mref = st.l = 0.0f;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) st.o[0][r] = 0.0f;
-  if (__ballot(live))
-    for (int s = 0; s < pl.splits; ++s) {
-      const int64_t at = ((int64_t)pl.slot + (int64_t)s * units + u) * QW + wq;
-      const float* ml = p.part_ml + (at * kWave + lane) * 2;
-      attn_join<32>(st, ml[0], ml[1], (const at_f32x4*)p.part + (at * OQ + d * 4) * kWave + lane,
-                    kWave);
+template <typename H, int DH, int NQ, int QW>
+__global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(AttnParams p) {
+  using C = AttnTile<DH, NQ, QW>;
+  __shared__ __align__(256) unsigned char lds[C::LDS];
+  __shared__ int s_any[kAtWaves];
+  AttnPos at, to;
+  const int id = (int)blockIdx.x;
+  AttnPlace mark{-1, 0, 0, 0};
+  int k = id;
+  if (attn_plan<C>(p, id, k, at, to)) {
+    AttnReq rq = attn_request<C>(p, at.b);
+    while (at.x < to.x) {  // uniform
+      if (at.u == rq.tiles * p.kv_heads) {  // on to the next request
+        ++at.b;
+        at.u = 0;
+        rq = attn_request<C>(p, at.b);
+      }
+      const int64_t left = to.x - at.x;
+      const int t1 = at.s + left < rq.steps ? at.s + (int)left : rq.steps;
+      const bool ends = t1 == rq.steps, begins = at.s == 0;
+      if (begins && !ends) {
+        mark.b = at.b;
+        mark.u = at.u;
+      } else if (ends && !begins) {
+        mark.ends = 1;
+      }
+      attn_piece<H, C>(p, lds, s_any, at.b, at.u, rq, at.s, t1,
+                       begins && ends ? -1 : 2 * k + (begins ? 1 : 0));
+      if (ends && (at.u + 1) % rq.tiles == 0 && rq.rows < p.T)
+        attn_clear<H, DH>(p, at.b, rq.rows, at.u / rq.tiles);
+      at.x += t1 - at.s;
+      at.s = 0;
+      ++at.u;
     }
-  if (in)
-    attn_store<H, 1>(p, ((int64_t)b * p.T + i) * p.q_heads + hq, d, st.m, st.l, live, st.o, DH);
+  }
+  if (threadIdx.x == 0) p.place[k] = mark;
+}
+
+// Merges the pieces of the unit that a workgroup's stretch began and did not
+// end: a wave per two 4-float pieces of a query wave's state.
+template <typename H, int DH, int NQ, int QW>
+__global__ __launch_bounds__(DH * NQ / 8) void attn_merge_kernel(AttnParams p) {
+  using C = AttnTile<DH, NQ, QW>;
+  const int wq = (int)(blockIdx.x % QW), k = (int)(blockIdx.x / QW);
+  const AttnPlace pl = p.place[k];
+  if (pl.b < 0) return;
+  const AttnReq rq = attn_request<C>(p, pl.b);
+  const int lane = threadIdx.x & 63, j0 = 2 * (threadIdx.x >> 6);
+  const AttnQuery me = attn_query<NQ>(p, rq, pl.u, wq, lane);
+  if (!__ballot(me.live)) return;
+  // pieces: slot 2 k + 1, then 2 (k + 1), 2 (k + 2), ... up to the one that ends
+  int n = 1;
+  while (k + n < p.groups - 1 && !p.place[k + n].ends) ++n;
+  ++n;
+  auto slot = [&](int s) -> int64_t {
+    return (int64_t)(s == 0 ? 2 * k + 1 : 2 * (k + s)) * QW + wq;
+  };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) m = fmaxf(m, p.part_ml[(slot(s) * kWave + lane) * 2]);
+  float l = 0.0f;
+  at_f32x4 o[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const int64_t at = slot(s);
+    const float* ml = p.part_ml + (at * kWave + lane) * 2;
+    const float a = ml[0] > -INFINITY ? __builtin_amdgcn_exp2f(ml[0] - m) : 0.0f;
+    l += ml[1] * a;
+    const at_f32x4* part = (const at_f32x4*)p.part + (at * C::PIECES + j0) * kWave + lane;
+    o[0] += part[0] * a;
+    o[1] += part[kWave] * a;
+  }
+  if (me.live)
+    attn_store<H, DH, NQ>(p, ((int64_t)pl.b * p.T + me.i) * p.q_heads + me.hq, j0, m, l, o, lane);
 }
 
 }  // namespace ddt

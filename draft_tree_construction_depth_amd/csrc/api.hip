@@ -1000,7 +1000,9 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   if (chk2 == DDT_EINVAL) return chk2;
   if (chk != DDT_OK || chk2 != DDT_OK) return DDT_ENOTSUP;
   const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap);
-  if (ap.rows.cap > (1 << 27)) return DDT_ENOTSUP;  // the plan counts steps in 32 bits
+  if (ap.rows.cap > (1 << 27) ||  // the plan counts steps in 32 bits
+      (page_table && (int64_t)kv_heads * page_size > (((int64_t)1 << 32) - 1) / (2 * head_dim)))
+    return DDT_ENOTSUP;  // ... and a page's bytes are addressed in 32
   if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
   ap.q = q;
   ap.k_cache = k_cache;

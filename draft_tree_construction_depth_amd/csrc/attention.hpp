@@ -376,11 +376,20 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
 #pragma unroll
     for (int r = 0; r < R; ++r) s[t][r] = 0.0f;
     const int row = NQ * t + lane % NQ;
+    at_u32x4 a[CPR / Z];
 #pragma unroll
-    for (int c = 0; c < CPR / Z; ++c) {
-      const at_u32x4 a = *(const at_u32x4*)(k + row * ROW + attn_k_chunk<DH>(row, Z * c + z) * 16);
-      s[t] = attn_mfma<H>(a, q[c], s[t]);
-    }
+    for (int c = 0; c < CPR / Z; ++c)
+      a[c] = *(const at_u32x4*)(k + row * ROW + attn_k_chunk<DH>(row, Z * c + z) * 16);
+#pragma unroll
+    for (int c = 0; c < CPR / Z; ++c) s[t] = attn_mfma<H>(a[c], q[c], s[t]);
+  }
+  // four fragments' reads ahead of the products
+  constexpr int kF = NB * CPR / Z, kAhead = 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+  for (int c = 0; c < kF; ++c) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (c + kAhead < kF) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
   // s[t][r] is row NQ t + 4 Z (r / 4) + 4 z + r % 4
   if (MASKED) {
@@ -395,6 +404,24 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
       }
     }
   }
+  // V^T fragments: product c = D u + d takes rows [8 Z u, 8 Z u + 8 Z), in
+  // two 4-row pieces of each lane, 4 Z rows apart, and head elements [NQ d,
+  // NQ d + NQ). Two are read ahead of the products, the first two here.
+  constexpr int U = KT / (8 * Z), D = DH / NQ;
+  const int ls = lane & 15, vrow = 4 * z + (ls >> 2);
+  const int vc = (NQ == 32 ? ((lane >> 4) & 1) * 2 : 0) + ((ls & 3) >> 1);
+  auto fragment = [&](int c) -> at_u32x4 {
+    typedef __attribute__((address_space(3))) at_s16x4 lds_s16x4;
+    const int u = c / D, d = c % D;
+    const int at = vrow * ROW + attn_v_chunk<DH>(vrow, NQ / 8 * d + vc) * 16 + (ls & 1) * 8;
+    struct {
+      at_s16x4 lo, hi;
+    } f;
+    f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (8 * Z * u) * ROW + at));
+    f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (8 * Z * u + 4 * Z) * ROW + at));
+    return __builtin_bit_cast(at_u32x4, f);
+  };
+  at_u32x4 f[3] = {fragment(0), fragment(1), {0, 0, 0, 0}};
   float top = s[0][0];
 #pragma unroll
   for (int t = 0; t < NB; ++t)
@@ -407,22 +434,13 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     const float m = top > st.m + kAtSlack ? top : st.m;
     const float keep = m > st.m ? __builtin_amdgcn_exp2f(st.m - m) : 1.0f;
 #pragma unroll
-    for (int d = 0; d < DH / NQ; ++d)
+    for (int d = 0; d < D; ++d)
 #pragma unroll
       for (int r = 0; r < R; ++r) st.o[d][r] *= keep;
     st.l *= keep;
     st.m = m;
     st.mref = m > -INFINITY ? m : 0.0f;
   }
-  float sum = 0.0f;
-#pragma unroll
-  for (int t = 0; t < NB; ++t)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], scale2, -st.mref));
-      sum += s[t][r];
-    }
-  st.l += sum;
   // Rows that a query does not see have weight 0, but 0 times a NaN or an
   // infinity among their values is no 0: such values (garbage behind the
   // block, on unmapped pages, or in other nodes' rows) are taken out of the
@@ -438,33 +456,43 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
       }
     dirty = __ballot(bad);
   }
-  // a product takes 8 Z rows: two 4-row pieces of each lane, 4 Z rows apart
-  const int ls = lane & 15, vrow = 4 * z + (ls >> 2);
-  const int vc = (NQ == 32 ? ((lane >> 4) & 1) * 2 : 0) + ((ls & 3) >> 1);
-  typedef __attribute__((address_space(3))) at_s16x4 lds_s16x4;
+  // weight i (0..7) of the rows of product group u
+  auto score = [&](int u, int i) -> float {
+    return NQ == 32 ? s[u >> 1][(8 * (u & 1) + i) % R] : s[NQ == 32 ? 0 : 2 * u + (i >> 2)][i & 3];
+  };
+  float sum[2] = {0.0f, 0.0f};
+  auto weigh = [&](int u, int i) {
+    const float w = __builtin_amdgcn_exp2f(fmaf(score(u, i), scale2, -st.mref));
+    if (NQ == 32)
+      s[u >> 1][(8 * (u & 1) + i) % R] = w;
+    else
+      s[NQ == 32 ? 0 : 2 * u + (i >> 2)][i & 3] = w;
+    sum[i & 1] += w;
+  };
 #pragma unroll
-  for (int u = 0; u < KT / (8 * Z); ++u) {
-    H w8[8];
+  for (int i = 0; i < 8; ++i) weigh(0, i);
+  at_u32x4 pb;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w8[i] = NQ == 32 ? (H)s[u >> 1][8 * (u & 1) + i] : (H)s[2 * u + (i >> 2)][i & 3];
-    const at_u32x4 pb = __builtin_bit_cast(at_u32x4, w8);
+  for (int c = 0; c < U * D; ++c) {
+    const int u = c / D, d = c % D;
+    if (d == 0) {
+      H w8[8];
 #pragma unroll
-    for (int d = 0; d < DH / NQ; ++d) {
-      const int at = vrow * ROW + attn_v_chunk<DH>(vrow, NQ / 8 * d + vc) * 16 + (ls & 1) * 8;
-      struct {
-        at_s16x4 lo, hi;
-      } f;
-      f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (8 * Z * u) * ROW + at));
-      f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4*)(v + (8 * Z * u + 4 * Z) * ROW + at));
-      at_u32x4 a = __builtin_bit_cast(at_u32x4, f);
-      if (MASKED && dirty)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = attn_finite_only<H>(a[i]);
-      st.o[d] = attn_mfma<H>(a, pb, st.o[d]);
+      for (int i = 0; i < 8; ++i) w8[i] = (H)score(u, i);
+      pb = __builtin_bit_cast(at_u32x4, w8);
     }
+    if (MASKED && dirty)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[c % 3][i] = attn_finite_only<H>(f[c % 3][i]);
+    st.o[d] = attn_mfma<H>(f[c % 3], pb, st.o[d]);
+    if (c + 2 < U * D) f[(c + 2) % 3] = fragment(c + 2);
+    // between the products: the exponentials of the next group
+    if (u + 1 < U)
+#pragma unroll
+      for (int i = 8 * d / D; i < 8 * (d + 1) / D; ++i) weigh(u + 1, i);
+    __builtin_amdgcn_sched_barrier(0);
   }
+  st.l += sum[0] + sum[1];
   while (MASKED && dirty) {  // uniform
     const int row = __builtin_ctzll(dirty);
     dirty &= dirty - 1;
@@ -612,25 +640,37 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   const int gt = wq * kWave + lane, ld_row = gt / C::CPR, ld_c = gt % C::CPR;
   unsigned char* const tiles = lds + g * C::NBUF * 2 * C::TILE;
   at_u32x4 kr[C::LOADS], vr[C::LOADS];
+  // the entries of the next tile's pages, as read: a test here would wait for
+  // them, and with them for the tile in flight
   int page[C::LOADS];
-  const int64_t page_rows = (int64_t)p.kv_heads * p.rows.page_size;
-  const H* const k0 = (const H*)p.k_cache + (int64_t)head * p.rows.page_size * DH + ld_c * 8;
-  const H* const v0 = (const H*)p.v_cache + (int64_t)head * p.rows.page_size * DH + ld_c * 8;
+  const bool paged = p.rows.table != nullptr;
+  const int32_t* const table = p.rows.table + (int64_t)b * p.rows.width;
+  const uint32_t page_bytes = (uint32_t)p.kv_heads * (uint32_t)p.rows.page_size * C::ROW;
+  const int row_mask = paged ? p.rows.page_size - 1 : 0x7FFFFFFF;
+  const int64_t base =
+      ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size * C::ROW + ld_c * 16;
+  const char* const k0 = (const char*)p.k_cache + base;
+  const char* const v0 = (const char*)p.v_cache + base;
   auto row_of = [&](int t, int k) {  // the cache row that chunk k is of, clamped into the request
     const int r = t * C::TR + g * C::KT + ld_row + k * STEP;
     return r < rq.len ? r : rq.len - 1;
   };
   auto find = [&](int t) {
+    if (paged) {
 #pragma unroll
-    for (int k = 0; k < C::LOADS; ++k) page[k] = page_of(p.rows, b, row_of(t, k));
+      for (int k = 0; k < C::LOADS; ++k) page[k] = table[row_of(t, k) >> p.rows.shift];
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::LOADS; ++k) page[k] = 0;
+    }
   };
   auto fetch = [&](int t) {
 #pragma unroll
     for (int k = 0; k < C::LOADS; ++k) {
       // rows on no page: some row's values, taken out by the mask
-      const int64_t pg = page[k] < 0 ? 0 : page[k];
-      const int rp = page[k] < 0 ? 0 : row_in_page(p.rows, row_of(t, k));
-      const int64_t at = (pg * page_rows + rp) * DH;
+      const uint32_t pg = (uint32_t)page[k] < (uint32_t)p.rows.pages ? page[k] : 0;
+      const uint64_t at = (uint64_t)pg * page_bytes +
+                          (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW;
       kr[k] = *(const at_u32x4*)(k0 + at);
       vr[k] = *(const at_u32x4*)(v0 + at);
     }

@@ -306,7 +306,8 @@ int ddtree_append_kv(const void* q, const void* k, const void* v, int dtype, int
  * dtype for its product with V.
  * Supported: head_dim 64, 128 or 256, q_heads a multiple of kv_heads
  * (DDT_EINVAL otherwise), T <= DDT_MAX_B + 1, 0 < scale < inf (DDT_EINVAL),
- * at most 2^27 cache rows per request (table_width * page_size).
+ * at most 2^27 cache rows per request (table_width * page_size), pages of a
+ * layer below 4 GiB.
  * The workspace (ddtree_attention_workspace_size bytes, no zero-fill needed;
  * pages_per_request = table_width, or 1 without a table) holds partial
  * results of long caches split over workgroups.

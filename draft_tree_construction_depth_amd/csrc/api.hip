@@ -482,7 +482,7 @@ void launch_append(const ddt::AppendParams& ap, int64_t blocks, int interleaved,
 // ---- attention: waves along the queries, workgroups, workspace -------------------
 struct AttnPlan {
   int NQ, QW;  // queries of a wave, waves side by side
-  int64_t groups, least;
+  int64_t groups, least, grid;
   bool merge;  // a unit can be cut
   size_t part, ml, end;
 };
@@ -509,6 +509,9 @@ AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_he
                            : batch * kv_heads * tiles * steps;
   const int64_t want = ((axis + pl.least - 1) / pl.least + 7) & ~(int64_t)7;
   if (want < pl.groups) pl.groups = want;
+  // or one for each unit, where there are many (attn_plan decides)
+  const int64_t units = (batch * kv_heads * tiles + 7) & ~(int64_t)7;
+  pl.grid = units >= 2 * pl.groups ? units : pl.groups;
   pl.merge = steps > 1;
   const int64_t slots = pl.merge ? 2 * pl.groups : 0;
   size_t o = align_up((size_t)pl.groups * sizeof(ddt::AttnPlace));
@@ -522,7 +525,7 @@ AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_he
 
 template <typename H, int DH, int NQ, int QW>
 int launch_attn_tile(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
-  hipLaunchKernelGGL((ddt::attn_kernel<H, DH, NQ, QW>), dim3((unsigned)pl.groups),
+  hipLaunchKernelGGL((ddt::attn_kernel<H, DH, NQ, QW>), dim3((unsigned)pl.grid),
                      dim3(ddt::kAtThreads), 0, st, ap);
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   if (!pl.merge) return DDT_OK;

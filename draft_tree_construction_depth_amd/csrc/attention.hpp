@@ -142,47 +142,78 @@ __device__ __forceinline__ AttnPos attn_uniform(const AttnPos& a) {
       __builtin_amdgcn_readfirstlane(a.s)};
 }
 
-// The stretch [from, to) of workgroup w of `groups`; false: none. The axis is
-// request after request, each tiles * kv_heads units of `steps`. An end that
-// falls close to a unit's is moved there (by up to an eighth of a stretch), so
-// that short units are not cut at all.
+// The stretch [from, to) of workgroup w; false: none. The axis is request
+// after request, each tiles * kv_heads units of `steps`, cut evenly for the
+// p.groups workgroups that the card holds at once. An end that falls close to
+// a unit's is moved there: by up to an eighth of a stretch, so that short
+// units are not cut at all, or, where a stretch is a few steps, by up to half
+// of one, so that no stretch has the start of two units to wait for.
+//
+// With many units, none of them long, each workgroup takes a whole one (to.x
+// < 0): the units' cache rows are then read by a key/value head's query tiles
+// at the same time, and the hardware deals the units out as they end.
 template <class C>
 __device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnPos& from, AttnPos& to) {
-  __shared__ int64_t s_part[kAtWaves];
+  __shared__ int64_t s_part[kAtWaves][2];
+  __shared__ int s_long[kAtWaves];
   __shared__ AttnPos s_pos[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  auto axis = [&](int64_t b) -> int64_t {
-    if (b >= p.batch) return 0;
+  auto axis = [&](int64_t b, int64_t& units, int& steps) {
+    units = 0;
+    steps = 0;
+    if (b >= p.batch) return;
     const AttnReq r = attn_request<C>(p, b);
-    return (int64_t)r.tiles * p.kv_heads * r.steps;
+    units = (int64_t)r.tiles * p.kv_heads;
+    steps = r.steps;
   };
-  int64_t total = 0;
+  int64_t total = 0, all_units = 0, units;
+  int longest = 0, steps;
   if (p.batch == 1) {
-    total = axis(0);
+    axis(0, all_units, longest);
+    total = all_units * longest;
   } else {
-    int64_t sum = 0;
-    for (int64_t b = tid; b < p.batch; b += kAtThreads) sum += axis(b);
-    sum = attn_wave_scan(sum);
-    if (lane == 63) s_part[wave] = sum;
+    for (int64_t b = tid; b < p.batch; b += kAtThreads) {
+      axis(b, units, steps);
+      total += units * steps;
+      all_units += units;
+      longest = steps > longest ? steps : longest;
+    }
+    total = attn_wave_scan(total);
+    all_units = attn_wave_scan(all_units);
+    longest = wave_max(longest);
+    if (lane == 63) {
+      s_part[wave][0] = total;
+      s_part[wave][1] = all_units;
+      s_long[wave] = longest;
+    }
     __syncthreads();
+    total = all_units = 0;
 #pragma unroll
-    for (int i = 0; i < kAtWaves; ++i) total += s_part[i];
+    for (int i = 0; i < kAtWaves; ++i) {
+      total += s_part[i][0];
+      all_units += s_part[i][1];
+      longest = s_long[i] > longest ? s_long[i] : longest;
+    }
   }
+  const bool whole = all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
   const int64_t want = (total + p.least - 1) / p.least;
-  const int n = want < p.groups ? (int)want : p.groups;
+  const int64_t n = whole ? all_units : (want < p.groups ? want : p.groups);
   // consecutive workgroups of one XCD (ids 8 apart) take consecutive
   // stretches: query tiles of one unit read its rows from one L2
-  const int per = (n + 7) >> 3;
-  if ((w >> 3) >= per) {  // the ids left over take the numbers from 8 per on
-    k = w;
-    return false;
-  }
-  k = (w & 7) * per + (w >> 3);
+  const int64_t per = (n + 7) >> 3;
+  k = w;
+  if ((w >> 3) >= per) return false;  // (these keep their numbers: those from 8 per on)
+  k = (int)((w & 7) * per) + (w >> 3);
   if (k >= n) return false;
-  const int64_t slack = (total / n) >> 3;
+  const int64_t range = total / n;
+  const int64_t slack = range < 8 ? range >> 1 : range >> 3;
   // end number e of the stretches, as a position in the request that holds it
   auto place = [&](int64_t e, int64_t before, int b, AttnPos& at) {
     const AttnReq r = attn_request<C>(p, b);
+    if (whole) {
+      at = AttnPos{-1, b, (int)(e - before), 0};
+      return;
+    }
     const int64_t x = total * e / n - before;
     int64_t u = x / r.steps, s = x - u * r.steps;
     if (e > 0 && e < n) {
@@ -199,19 +230,21 @@ __device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnPos& from, Att
     place(k, 0, 0, from);
     place(k + 1, 0, 0, to);
   } else {
-    const int64_t x0 = total * k / n, x1 = total * (k + 1) / n;
+    const int64_t x0 = whole ? k : total * k / n, x1 = whole ? k + 1 : total * (k + 1) / n;
     int64_t base = 0;
     for (int64_t b0 = 0; b0 < p.batch; b0 += kAtThreads) {
-      const int64_t b = b0 + tid, mine = axis(b);
+      const int64_t b = b0 + tid;
+      axis(b, units, steps);
+      const int64_t mine = whole ? units : units * steps;
       int64_t incl = attn_wave_scan(mine);
       __syncthreads();  // s_part's readers before this round
-      if (lane == 63) s_part[wave] = incl;
+      if (lane == 63) s_part[wave][0] = incl;
       __syncthreads();
       int64_t all = 0;
 #pragma unroll
       for (int i = 0; i < kAtWaves; ++i) {
-        incl += i < wave ? s_part[i] : 0;
-        all += s_part[i];
+        incl += i < wave ? s_part[i][0] : 0;
+        all += s_part[i][0];
       }
       const int64_t before = base + incl - mine;
       if (x0 >= before && x0 < before + mine) place(k, before, (int)b, s_pos[0]);
@@ -780,14 +813,16 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
   AttnPlace mark{-1, 0, 0, 0};
   int k = id;
   if (attn_plan<C>(p, id, k, at, to)) {
+    const bool whole = to.x < 0;
     AttnReq rq = attn_request<C>(p, at.b);
-    while (at.x < to.x) {  // uniform
+    do {  // uniform; no stretch is empty but for ends moved onto one another
+      if (!whole && at.x >= to.x) break;
       if (at.u == rq.tiles * p.kv_heads) {  // on to the next request
         ++at.b;
         at.u = 0;
         rq = attn_request<C>(p, at.b);
       }
-      const int64_t left = to.x - at.x;
+      const int64_t left = whole ? rq.steps : to.x - at.x;
       const int t1 = at.s + left < rq.steps ? at.s + (int)left : rq.steps;
       const bool ends = t1 == rq.steps, begins = at.s == 0;
       if (begins && !ends) {
@@ -803,9 +838,9 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
       at.x += t1 - at.s;
       at.s = 0;
       ++at.u;
-    }
+    } while (!whole);
   }
-  if (threadIdx.x == 0) p.place[k] = mark;
+  if (threadIdx.x == 0 && k < p.groups) p.place[k] = mark;
 }
 
 // Merges the pieces of the unit that a workgroup's stretch began and did not

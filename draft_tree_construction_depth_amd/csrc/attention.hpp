@@ -65,10 +65,13 @@ struct AttnTile {
 };
 
 // What a workgroup's stretch leaves to merge: the unit that it begins and does
-// not end (slot 2 w + 1; b < 0: none), and whether its first piece (slot 2 w),
-// the continuation of the unit before, ends that unit.
+// not end (pieces 0: none), whose first piece is in slot 2 w + 1 and the others
+// in 2 (w + 1), 2 (w + 2), ..., the continuations with which the next stretches
+// begin.
 struct AttnPlace {
-  int32_t b, u, ends, pad;
+  int32_t pieces, b, u;
+  int32_t rows, waves, tiles;  // of AttnReq
+  int32_t pad[2];
 };
 
 struct AttnParams {
@@ -133,6 +136,11 @@ struct AttnPos {
   int b, u, s;
 };
 
+// The cut of the axis: end e of n stretches lies at total * e / n.
+struct AttnCut {
+  int64_t n, total, range, extra, slack;
+};
+
 __device__ __forceinline__ AttnPos attn_uniform(const AttnPos& a) {
   const uint64_t x = (uint64_t)a.x;
   return AttnPos{
@@ -140,6 +148,23 @@ __device__ __forceinline__ AttnPos attn_uniform(const AttnPos& a) {
                 (uint32_t)__builtin_amdgcn_readfirstlane((int)x)),
       __builtin_amdgcn_readfirstlane(a.b), __builtin_amdgcn_readfirstlane(a.u),
       __builtin_amdgcn_readfirstlane(a.s)};
+}
+
+// a / b for a >= 0, b > 0: a 64-bit division is some 130 instructions and
+// hardly ever needed.
+__device__ __forceinline__ int64_t attn_div(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+__device__ __forceinline__ int64_t attn_end(const AttnCut& c, int64_t e) {
+  return c.range * e + attn_div(c.extra * e, c.n);
+}
+
+// Step s of a unit's `steps` as the end of a stretch: 0 or `steps` where that
+// is near.
+__device__ __forceinline__ int64_t attn_near(const AttnCut& c, int64_t s, int steps) {
+  if (s <= c.slack && s <= steps - s) return 0;
+  return steps - s <= c.slack ? steps : s;
 }
 
 // The stretch [from, to) of workgroup w; false: none. The axis is request
@@ -153,7 +178,8 @@ __device__ __forceinline__ AttnPos attn_uniform(const AttnPos& a) {
 // < 0): the units' cache rows are then read by a key/value head's query tiles
 // at the same time, and the hardware deals the units out as they end.
 template <class C>
-__device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnPos& from, AttnPos& to) {
+__device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnCut& cut, AttnPos& from,
+                          AttnPos& to) {
   __shared__ int64_t s_part[kAtWaves][2];
   __shared__ int s_long[kAtWaves];
   __shared__ AttnPos s_pos[2];
@@ -196,7 +222,7 @@ __device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnPos& from, Att
     }
   }
   const bool whole = all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
-  const int64_t want = (total + p.least - 1) / p.least;
+  const int64_t want = attn_div(total + p.least - 1, p.least);
   const int64_t n = whole ? all_units : (want < p.groups ? want : p.groups);
   // consecutive workgroups of one XCD (ids 8 apart) take consecutive
   // stretches: query tiles of one unit read its rows from one L2
@@ -205,32 +231,32 @@ __device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnPos& from, Att
   if ((w >> 3) >= per) return false;  // (these keep their numbers: those from 8 per on)
   k = (int)((w & 7) * per) + (w >> 3);
   if (k >= n) return false;
-  const int64_t range = total / n;
-  const int64_t slack = range < 8 ? range >> 1 : range >> 3;
+  cut.n = n;
+  cut.total = total;
+  cut.range = attn_div(total, n);
+  cut.extra = total - cut.range * n;
+  cut.slack = cut.range < 8 ? cut.range >> 1 : cut.range >> 3;
   // end number e of the stretches, as a position in the request that holds it
   auto place = [&](int64_t e, int64_t before, int b, AttnPos& at) {
-    const AttnReq r = attn_request<C>(p, b);
     if (whole) {
       at = AttnPos{-1, b, (int)(e - before), 0};
       return;
     }
-    const int64_t x = total * e / n - before;
-    int64_t u = x / r.steps, s = x - u * r.steps;
-    if (e > 0 && e < n) {
-      if (s <= slack && s <= r.steps - s) {
-        s = 0;
-      } else if (r.steps - s <= slack) {
-        s = 0;
-        ++u;
-      }
-    }
-    at = AttnPos{before + u * r.steps + s, b, (int)u, (int)s};
+    const AttnReq r = attn_request<C>(p, b);
+    const int64_t x = attn_end(cut, e) - before;
+    int64_t u = attn_div(x, r.steps), s = x - u * r.steps;
+    if (e > 0 && e < n) s = attn_near(cut, s, r.steps);
+    at.x = before + u * r.steps + s;
+    at.b = b;
+    at.u = (int)u + (s == r.steps);
+    at.s = s == r.steps ? 0 : (int)s;
   };
   if (p.batch == 1) {
     place(k, 0, 0, from);
     place(k + 1, 0, 0, to);
   } else {
-    const int64_t x0 = whole ? k : total * k / n, x1 = whole ? k + 1 : total * (k + 1) / n;
+    const int64_t x0 = whole ? k : attn_end(cut, k),
+                  x1 = whole ? k + 1 : attn_end(cut, k + 1);
     int64_t base = 0;
     for (int64_t b0 = 0; b0 < p.batch; b0 += kAtThreads) {
       const int64_t b = b0 + tid;
@@ -810,9 +836,10 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
   __shared__ int s_any[kAtWaves];
   AttnPos at, to;
   const int id = (int)blockIdx.x;
-  AttnPlace mark{-1, 0, 0, 0};
+  AttnPlace mark{};
+  AttnCut cut;
   int k = id;
-  if (attn_plan<C>(p, id, k, at, to)) {
+  if (attn_plan<C>(p, id, k, cut, at, to)) {
     const bool whole = to.x < 0;
     AttnReq rq = attn_request<C>(p, at.b);
     do {  // uniform; no stretch is empty but for ends moved onto one another
@@ -826,10 +853,16 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
       const int t1 = at.s + left < rq.steps ? at.s + (int)left : rq.steps;
       const bool ends = t1 == rq.steps, begins = at.s == 0;
       if (begins && !ends) {
-        mark.b = at.b;
-        mark.u = at.u;
-      } else if (ends && !begins) {
-        mark.ends = 1;
+        // the first end of a stretch at or behind the unit's
+        const int64_t x1 = at.x + rq.steps;
+        int64_t e = attn_div((x1 - cut.slack) * cut.n, cut.total);
+        e = e > k + 1 ? e : k + 1;
+        while (e < cut.n) {
+          const int64_t s = attn_end(cut, e) - at.x;
+          if (s >= rq.steps || attn_near(cut, s, rq.steps) == rq.steps) break;
+          ++e;
+        }
+        mark = AttnPlace{(int)(e - k), at.b, at.u, rq.rows, rq.waves, rq.tiles, {0, 0}};
       }
       attn_piece<H, C>(p, lds, s_any, at.b, at.u, rq, at.s, t1,
                        begins && ends ? -1 : 2 * k + (begins ? 1 : 0));
@@ -844,38 +877,39 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
 }
 
 // Merges the pieces of the unit that a workgroup's stretch began and did not
-// end: a wave per two 4-float pieces of a query wave's state.
+// end: a wave per stretch, query wave and four 4-float pieces of its state, as
+// a workgroup of its own (with few units cut, the pieces' bytes have to come
+// in through as many CUs as there are).
 template <typename H, int DH, int NQ, int QW>
-__global__ __launch_bounds__(DH * NQ / 8) void attn_merge_kernel(AttnParams p) {
+__global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
   using C = AttnTile<DH, NQ, QW>;
-  const int wq = (int)(blockIdx.x % QW), k = (int)(blockIdx.x / QW);
+  constexpr int PP = 4, PER = C::PIECES / PP;  // waves of a state
+  const int k = (int)(blockIdx.x / (QW * PER)), r = (int)(blockIdx.x % (QW * PER));
   const AttnPlace pl = p.place[k];
-  if (pl.b < 0) return;
-  const AttnReq rq = attn_request<C>(p, pl.b);
-  const int lane = threadIdx.x & 63, j0 = 2 * (threadIdx.x >> 6);
+  if (pl.pieces == 0) return;
+  const int lane = threadIdx.x, wq = r / PER, j0 = PP * (r % PER);
+  AttnReq rq;
+  rq.rows = pl.rows;
+  rq.waves = pl.waves;
+  rq.tiles = pl.tiles;
   const AttnQuery me = attn_query<NQ>(p, rq, pl.u, wq, lane);
   if (!__ballot(me.live)) return;
-  // pieces: slot 2 k + 1, then 2 (k + 1), 2 (k + 2), ... up to the one that ends
-  int n = 1;
-  while (k + n < p.groups - 1 && !p.place[k + n].ends) ++n;
-  ++n;
-  auto slot = [&](int s) -> int64_t {
-    return (int64_t)(s == 0 ? 2 * k + 1 : 2 * (k + s)) * QW + wq;
-  };
-  float m = -INFINITY;
+  float m = -INFINITY, l = 0.0f;
+  at_f32x4 o[PP];
+#pragma unroll
+  for (int j = 0; j < PP; ++j) o[j] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-  for (int s = 0; s < n; ++s) m = fmaxf(m, p.part_ml[(slot(s) * kWave + lane) * 2]);
-  float l = 0.0f;
-  at_f32x4 o[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const int64_t at = slot(s);
-    const float* ml = p.part_ml + (at * kWave + lane) * 2;
-    const float a = ml[0] > -INFINITY ? __builtin_amdgcn_exp2f(ml[0] - m) : 0.0f;
-    l += ml[1] * a;
+  for (int s = 0; s < pl.pieces; ++s) {
+    const int64_t at = (int64_t)(s == 0 ? 2 * k + 1 : 2 * (k + s)) * QW + wq;
+    const float2 ml = *(const float2*)(p.part_ml + (at * kWave + lane) * 2);
     const at_f32x4* part = (const at_f32x4*)p.part + (at * C::PIECES + j0) * kWave + lane;
-    o[0] += part[0] * a;
-    o[1] += part[kWave] * a;
+    const float top = fmaxf(m, ml.x);
+    const float a = m > -INFINITY ? __builtin_amdgcn_exp2f(m - top) : 0.0f;
+    const float b = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - top) : 0.0f;
+    m = top;
+    l = l * a + ml.y * b;
+#pragma unroll
+    for (int j = 0; j < PP; ++j) o[j] = o[j] * a + part[j * kWave] * b;
   }
   if (me.live)
     attn_store<H, DH, NQ>(p, ((int64_t)pl.b * p.T + me.i) * p.q_heads + me.hq, j0, m, l, o, lane);

@@ -707,15 +707,28 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   const uint32_t page_bytes = (uint32_t)p.kv_heads * (uint32_t)p.rows.page_size * C::ROW;
   const int row_mask = paged ? p.rows.page_size - 1 : 0x7FFFFFFF;
   const int64_t base =
-      ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size * C::ROW + ld_c * 16;
-  const char* const k0 = (const char*)p.k_cache + base;
-  const char* const v0 = (const char*)p.v_cache + base;
+      ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size * C::ROW;
+  const char* const kh = (const char*)p.k_cache + base;
+  const char* const vh = (const char*)p.v_cache + base;
   auto row_of = [&](int t, int k) {  // the cache row that chunk k is of, clamped into the request
     const int r = t * C::TR + g * C::KT + ld_row + k * STEP;
     return r < rq.len ? r : rq.len - 1;
   };
+  // Pages of STEP rows or more: the STEP rows that a group's waves load at
+  // once lie on one page, so its address is scalar. (The entry still comes by
+  // a vector load: a scalar one would make every LDS wait a full one.)
+  const bool wide = paged && p.rows.page_size >= STEP;
+  const uint32_t lane_at = (uint32_t)(ld_row * C::ROW + ld_c * 16);
+  int zero = 0;
+  asm volatile("" : "+v"(zero));
   auto find = [&](int t) {
-    if (paged) {
+    if (wide) {
+#pragma unroll
+      for (int k = 0; k < C::LOADS; ++k) {
+        const int r = t * C::TR + g * C::KT + k * STEP;
+        page[k] = table[((r < rq.len ? r : rq.len - 1) >> p.rows.shift) + zero];
+      }
+    } else if (paged) {
 #pragma unroll
       for (int k = 0; k < C::LOADS; ++k) page[k] = table[row_of(t, k) >> p.rows.shift];
     } else {
@@ -724,14 +737,28 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
     }
   };
   auto fetch = [&](int t) {
+    if (wide) {
+#pragma unroll
+      for (int k = 0; k < C::LOADS; ++k) {
+        uint32_t pg = (uint32_t)__builtin_amdgcn_readfirstlane(page[k]);
+        pg = pg < (uint32_t)p.rows.pages ? pg : 0;
+        // (rows behind the request's last are on the page too)
+        const uint64_t at =
+            (uint64_t)pg * page_bytes +
+            (uint64_t)(uint32_t)((t * C::TR + g * C::KT + k * STEP) & row_mask) * C::ROW;
+        kr[k] = *(const at_u32x4*)(kh + at + lane_at);
+        vr[k] = *(const at_u32x4*)(vh + at + lane_at);
+      }
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < C::LOADS; ++k) {
       // rows on no page: some row's values, taken out by the mask
       const uint32_t pg = (uint32_t)page[k] < (uint32_t)p.rows.pages ? page[k] : 0;
       const uint64_t at = (uint64_t)pg * page_bytes +
-                          (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW;
-      kr[k] = *(const at_u32x4*)(k0 + at);
-      vr[k] = *(const at_u32x4*)(v0 + at);
+                          (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW + ld_c * 16;
+      kr[k] = *(const at_u32x4*)(kh + at);
+      vr[k] = *(const at_u32x4*)(vh + at);
     }
   };
   // steps before tm see every row they hold

@@ -587,7 +587,8 @@ SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bo
   SvPlan pl;
   pl.S = (int)((V + (V % N ? N - 1 : 0) + chunk - 1) / chunk);
   const int64_t rows = batch * T + (chain ? batch * (T - 1) : 0);
-  pl.stepped = false;
+  // Many rows: only the path's, one launch for each depth.
+  pl.stepped = rows * V * (int64_t)elem_size(dtype) > (L + 1) * ((int64_t)12 << 20);
   const size_t rec = sizeof(ddt::SvRec);
   size_t o = 0;
   pl.rec = o;
@@ -599,18 +600,20 @@ SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bo
   pl.rest = o;
   if (chain) o = align_up(o + (size_t)batch * pl.S * sizeof(double));
   pl.end = o;
-  (void)rows;
   return pl;
 }
 
 template <int DT, bool CHAIN>
 int accept_launch(const SvPlan& pl, const ddt::SvParams& sp, hipStream_t st) {
-  const dim3 block(ddt::kSvThreads), each((unsigned)sp.batch);
-  const int64_t per = CHAIN ? 2 : 1;
+  const dim3 block(ddt::kSvThreads), finish(ddt::kSvFinish), each((unsigned)sp.batch);
+  const unsigned chunks = (unsigned)(sp.batch * pl.S);
   if (pl.stepped) {
     for (int step = 0; step <= sp.L; ++step) {
-      hipLaunchKernelGGL((ddt::sv_step_kernel<DT, CHAIN>), dim3((unsigned)(sp.batch * per * pl.S)),
-                         block, 0, st, sp, step);
+      if (CHAIN)
+        hipLaunchKernelGGL((ddt::sv_chain_step_kernel<DT>), dim3(2 * chunks), block, 0, st, sp,
+                           step);
+      else
+        hipLaunchKernelGGL((ddt::sv_step_kernel<DT>), dim3(chunks), block, 0, st, sp, step);
       if (hipGetLastError() != hipSuccess) return DDT_EHIP;
     }
   } else {
@@ -620,16 +623,12 @@ int accept_launch(const SvPlan& pl, const ddt::SvParams& sp, hipStream_t st) {
     if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   }
   if (!CHAIN) {
-    hipLaunchKernelGGL((ddt::sv_finish_kernel<DT>), each, block, 0, st, sp, sp.L);
+    hipLaunchKernelGGL((ddt::sv_finish_kernel<DT>), each, finish, 0, st, sp, sp.L);
     return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
   }
-  const int at = pl.stepped ? sp.L + 1 : 0;  // the walk's last state
-  hipLaunchKernelGGL((ddt::sv_chain_walk_kernel<DT>), each, block, 0, st, sp, sp.L);
+  hipLaunchKernelGGL((ddt::sv_chain_rest_kernel<DT>), dim3(chunks), block, 0, st, sp, sp.L);
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
-  hipLaunchKernelGGL((ddt::sv_chain_rest_kernel<DT>), dim3((unsigned)(sp.batch * pl.S)), block, 0,
-                     st, sp, at);
-  if (hipGetLastError() != hipSuccess) return DDT_EHIP;
-  hipLaunchKernelGGL((ddt::sv_chain_finish_kernel<DT>), each, block, 0, st, sp, at);
+  hipLaunchKernelGGL((ddt::sv_chain_finish_kernel<DT>), each, finish, 0, st, sp);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
 }
 

@@ -18,13 +18,15 @@
 // Weights, sums and comparisons are float64: a token's interval on the line
 // can be as short as 1/V of it, and with V = 152 k float32 sums (1e-7 of the
 // line) would move one token in fifty of a flat row. CDNA4 runs a float64
-// FMA at the rate of an unpacked float32 one; exp2 is a degree-11 polynomial.
+// FMA at the rate of an unpacked float32 one; exp2 is a polynomial of degree 9
+// in the sums, which the vector units bound (17 instructions a logit).
 //
 // The row sums (records) are formed by workgroups of 256 threads, each over a
 // chunk of 8 16-byte vectors per thread held in registers: its maximum, then
 // the sum of its weights against that maximum. Only the rows on the path
 // matter, but which they are is known only step by step; the host picks one
-// of two schedules (accept_plan in api.hip).
+// of two schedules (accept_plan in api.hip): all rows' records in one launch,
+// or those of the path's rows, one launch for each depth.
 #pragma once
 
 #include "common.hpp"
@@ -36,6 +38,7 @@ constexpr int kSvVecs = 8;       // 16-byte vectors per thread and chunk
 constexpr int kSvMaxS = 512;     // chunks per row
 constexpr int kSvMaxB = 512;     // nodes
 constexpr int kSvChunkMax = kSvThreads * kSvVecs * 8;  // elements (bf16)
+constexpr int kSvFinish = 1024;  // threads of the launches that end a walk
 
 struct SvRec {
   double sum;  // of exp2((x - mx) / T log2 e) over the chunk
@@ -79,9 +82,12 @@ struct SvVec {
   static constexpr int N = DT == 0 ? 8 : 4;  // elements of a 16-byte vector
   sv_u32x4 r;
   // element e; NaN counts as -inf, +inf as the largest finite value
+  __device__ __forceinline__ float raw(int e) const {
+    return DT == 0 ? __uint_as_float(e & 1 ? r[e >> 1] & 0xFFFF0000u : r[e >> 1] << 16)
+                   : __uint_as_float(r[e & 3]);
+  }
   __device__ __forceinline__ float at(int e) const {
-    const float x = DT == 0 ? __uint_as_float(e & 1 ? r[e >> 1] & 0xFFFF0000u : r[e >> 1] << 16)
-                            : __uint_as_float(r[e & 3]);
+    const float x = raw(e);
     return x == x ? fminf(x, 3.402823466e38f) : -INFINITY;
   }
 };
@@ -137,6 +143,29 @@ __device__ __forceinline__ double sv_exp2(double y) {
   s = fma(s, z, 1.0);
   s = fma(s, z, 1.0);
   return ldexp(s, (int)k);
+}
+
+// The same for the sums: y within [-1000, 0] (what is below counts as 2^-1000),
+// 2^f by the polynomial through its values at the ten Chebyshev nodes of
+// [-1/2, 1/2], its constant 1.0000000000000135 set to 1 (within 3.3e-14 of
+// it), 2^k added to the exponent's bits.
+__device__ __forceinline__ double sv_exp2_fast(double y) {
+  y = fmax(y, -1000.0);
+  const double big = 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits are k
+  const double t = y + big;
+  const double f = y - (t - big);
+  double s = 1.0205905413765595471e-07;
+  s = fma(s, f, 1.3259645244887110601e-06);
+  s = fma(s, f, 1.5252672924850737155e-05);
+  s = fma(s, f, 0.00015403433751251009655);
+  s = fma(s, f, 0.0013333558200794592453);
+  s = fma(s, f, 0.0096181291939343126207);
+  s = fma(s, f, 0.055504108664651670424);
+  s = fma(s, f, 0.24022650695640340723);
+  s = fma(s, f, 0.69314718055994617441);
+  s = fma(s, f, 1.0);
+  const uint64_t k = (uint64_t)__builtin_bit_cast(uint64_t, t) << 52;
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, s) + k);
 }
 
 // Inclusive scan of one double per lane over the wave (every lane active).
@@ -209,6 +238,28 @@ __device__ __forceinline__ SvRow sv_combine(const SvRec* rec, int S, const SvHea
   return row;
 }
 
+// This thread's part of a chunk's sum of weights against its maximum m.
+template <int DT>
+__device__ __forceinline__ double sv_sum(const SvVec<DT> (&x)[kSvVecs], float m, const SvHeat& h) {
+  constexpr int N = SvVec<DT>::N;
+  const double ms = (double)m * h.s;
+  double z[2] = {0.0, 0.0};
+  if (fabs(ms) < 1024.0) {
+    // (x - m) s as x s - m s is within 2^-43 then; NaN and -inf end at the
+    // least weight by the maximum in sv_exp2_fast
+#pragma unroll
+    for (int i = 0; i < kSvVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) z[e & 1] += sv_exp2_fast(fma((double)x[i].raw(e), h.s, -ms));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSvVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) z[e & 1] += sv_exp2(((double)x[i].at(e) - (double)m) * h.s);
+  }
+  return z[0] + z[1];
+}
+
 // One chunk's record.
 template <int DT>
 __device__ __forceinline__ void sv_chunk(const void* base, int64_t r0, int64_t V, int c,
@@ -228,8 +279,8 @@ __device__ __forceinline__ void sv_chunk(const void* base, int64_t r0, int64_t V
 #pragma unroll
   for (int i = 0; i < kSvVecs; ++i)
 #pragma unroll
-    for (int e = 0; e < N; ++e) m = fmaxf(m, x[i].at(e));
-  m = wave_max(m);
+    for (int e = 0; e < N; ++e) m = fmaxf(m, x[i].raw(e));  // (passes NaN over)
+  m = wave_max(fminf(m, 3.402823466e38f));
   if ((tid & 63) == 0) s_m[w] = m;
   __syncthreads();
   m = s_m[0];
@@ -253,17 +304,13 @@ __device__ __forceinline__ void sv_chunk(const void* base, int64_t r0, int64_t V
       *out = SvRec{0.0, m, arg};
     }
   } else {
-    double z = 0.0;
-#pragma unroll
-    for (int i = 0; i < kSvVecs; ++i)
-#pragma unroll
-      for (int e = 0; e < N; ++e) z += sv_exp2(((double)x[i].at(e) - (double)m) * h.s);
-    z = wave_sum(z);
+    const double z = wave_sum(sv_sum<DT>(x, m, h));
     if ((tid & 63) == 0) s_s[w] = z;
     __syncthreads();
     if (tid == 0) {
-      for (int i = 1; i < NW; ++i) z += s_s[i];
-      *out = SvRec{m > -INFINITY ? z : 0.0, m, 0x7FFFFFFF};
+      double all = z;
+      for (int i = 1; i < NW; ++i) all += s_s[i];
+      *out = SvRec{m > -INFINITY ? all : 0.0, m, 0x7FFFFFFF};
     }
   }
 }
@@ -284,105 +331,162 @@ __global__ __launch_bounds__(kSvThreads) void sv_rows_kernel(SvParams p) {
                (q ? p.rec_q : p.rec) + row * p.S + c);
 }
 
-// LDS of a decision and of the final draw.
-struct SvShared {
-  double w[kSvMaxB];
-  int tok[kSvMaxB];
-  int pick;
-  int n;
-  double edge;
-  double z;
-  double seg[kSvVecs][kSvThreads / kWave];
-  uint32_t bits[kSvChunkMax / 32];
-  int found;
-  int last;
-  double rest[kSvMaxS];
-};
-
-// The tree's decision at one node: the child that t = u Z falls on (-1: none),
-// and the children's total weight. The tokens of the children that take a
-// part of the line are left in sh.tok[0 .. sh.n). Every thread calls it.
-template <int DT>
-__device__ int sv_decide_tree(const SvParams& p, int64_t b, int node, int d, const SvRow& row,
-                              SvShared& sh, double& t, double& edge, double& wt) {
-  const int n = d < p.L ? sv_count(p, b) : 0;
-  const int B = p.T - 1, tid = threadIdx.x, lane = tid & 63;
-  const int64_t r0 = (b * p.T + node) * p.V;
-  t = sv_uniform(p, b, d) * row.Z;
-  __syncthreads();
-  for (int j = tid; j < n; j += kSvThreads) {
-    int tok = -1;
-    if (p.parents[b * B + j] == node && node <= j) {
-      tok = p.tokens[b * B + j];
-      if (tok < 0 || tok >= p.V) tok = -1;
-    }
-    sh.tok[j] = tok;
-    sh.w[j] = tok >= 0 ? row.weight(sv_logit<DT>(p.logits, r0, tok), tok) : 0.0;
-  }
-  __syncthreads();
-  // a token that an earlier sibling carries already takes no second part
-  bool dup[2] = {false, false};
-  for (int q = 0; q < 2; ++q) {
-    const int j = tid + q * kSvThreads;
-    if (j < n && sh.tok[j] >= 0)
-      for (int i = 0; i < j; ++i) dup[q] |= sh.tok[i] == sh.tok[j];
-  }
-  __syncthreads();
-  for (int q = 0; q < 2; ++q) {
-    const int j = tid + q * kSvThreads;
-    if (dup[q]) {
-      sh.tok[j] = -1;
-      sh.w[j] = 0.0;
-    }
-  }
-  __syncthreads();
-  if (tid < kWave) {
-    double base = 0.0;
-    int pick = -1, kept = 0;
-    for (int j0 = 0; j0 < n; j0 += kWave) {
-      const int j = j0 + lane;
-      const int tok = j < n ? sh.tok[j] : -1;
-      const uint64_t kids = __ballot(tok >= 0);
-      if (!kids) continue;
-      const double cum = base + wave_incl_scan_f64(j < n ? sh.w[j] : 0.0);
-      const uint64_t hit = __ballot(tok >= 0 && t < cum);
-      if (hit && pick < 0) pick = j0 + __builtin_ctzll(hit);
-      base = __shfl(cum, 63);
-      if (tok >= 0) sh.tok[kept + lanes_below(kids)] = tok;  // never ahead of the reads
-      kept += __popcll(kids);
-    }
-    if (lane == 0) {
-      sh.pick = pick;
-      sh.edge = base;
-      sh.n = kept;
-      sh.z = pick >= 0 ? sh.w[pick] : 0.0;
-    }
-  }
-  __syncthreads();
-  edge = sh.edge;
-  wt = sh.z;
-  return sh.pick;
-}
-
 __device__ __forceinline__ float sv_logp(double w, double Z) {
   return Z > 0.0 ? (float)(log(w) - log(Z)) : -INFINITY;
 }
 
+// Where the records of a row lie: by row, or (stepped) by request and the
+// parity of the depth.
+__device__ __forceinline__ int64_t sv_rec_at(const SvParams& p, int64_t b, int at, int d, int per) {
+  return p.stepped ? ((int64_t)(d & 1) * p.batch + b) * p.S : (b * per + at) * p.S;
+}
+
+// ---- trees: the line at a node ------------------------------------------------
+// A node's key: its parent and its token in one word (B <= 512, V <= 2^22); a
+// node that cannot be accepted has none.
+constexpr uint32_t kSvNoKey = 0xFFFFFFFFu;
+
+__device__ __forceinline__ uint32_t sv_key(const SvParams& p, int64_t b, int j, int n) {
+  if (j >= n) return kSvNoKey;
+  const int par = p.parents[b * (p.T - 1) + j], tok = p.tokens[b * (p.T - 1) + j];
+  if (par < 0 || par > j || tok < 0 || tok >= p.V) return kSvNoKey;
+  return (uint32_t)par << 22 | (uint32_t)tok;
+}
+
+// Walk state of a request's tree in LDS, by node j (number j + 1).
+struct SvTree {
+  uint32_t key[kSvMaxB];
+  double w[kSvMaxB];  // weight of the node's token in its parent's row
+  // the decision: child hit (-1: none), all children's weight, their count and
+  // tokens
+  int pick, kids;
+  double edge;
+  int tok[kSvMaxB];
+};
+
+// Keys whose token an earlier sibling carries already take no second part of
+// the line. Every thread calls it; keys and a barrier before, a barrier after.
+template <int NT>
+__device__ __forceinline__ void sv_unique(SvTree& t, int n) {
+  bool dup[kSvMaxB / NT > 0 ? kSvMaxB / NT : 1];
+#pragma unroll
+  for (int q = 0; q < (kSvMaxB + NT - 1) / NT; ++q) {
+    const int j = threadIdx.x + q * NT;
+    dup[q] = false;
+    if (j < n && t.key[j] != kSvNoKey)
+      for (int i = 0; i < j; ++i) dup[q] |= t.key[i] == t.key[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < (kSvMaxB + NT - 1) / NT; ++q)
+    if (dup[q]) t.key[threadIdx.x + q * NT] = kSvNoKey;
+}
+
+// Where position `at` of the line falls at a node, by one wave: t.pick,
+// t.edge and, for the draw after it, the children's tokens.
+__device__ __forceinline__ void sv_hit(SvTree& t, int node, int n, double at) {
+  const int lane = threadIdx.x & 63;
+  double base = 0.0;
+  int pick = -1, kept = 0;
+  for (int j0 = 0; j0 < n; j0 += kWave) {
+    const int j = j0 + lane;
+    const uint32_t key = j < n ? t.key[j] : kSvNoKey;
+    const bool kid = key != kSvNoKey && (int)(key >> 22) == node;
+    const uint64_t kids = __ballot(kid);
+    if (!kids) continue;
+    const double cum = base + wave_incl_scan_f64(kid ? t.w[j] : 0.0);
+    const uint64_t hit = __ballot(kid && at < cum);
+    if (kid) t.tok[kept + lanes_below(kids)] = (int)(key & 0x3FFFFFu);
+    kept += __popcll(kids);
+    base = __shfl(cum, 63);
+    if (hit) {
+      pick = j0 + __builtin_ctzll(hit);
+      break;
+    }
+  }
+  if (lane == 0) {
+    t.pick = pick;
+    t.edge = base;
+    t.kids = kept;
+  }
+}
+
+// One step of the walk for every request: the decision at the row whose
+// records the step before formed, then one chunk of the next row's records.
+template <int DT>
+__global__ __launch_bounds__(kSvThreads) void sv_step_kernel(SvParams p, int step) {
+  __shared__ SvTree sh;
+  const int64_t b = blockIdx.x / p.S;
+  const int c = (int)(blockIdx.x - b * p.S), tid = threadIdx.x;
+  const SvHeat h = sv_heat(p, b);
+  SvState st{0, 0, 0, 0};
+  if (step > 0) {
+    const int d = step - 1;
+    const int n = d < p.L ? sv_count(p, b) : 0;
+    const uint32_t k0 = sv_key(p, b, tid, n), k1 = sv_key(p, b, tid + kSvThreads, n);
+    st = p.state[(int64_t)d * p.batch + b];
+    if (!st.done) {
+      // the node's children
+      const int64_t r0 = (b * p.T + st.at) * p.V;
+      const bool kid0 = k0 != kSvNoKey && (int)(k0 >> 22) == st.at;
+      const bool kid1 = k1 != kSvNoKey && (int)(k1 >> 22) == st.at;
+      const int t0 = (int)(k0 & 0x3FFFFFu), t1 = (int)(k1 & 0x3FFFFFu);
+      const float x0 = kid0 ? sv_logit<DT>(p.logits, r0, t0) : 0.0f;
+      const float x1 = kid1 ? sv_logit<DT>(p.logits, r0, t1) : 0.0f;
+      const SvRow row = sv_combine(p.rec + sv_rec_at(p, b, st.at, d, p.T), p.S, h);
+      sh.key[tid] = kid0 ? k0 : kSvNoKey;
+      sh.key[tid + kSvThreads] = kid1 ? k1 : kSvNoKey;
+      sh.w[tid] = kid0 ? row.weight(x0, t0) : 0.0;
+      sh.w[tid + kSvThreads] = kid1 ? row.weight(x1, t1) : 0.0;
+      __syncthreads();
+      sv_unique<kSvThreads>(sh, n);
+      __syncthreads();
+      if (tid < kWave) sv_hit(sh, st.at, n, sv_uniform(p, b, d) * row.Z);
+      __syncthreads();
+      if (sh.pick >= 0) {
+        if (c == 0 && tid == 0) {
+          p.accepted[b * p.L + d] = sh.pick + 1;
+          if (p.logp) p.logp[b * (p.L + 1) + d] = sv_logp(sh.w[sh.pick], row.Z);
+        }
+        st.at = sh.pick + 1;
+        st.depth = step;
+      } else {
+        st.done = 1;
+      }
+    }
+  }
+  if (c == 0 && tid == 0) p.state[(int64_t)step * p.batch + b] = st;
+  if (st.done) return;
+  sv_chunk<DT>(p.logits, (b * p.T + st.at) * p.V, p.V, c, h,
+               p.rec + ((int64_t)(step & 1) * p.batch + b) * p.S + c);
+}
+
+// ---- the draw of the next token --------------------------------------------------
+template <int NT>
+struct SvDraw {
+  static constexpr int VECS = kSvThreads * kSvVecs / NT;  // vectors per thread
+  double z;
+  int found, last;
+  double seg[VECS][NT / kWave];
+  uint32_t bits[kSvChunkMax / 32];
+  double rest[kSvMaxS];
+};
+
 // Draws from the weights of a chunk (minus q's for PQ, without the tokens
 // marked in sh.bits): the first element whose running sum passes t, else the
-// last with any weight, else -1. w_out: its weight. Every thread calls it.
-template <int DT, bool PQ>
+// last with any weight, else -1. Every thread calls it.
+template <int DT, bool PQ, int NT>
 __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, const SvRow& row,
-                             const SvRow& rowq, bool marked, double t, SvShared& sh, double& w_out) {
-  constexpr int N = SvVec<DT>::N, NW = kSvThreads / kWave;
+                             const SvRow& rowq, bool marked, double t, SvDraw<NT>& sh) {
+  constexpr int N = SvVec<DT>::N, NW = NT / kWave, VECS = SvDraw<NT>::VECS;
   const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
   const int64_t v0 = (int64_t)c * kSvThreads * kSvVecs;
   const int off = (int)(rp & (N - 1));
   const double zp = 1.0 / row.Z, zq = PQ ? 1.0 / rowq.Z : 0.0;
-  SvVec<DT> x[kSvVecs], y[PQ ? kSvVecs : 1];
-  double incl[kSvVecs];
+  SvVec<DT> x[VECS], y[PQ ? VECS : 1];
+  double incl[VECS];
   auto weight = [&](int i, int e) -> double {
-    const int64_t id = (v0 + i * kSvThreads + tid) * N - off + e;
+    const int64_t id = (v0 + i * NT + tid) * N - off + e;
     if (id < 0 || id >= p.V) return 0.0;
     double a = row.weight(x[i].at(e), id);
     if (PQ) a = fmax(a * zp - rowq.weight(y[PQ ? i : 0].at(e), id) * zq, 0.0);
@@ -391,15 +495,15 @@ __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, c
     return a;
   };
 #pragma unroll
-  for (int i = 0; i < kSvVecs; ++i) {
-    const int64_t e0 = (v0 + i * kSvThreads + tid) * N - off;
+  for (int i = 0; i < VECS; ++i) {
+    const int64_t e0 = (v0 + i * NT + tid) * N - off;
     x[i] = sv_load<DT>(p.logits, rp, e0, p.V);
     if (PQ) y[PQ ? i : 0] = sv_load<DT>(p.draft, rq, e0, p.V);
   }
   if (tid == 0) sh.found = sh.last = -1;
   int last = -1;
 #pragma unroll
-  for (int i = 0; i < kSvVecs; ++i) {
+  for (int i = 0; i < VECS; ++i) {
     double sum = 0.0;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -413,7 +517,7 @@ __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, c
   __syncthreads();
   double run = 0.0;
   int hit = -1;
-  for (int g = 0; g < kSvVecs * NW; ++g) {
+  for (int g = 0; g < VECS * NW; ++g) {
     const double s = sh.seg[g / NW][g % NW];
     if (run + s > t) {
       hit = g;
@@ -424,7 +528,7 @@ __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, c
   if (hit >= 0) {
     if (w == hit % NW) {
 #pragma unroll
-      for (int i = 0; i < kSvVecs; ++i) {
+      for (int i = 0; i < VECS; ++i) {
         if (i != hit / NW) continue;
         const uint64_t over = __ballot(run + incl[i] > t);
         const int l = __builtin_ctzll(over);
@@ -432,53 +536,38 @@ __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, c
         if (lane == l) {
           double cum = run + (lane > 0 ? before : 0.0);
           int at = -1;
-          double wa = 0.0;
 #pragma unroll
           for (int e = 0; e < N; ++e) {
             const double a = weight(i, e);
             const bool open = at < 0 || !(cum > t);
             cum += a;
-            if (a > 0.0 && open) {
-              at = e;
-              wa = a;
-            }
+            if (a > 0.0 && open) at = e;
           }
-          sh.found = (int)((v0 + i * kSvThreads + tid) * N - off) + at;
-          sh.z = wa;
+          sh.found = (int)((v0 + i * NT + tid) * N - off) + at;
         }
       }
     }
-    __syncthreads();
   } else {
     // the last element with any weight
-    const int id = last < 0 ? -1
-                            : (int)((v0 + (last / N) * kSvThreads + tid) * N - off) + last % N;
+    const int id =
+        last < 0 ? -1 : (int)((v0 + (last / N) * NT + tid) * N - off) + last % N;
     const int top = wave_max(id);
-    if (lane == 0) atomicMax(&sh.last, top);
-    __syncthreads();
-    const int pickid = sh.last;
-    if (pickid >= 0 && pickid == id) {
-#pragma unroll
-      for (int i = 0; i < kSvVecs; ++i)
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (i * N + e == last) sh.z = weight(i, e);
-    }
-    if (tid == 0) sh.found = pickid;
-    __syncthreads();
+    if (lane == 0) atomicMax(&sh.found, top);
   }
+  __syncthreads();
   const int found = sh.found;
-  w_out = sh.z;
   __syncthreads();
   return found;
 }
 
 // Draws the next token from a row whose chunk sums are sh.rest[0 .. S): the
 // chunk that t falls into, then the element; where rounding leaves no weight
-// there, the chunks behind it, then those before it. Every thread calls it.
-template <int DT, bool PQ>
+// there, the chunks behind it, then those before it. tok: the n_marked tokens
+// without a part. Every thread calls it.
+template <int DT, bool PQ, int NT>
 __device__ int sv_draw(const SvParams& p, int64_t rp, int64_t rq, const SvRow& row,
-                       const SvRow& rowq, int n_marked, double t, SvShared& sh, double& w_out) {
+                       const SvRow& rowq, const int* tok, int n_marked, double t,
+                       SvDraw<NT>& sh) {
   constexpr int N = SvVec<DT>::N;
   const int tid = threadIdx.x;
   double before = 0.0;
@@ -498,177 +587,230 @@ __device__ int sv_draw(const SvParams& p, int64_t rp, int64_t rq, const SvRow& r
     // behind c0 the first weight is taken, before it (or past the end) the last
     const double tc = a == 0 && !past_end ? fmax(t - before, 0.0) : (c > c0 ? 0.0 : 1e300);
     if (n_marked > 0) {
-      for (int i = tid; i < kSvChunkMax / 32; i += kSvThreads) sh.bits[i] = 0;
+      for (int i = tid; i < kSvChunkMax / 32; i += NT) sh.bits[i] = 0;
       __syncthreads();
-      for (int i = tid; i < n_marked; i += kSvThreads) {
-        const int64_t k = (int64_t)sh.tok[i] + off - (int64_t)c * kSvThreads * kSvVecs * N;
-        if (k >= 0 && k < kSvThreads * kSvVecs * N)
-          atomicOr(&sh.bits[k >> 5], 1u << (k & 31));
+      for (int i = tid; i < n_marked; i += NT) {
+        const int64_t k = (int64_t)tok[i] + off - (int64_t)c * kSvThreads * kSvVecs * N;
+        if (k >= 0 && k < kSvThreads * kSvVecs * N) atomicOr(&sh.bits[k >> 5], 1u << (k & 31));
       }
       __syncthreads();
     }
-    const int id = sv_draw_chunk<DT, PQ>(p, rp, rq, c, row, rowq, n_marked > 0, tc, sh, w_out);
+    const int id = sv_draw_chunk<DT, PQ, NT>(p, rp, rq, c, row, rowq, n_marked > 0, tc, sh);
     if (id >= 0) return id;
   }
   return -1;
 }
 
-// Where the records of a row lie: by row, or (stepped) by request and the
-// parity of the depth.
-__device__ __forceinline__ int64_t sv_rec_at(const SvParams& p, int64_t b, int at, int d, int per) {
-  return p.stepped ? ((int64_t)(d & 1) * p.batch + b) * p.S : (b * per + at) * p.S;
-}
-
-// A chain's test of guess d at row d: true where it stands.
-template <int DT>
-__device__ bool sv_decide_chain(const SvParams& p, int64_t b, int d, const SvRow& row,
-                                const SvRow& rowq, double& wt) {
-  const int P = p.T - 1;
-  const int x = p.tokens[b * P + d];
-  wt = 0.0;
-  if (x < 0 || x >= p.V) return false;
-  const double wp = row.weight(sv_logit<DT>(p.logits, (b * p.T + d) * p.V, x), x);
-  const double wq = rowq.weight(sv_logit<DT>(p.draft, (b * P + d) * p.V, x), x);
-  wt = wp;
-  // (a drafter's row with every token masked has q = 0)
-  return sv_uniform(p, b, d) * wq * row.Z < wp * (rowq.Z > 0.0 ? rowq.Z : 1.0);
-}
-
-// One decision at (st.at, st.depth), whose row's records are complete:
-// advances st, or marks it done. Writes the accepted node and its
-// log-probability where `write`.
-template <int DT, bool CHAIN>
-__device__ void sv_advance(const SvParams& p, int64_t b, SvState& st, bool write, SvShared& sh,
-                           SvRow& row, SvRow& rowq, double& t, double& edge) {
-  const SvHeat h = sv_heat(p, b);
-  const int d = st.depth, P = p.T - 1;
-  row = sv_combine(p.rec + sv_rec_at(p, b, st.at, d, p.T), p.S, h);
-  double wt = 0.0;
-  int next = -1;
-  if (CHAIN) {
-    if (d < sv_count(p, b)) {
-      rowq = sv_combine(p.rec_q + sv_rec_at(p, b, d, d, P), p.S, h);
-      if (sv_decide_chain<DT>(p, b, d, row, rowq, wt)) next = d + 1;
-      else st.done = 2;
-    } else {
-      st.done = 1;
-    }
-  } else {
-    const int pick = sv_decide_tree<DT>(p, b, st.at, d, row, sh, t, edge, wt);
-    if (pick >= 0) next = pick + 1;
-    else st.done = 1;
-  }
-  if (next >= 0) {
-    if (write && threadIdx.x == 0) {
-      if (!CHAIN) p.accepted[b * p.L + d] = next;
-      if (p.logp) p.logp[b * (p.L + 1) + d] = sv_logp(wt, row.Z);
-    }
-    st.at = next;
-    st.depth = d + 1;
-  }
-}
-
-// One step of the walk for every request: the decision at the row whose
-// records the step before formed, then one chunk of the next row's records.
-template <int DT, bool CHAIN>
-__global__ __launch_bounds__(kSvThreads) void sv_step_kernel(SvParams p, int step) {
-  __shared__ SvShared sh;
-  const int64_t id = blockIdx.x;
-  const int64_t per = CHAIN ? 2 * (int64_t)p.S : p.S;
-  const int64_t b = id / per;
-  int c = (int)(id - b * per);
-  const bool q = CHAIN && c >= p.S;
-  const bool first = c == 0;
-  if (q) c -= p.S;
-  SvState st{0, 0, 0, 0};
-  if (step > 0) {
-    st = p.state[(int64_t)(step - 1) * p.batch + b];
-    if (!st.done) {
-      SvRow row, rowq;
-      double t, edge;
-      sv_advance<DT, CHAIN>(p, b, st, first, sh, row, rowq, t, edge);
-    }
-  }
-  if (first && threadIdx.x == 0) p.state[(int64_t)step * p.batch + b] = st;
-  if (st.done || (q && st.at >= sv_count(p, b))) return;
-  const int64_t row = b * (q ? p.T - 1 : p.T) + st.at;
-  sv_chunk<DT>(q ? p.draft : p.logits, row * p.V, p.V, c, sv_heat(p, b),
-               (q ? p.rec_q : p.rec) + ((int64_t)(step & 1) * p.batch + b) * p.S + c);
-}
-
-template <int DT, bool CHAIN>
-__device__ void sv_tail(const SvParams& p, int64_t b, const SvState& st, int token, double w,
-                        double Z) {
-  for (int i = st.depth + threadIdx.x; i <= p.L; i += kSvThreads) {
+template <bool CHAIN>
+__device__ void sv_tail(const SvParams& p, int64_t b, int depth, int token, double w, double Z) {
+  for (int i = depth + threadIdx.x; i <= p.L; i += blockDim.x) {
     if (!CHAIN && i < p.L) p.accepted[b * p.L + i] = -1;
-    if (p.logp) p.logp[b * (p.L + 1) + i] = i > st.depth ? 0.0f : (token < 0 ? -INFINITY : sv_logp(w, Z));
+    if (p.logp)
+      p.logp[b * (p.L + 1) + i] = i > depth ? 0.0f : (token < 0 ? -INFINITY : sv_logp(w, Z));
   }
   if (threadIdx.x == 0) {
-    p.accept_len[b] = st.depth;
+    p.accept_len[b] = depth;
     p.next_token[b] = token;
   }
 }
 
-// Trees: the rest of the walk and the next token, one workgroup per request.
+// Trees: the walk (unless it was stepped) and the next token, one workgroup
+// per request. Every row's sums and every node's weight are formed
+// side by side first, so that the walk itself only reads LDS.
 template <int DT>
-__global__ __launch_bounds__(kSvThreads) void sv_finish_kernel(SvParams p, int step) {
-  __shared__ SvShared sh;
+__global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int step) {
+  constexpr int NT = kSvFinish, N = SvVec<DT>::N;
+  __shared__ SvTree sh;
+  __shared__ SvDraw<NT> dr;
+  __shared__ double s_Z[kSvMaxB + 1];
+  __shared__ float s_M[kSvMaxB + 1];
+  __shared__ int s_arg[kSvMaxB + 1];
   const int64_t b = blockIdx.x;
-  SvState st{0, 0, 0, 0};
-  if (p.stepped) st = p.state[(int64_t)step * p.batch + b];
-  SvRow row, rowq;
-  double t = 0.0, edge = 0.0;
-  st.done = 0;  // a decision that ended the walk is made again, for its line
-  while (!st.done) sv_advance<DT, false>(p, b, st, true, sh, row, rowq, t, edge);
-  const int n = sh.n;
+  const int tid = threadIdx.x;
+  const SvHeat h = sv_heat(p, b);
+  const int count = sv_count(p, b);
+  uint32_t key = sv_key(p, b, tid, count);
+  int node = 0, d = 0;
+  if (p.stepped) {
+    const SvState st = p.state[(int64_t)step * p.batch + b];
+    node = st.at;
+    d = st.depth;
+    // the walk has ended here; its node's line is formed again
+    if (key != kSvNoKey && (int)(key >> 22) != node) key = kSvNoKey;
+  }
+  const int par = (int)(key >> 22), tok = (int)(key & 0x3FFFFFu);
+  const float x = key != kSvNoKey ? sv_logit<DT>(p.logits, (b * p.T + par) * p.V, tok) : 0.0f;
+  if (tid < kSvMaxB) sh.key[tid] = key;
+  // the rows' maxima and sums: a wave takes a row (stepped: the node's only)
+  for (int r = p.stepped ? node : tid >> 6; r <= (p.stepped ? node : count); r += NT / kWave) {
+    const SvRow row = sv_combine(p.rec + sv_rec_at(p, b, r, d, p.T), p.S, h);
+    if ((tid & 63) == 0) {
+      s_Z[r] = row.Z;
+      s_M[r] = (float)row.M;
+      s_arg[r] = row.arg;
+    }
+    if (p.stepped) break;
+  }
+  __syncthreads();
+  auto row_of = [&](int r) {
+    SvRow row;
+    row.M = (double)s_M[r];
+    row.Z = s_Z[r];
+    row.s = h.s;
+    row.arg = s_arg[r];
+    row.greedy = h.greedy;
+    return row;
+  };
+  if (tid < kSvMaxB) sh.w[tid] = key != kSvNoKey ? row_of(par).weight(x, tok) : 0.0;
+  sv_unique<NT>(sh, count);
+  __syncthreads();
+  if (tid < kWave) {
+    for (;;) {
+      sv_hit(sh, node, d < p.L ? count : 0, p.stepped ? 1e300 : sv_uniform(p, b, d) * s_Z[node]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int pick = sh.pick;
+      if (pick < 0) break;
+      if (tid == 0) {
+        p.accepted[b * p.L + d] = pick + 1;
+        if (p.logp) p.logp[b * (p.L + 1) + d] = sv_logp(sh.w[pick], s_Z[node]);
+      }
+      node = pick + 1;
+      ++d;
+    }
+    if (tid == 0) {
+      dr.found = node;
+      dr.last = d;
+    }
+  }
+  __syncthreads();
+  node = dr.found;
+  d = dr.last;
+  const SvRow row = row_of(node);
+  const int n = sh.kids;
   int token = -1;
   double w = 0.0;
-  if (row.greedy) {
+  if (row.Z > 0.0 && row.greedy) {
     token = row.arg;
     w = 1.0;
   } else if (row.Z > 0.0) {
     // the chunks' weights without the children's
-    const SvRec* rec = p.rec + sv_rec_at(p, b, st.at, st.depth, p.T);
-    const int64_t r0 = (b * p.T + st.at) * p.V;
-    constexpr int N = SvVec<DT>::N;
+    const SvRec* rec = p.rec + sv_rec_at(p, b, node, d, p.T);
+    const int64_t r0 = (b * p.T + node) * p.V;
     const int off = (int)(r0 & (N - 1));
-    for (int i = threadIdx.x; i < n; i += kSvThreads)
-      sh.w[i] = row.weight(sv_logit<DT>(p.logits, r0, sh.tok[i]), sh.tok[i]);
-    __syncthreads();
-    for (int c = threadIdx.x; c < p.S; c += kSvThreads) {
+    const double at = sv_uniform(p, b, d) * row.Z - sh.edge;
+    for (int c = tid; c < p.S; c += NT) {
       double s = rec[c].sum * sv_exp2(((double)rec[c].mx - row.M) * row.s);
-      for (int i = 0; i < n; ++i)
-        if ((sh.tok[i] + off) / (kSvThreads * kSvVecs * N) == c) s -= sh.w[i];
-      sh.rest[c] = fmax(s, 0.0);
+      for (int j = 0; j < count && n > 0; ++j) {
+        const uint32_t k = sh.key[j];
+        if (k != kSvNoKey && (int)(k >> 22) == node &&
+            ((int)(k & 0x3FFFFFu) + off) / (kSvThreads * kSvVecs * N) == c)
+          s -= sh.w[j];
+      }
+      dr.rest[c] = fmax(s, 0.0);
     }
     __syncthreads();
-    token = sv_draw<DT, false>(p, r0, 0, row, row, n, t - edge, sh, w);
+    token = sv_draw<DT, false, NT>(p, r0, 0, row, row, sh.tok, n, at, dr);
+    if (token >= 0) w = row.weight(sv_logit<DT>(p.logits, r0, token), token);
   }
-  sv_tail<DT, false>(p, b, st, token, w, row.Z);
+  sv_tail<false>(p, b, d, token, w, row.Z);
 }
 
-// Chains: the rest of the walk.
+// ---- chains ----------------------------------------------------------------------
+// A chain's test of guess i: true where it stands. wt: its weight.
 template <int DT>
-__global__ __launch_bounds__(kSvThreads) void sv_chain_walk_kernel(SvParams p, int step) {
-  __shared__ SvShared sh;
-  const int64_t b = blockIdx.x;
-  SvState st{0, 0, 0, 0};
-  if (p.stepped) st = p.state[(int64_t)step * p.batch + b];
-  SvRow row, rowq;
-  double t, edge;
-  while (!st.done) sv_advance<DT, true>(p, b, st, true, sh, row, rowq, t, edge);
-  if (threadIdx.x == 0) p.state[(int64_t)(p.stepped ? step + 1 : 0) * p.batch + b] = st;
+__device__ bool sv_stands(const SvParams& p, int64_t b, int i, int token, float xp, float xq,
+                          const SvRow& row, const SvRow& rowq, double& wt) {
+  wt = 0.0;
+  if (token < 0 || token >= p.V) return false;
+  const double wp = row.weight(xp, token), wq = rowq.weight(xq, token);
+  wt = wp;
+  // (a drafter's row with every token masked has q = 0)
+  return sv_uniform(p, b, i) * wq * row.Z < wp * (rowq.Z > 0.0 ? rowq.Z : 1.0);
 }
 
-// Chains: chunk sums of max(0, p - q) where a guess fell.
+// Guess i's test by one wave.
+template <int DT>
+__device__ bool sv_test(const SvParams& p, int64_t b, int i, const SvHeat& h, double& wt,
+                        SvRow& row) {
+  const int P = p.T - 1;
+  const int token = p.tokens[b * P + i];
+  const bool in = token >= 0 && token < p.V;
+  const float xp = in ? sv_logit<DT>(p.logits, (b * p.T + i) * p.V, token) : 0.0f;
+  const float xq = in ? sv_logit<DT>(p.draft, (b * P + i) * p.V, token) : 0.0f;
+  row = sv_combine(p.rec + sv_rec_at(p, b, i, i, p.T), p.S, h);
+  const SvRow rowq = sv_combine(p.rec_q + sv_rec_at(p, b, i, i, P), p.S, h);
+  return sv_stands<DT>(p, b, i, token, xp, xq, row, rowq, wt);
+}
+
+// One step of a chain for every request: the test of the guess whose rows'
+// records the step before formed, then one chunk of the next rows' records.
+template <int DT>
+__global__ __launch_bounds__(kSvThreads) void sv_chain_step_kernel(SvParams p, int step) {
+  const int64_t b = blockIdx.x / (2 * p.S);
+  int c = (int)(blockIdx.x - b * 2 * p.S);
+  const bool q = c >= p.S, first = c == 0 && threadIdx.x == 0;
+  if (q) c -= p.S;
+  const SvHeat h = sv_heat(p, b);
+  const int keep = sv_count(p, b);
+  SvState st{0, 0, 0, 0};
+  if (step > 0) {
+    st = p.state[(int64_t)(step - 1) * p.batch + b];
+    if (!st.done) {
+      double wt = 0.0;
+      SvRow row;
+      if (st.at >= keep) {
+        st.done = 1;
+      } else if (sv_test<DT>(p, b, st.at, h, wt, row)) {  // every wave for itself
+        if (first && p.logp) p.logp[b * (p.L + 1) + st.at] = sv_logp(wt, row.Z);
+        st.at = st.depth = step;
+      } else {
+        st.done = 2;
+      }
+    }
+  }
+  if (first) p.state[(int64_t)step * p.batch + b] = st;
+  if (st.done || (q && st.at >= keep)) return;
+  const int64_t row = b * (q ? p.T - 1 : p.T) + st.at;
+  sv_chunk<DT>(q ? p.draft : p.logits, row * p.V, p.V, c, h,
+               (q ? p.rec_q : p.rec) + ((int64_t)(step & 1) * p.batch + b) * p.S + c);
+}
+
+// Chains: the tests (all of them side by side, or stepped the last one), and
+// chunk sums of max(0, p - q) where a guess fell. Every workgroup of a request
+// forms the same state.
 template <int DT>
 __global__ __launch_bounds__(kSvThreads) void sv_chain_rest_kernel(SvParams p, int step) {
   constexpr int N = SvVec<DT>::N, NW = kSvThreads / kWave;
   __shared__ double s_s[NW];
+  __shared__ float s_logp[DDT_MAX_L];
+  __shared__ int s_ok[DDT_MAX_L];
   const int64_t b = blockIdx.x / p.S;
-  const int c = (int)(blockIdx.x - b * p.S), tid = threadIdx.x;
-  const SvState st = p.state[(int64_t)step * p.batch + b];
+  const int c = (int)(blockIdx.x - b * p.S), tid = threadIdx.x, wave = tid >> 6;
   const SvHeat h = sv_heat(p, b);
+  const int keep = sv_count(p, b);
+  SvState st{0, 0, 0, 0};
+  if (p.stepped) st = p.state[(int64_t)step * p.batch + b];
+  if (!st.done) {
+    const int i0 = p.stepped ? st.at : 0;
+    for (int i = i0 + (p.stepped ? 0 : wave); i < keep; i += p.stepped ? kSvMaxB : NW) {
+      double wt = 0.0;
+      SvRow row;
+      const bool ok = sv_test<DT>(p, b, i, h, wt, row);
+      if ((tid & 63) == 0) {
+        s_ok[i] = ok;
+        s_logp[i] = sv_logp(wt, row.Z);
+      }
+    }
+    __syncthreads();
+    int at = i0;
+    while (at < keep && s_ok[at]) ++at;
+    if (c == 0 && p.logp)
+      for (int i = i0 + tid; i < at; i += kSvThreads) p.logp[b * (p.L + 1) + i] = s_logp[i];
+    st.at = st.depth = at;
+    st.done = at < keep ? 2 : 1;
+  }
+  if (c == 0 && tid == 0) p.state[(int64_t)(p.L + 1) * p.batch + b] = st;
   if (st.done != 2 || h.greedy) return;
   const int64_t rp = (b * p.T + st.at) * p.V, rq = (b * (p.T - 1) + st.at) * p.V;
   const int off = (int)(rp & (N - 1));
@@ -692,7 +834,7 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_rest_kernel(SvParams p, i
                     sv_exp2(((double)y[i].at(e) - rowq.M) * h.s) * zq,
                 0.0);
   z = wave_sum(z);
-  if ((tid & 63) == 0) s_s[tid >> 6] = z;
+  if ((tid & 63) == 0) s_s[wave] = z;
   __syncthreads();
   if (tid == 0) {
     for (int i = 1; i < NW; ++i) z += s_s[i];
@@ -702,10 +844,11 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_rest_kernel(SvParams p, i
 
 // Chains: the next token.
 template <int DT>
-__global__ __launch_bounds__(kSvThreads) void sv_chain_finish_kernel(SvParams p, int step) {
-  __shared__ SvShared sh;
+__global__ __launch_bounds__(kSvFinish) void sv_chain_finish_kernel(SvParams p) {
+  constexpr int NT = kSvFinish;
+  __shared__ SvDraw<NT> dr;
   const int64_t b = blockIdx.x;
-  const SvState st = p.state[(int64_t)step * p.batch + b];
+  const SvState st = p.state[(int64_t)(p.L + 1) * p.batch + b];
   const SvHeat h = sv_heat(p, b);
   const int d = st.depth;
   const SvRec* rec = p.rec + sv_rec_at(p, b, st.at, d, p.T);
@@ -713,31 +856,31 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_finish_kernel(SvParams p,
   const int64_t rp = (b * p.T + st.at) * p.V;
   int token = -1;
   double w = 0.0;
-  if (row.greedy) {
+  if (row.Z > 0.0 && row.greedy) {
     token = row.arg;
     w = 1.0;
   } else if (row.Z > 0.0) {
     const double u = sv_uniform(p, b, p.L);
     if (st.done == 2) {
       const SvRow rowq = sv_combine(p.rec_q + sv_rec_at(p, b, st.at, d, p.T - 1), p.S, h);
-      for (int c = threadIdx.x; c < p.S; c += kSvThreads) sh.rest[c] = p.rest[b * p.S + c];
+      for (int c = threadIdx.x; c < p.S; c += NT) dr.rest[c] = p.rest[b * p.S + c];
       __syncthreads();
       double total = 0.0;
-      for (int c = 0; c < p.S; ++c) total += sh.rest[c];
+      for (int c = 0; c < p.S; ++c) total += dr.rest[c];
       if (total > 0.0 && rowq.Z > 0.0)
-        token = sv_draw<DT, true>(p, rp, (b * (p.T - 1) + st.at) * p.V, row, rowq, 0, u * total,
-                                  sh, w);
+        token = sv_draw<DT, true, NT>(p, rp, (b * (p.T - 1) + st.at) * p.V, row, rowq, nullptr, 0,
+                                      u * total, dr);
     }
     if (token < 0) {  // the whole chain stands, or p = q
       __syncthreads();
-      for (int c = threadIdx.x; c < p.S; c += kSvThreads)
-        sh.rest[c] = rec[c].sum * sv_exp2(((double)rec[c].mx - row.M) * row.s);
+      for (int c = threadIdx.x; c < p.S; c += NT)
+        dr.rest[c] = rec[c].sum * sv_exp2(((double)rec[c].mx - row.M) * row.s);
       __syncthreads();
-      token = sv_draw<DT, false>(p, rp, 0, row, row, 0, u * row.Z, sh, w);
+      token = sv_draw<DT, false, NT>(p, rp, 0, row, row, nullptr, 0, u * row.Z, dr);
     }
     if (token >= 0) w = row.weight(sv_logit<DT>(p.logits, rp, token), token);
   }
-  sv_tail<DT, true>(p, b, st, token, w, row.Z);
+  sv_tail<true>(p, b, d, token, w, row.Z);
 }
 
 }  // namespace ddt

@@ -626,7 +626,8 @@ int accept_launch(const SvPlan& pl, const ddt::SvParams& sp, hipStream_t st) {
     hipLaunchKernelGGL((ddt::sv_finish_kernel<DT>), each, finish, 0, st, sp, sp.L);
     return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
   }
-  hipLaunchKernelGGL((ddt::sv_chain_rest_kernel<DT>), dim3(chunks), block, 0, st, sp, sp.L);
+  hipLaunchKernelGGL((ddt::sv_chain_rest_kernel<DT>), dim3(chunks), dim3(ddt::kSvRest), 0, st, sp,
+                     sp.L);
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   hipLaunchKernelGGL((ddt::sv_chain_finish_kernel<DT>), each, finish, 0, st, sp);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;

@@ -168,14 +168,25 @@ __device__ __forceinline__ double sv_exp2_fast(double y) {
   return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, s) + k);
 }
 
-// Inclusive scan of one double per lane over the wave (every lane active).
+// Inclusive scan of one double per lane over the wave (every lane active), by
+// DPP as in wave_incl_scan.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double sv_shifted(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 __device__ __forceinline__ double wave_incl_scan_f64(double x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+  x += sv_shifted<0x111, 0xf>(x);
+  x += sv_shifted<0x112, 0xf>(x);
+  x += sv_shifted<0x114, 0xf>(x);
+  x += sv_shifted<0x118, 0xf>(x);
+  x += sv_shifted<0x142, 0xa>(x);
+  x += sv_shifted<0x143, 0xc>(x);
   return x;
 }
 
@@ -214,28 +225,43 @@ struct SvRow {
   }
 };
 
-// Combines a row's S records; every wave does it for itself.
-__device__ __forceinline__ SvRow sv_combine(const SvRec* rec, int S, const SvHeat& h) {
-  const int lane = threadIdx.x & 63;
+// Lanes that combine one row's records: 16, 32 or 64.
+__device__ __forceinline__ int sv_lanes(int S) { return S <= 16 ? 16 : (S <= 32 ? 32 : 64); }
+
+// Combines a row's S records by groups of `lanes` lanes, a row each.
+__device__ __forceinline__ SvRow sv_combine(const SvRec* rec, int S, const SvHeat& h, int lanes) {
+  const int l = threadIdx.x & (lanes - 1);
   float m = -INFINITY;
-  for (int c = lane; c < S; c += kWave) m = fmaxf(m, rec[c].mx);
-  m = wave_max(m);
-  double z = 0.0;
-  int arg = 0x7FFFFFFF;
-  for (int c = lane; c < S; c += kWave) {
-    const SvRec r = rec[c];
-    z += r.sum * sv_exp2(((double)r.mx - (double)m) * h.s);
+  SvRec r{0.0, -INFINITY, 0x7FFFFFFF};
+  if (l < S) r = rec[l];
+  m = r.mx;
+  for (int c = l + lanes; c < S; c += lanes) m = fmaxf(m, rec[c].mx);
+  for (int d = 1; d < lanes; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const bool any = m > -INFINITY;
+  double z = any ? r.sum * sv_exp2(((double)r.mx - (double)m) * h.s) : 0.0;
+  int arg = r.mx == m ? r.arg : 0x7FFFFFFF;
+  for (int c = l + lanes; c < S; c += lanes) {
+    r = rec[c];
+    if (any) z += r.sum * sv_exp2(((double)r.mx - (double)m) * h.s);
     if (r.mx == m && r.arg < arg) arg = r.arg;
+  }
+  for (int d = 1; d < lanes; d <<= 1) {
+    z += __shfl_xor(z, d);
+    const int o = __shfl_xor(arg, d);
+    arg = o < arg ? o : arg;
   }
   SvRow row;
   row.M = (double)m;
   row.s = h.s;
   row.greedy = h.greedy;
-  const bool any = m > -INFINITY;
-  z = wave_sum(z);
   row.Z = !any ? 0.0 : (h.greedy ? 1.0 : z);
-  row.arg = any && h.greedy ? wave_min(arg) : -1;
+  row.arg = any && h.greedy ? arg : -1;
   return row;
+}
+
+// The same by every wave for itself.
+__device__ __forceinline__ SvRow sv_combine(const SvRec* rec, int S, const SvHeat& h) {
+  return sv_combine(rec, S, h, sv_lanes(S));
 }
 
 // This thread's part of a chunk's sum of weights against its maximum m.
@@ -346,8 +372,8 @@ __device__ __forceinline__ int64_t sv_rec_at(const SvParams& p, int64_t b, int a
 // node that cannot be accepted has none.
 constexpr uint32_t kSvNoKey = 0xFFFFFFFFu;
 
-__device__ __forceinline__ uint32_t sv_key(const SvParams& p, int64_t b, int j, int n) {
-  if (j >= n) return kSvNoKey;
+__device__ __forceinline__ uint32_t sv_key(const SvParams& p, int64_t b, int j) {
+  if (j >= p.T - 1) return kSvNoKey;
   const int par = p.parents[b * (p.T - 1) + j], tok = p.tokens[b * (p.T - 1) + j];
   if (par < 0 || par > j || tok < 0 || tok >= p.V) return kSvNoKey;
   return (uint32_t)par << 22 | (uint32_t)tok;
@@ -357,33 +383,17 @@ __device__ __forceinline__ uint32_t sv_key(const SvParams& p, int64_t b, int j, 
 struct SvTree {
   uint32_t key[kSvMaxB];
   double w[kSvMaxB];  // weight of the node's token in its parent's row
-  // the decision: child hit (-1: none), all children's weight, their count and
-  // tokens
+  // the decision: child hit (-1: none), all children's weight, and the
+  // children that take a part of the line: their tokens and weights
   int pick, kids;
   double edge;
   int tok[kSvMaxB];
+  double part[kSvMaxB];
 };
 
-// Keys whose token an earlier sibling carries already take no second part of
-// the line. Every thread calls it; keys and a barrier before, a barrier after.
-template <int NT>
-__device__ __forceinline__ void sv_unique(SvTree& t, int n) {
-  bool dup[kSvMaxB / NT > 0 ? kSvMaxB / NT : 1];
-#pragma unroll
-  for (int q = 0; q < (kSvMaxB + NT - 1) / NT; ++q) {
-    const int j = threadIdx.x + q * NT;
-    dup[q] = false;
-    if (j < n && t.key[j] != kSvNoKey)
-      for (int i = 0; i < j; ++i) dup[q] |= t.key[i] == t.key[j];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < (kSvMaxB + NT - 1) / NT; ++q)
-    if (dup[q]) t.key[threadIdx.x + q * NT] = kSvNoKey;
-}
-
 // Where position `at` of the line falls at a node, by one wave: t.pick,
-// t.edge and, for the draw after it, the children's tokens.
+// t.edge and, for the draw after it, the children's parts. A token that an
+// earlier sibling carries already takes no second part.
 __device__ __forceinline__ void sv_hit(SvTree& t, int node, int n, double at) {
   const int lane = threadIdx.x & 63;
   double base = 0.0;
@@ -391,14 +401,25 @@ __device__ __forceinline__ void sv_hit(SvTree& t, int node, int n, double at) {
   for (int j0 = 0; j0 < n; j0 += kWave) {
     const int j = j0 + lane;
     const uint32_t key = j < n ? t.key[j] : kSvNoKey;
-    const bool kid = key != kSvNoKey && (int)(key >> 22) == node;
-    const uint64_t kids = __ballot(kid);
+    bool kid = key != kSvNoKey && (int)(key >> 22) == node;
+    uint64_t kids = __ballot(kid);
     if (!kids) continue;
-    const double cum = base + wave_incl_scan_f64(kid ? t.w[j] : 0.0);
+    const int tok = (int)(key & 0x3FFFFFu);
+    for (int i = 0; i < kept; ++i) kid = kid && t.tok[i] != tok;
+    for (uint64_t left = kids; left & (left - 1); left &= left - 1) {
+      const int l = __builtin_ctzll(left);
+      kid = kid && (lane <= l || tok != __builtin_amdgcn_readlane(tok, l));
+    }
+    kids = __ballot(kid);
+    const double w = kid ? t.w[j] : 0.0;
+    const double cum = base + wave_incl_scan_f64(w);
     const uint64_t hit = __ballot(kid && at < cum);
-    if (kid) t.tok[kept + lanes_below(kids)] = (int)(key & 0x3FFFFFu);
+    if (kid) {
+      t.tok[kept + lanes_below(kids)] = tok;
+      t.part[kept + lanes_below(kids)] = w;
+    }
     kept += __popcll(kids);
-    base = __shfl(cum, 63);
+    base = lane_value(cum, 63);
     if (hit) {
       pick = j0 + __builtin_ctzll(hit);
       break;
@@ -422,10 +443,10 @@ __global__ __launch_bounds__(kSvThreads) void sv_step_kernel(SvParams p, int ste
   SvState st{0, 0, 0, 0};
   if (step > 0) {
     const int d = step - 1;
-    const int n = d < p.L ? sv_count(p, b) : 0;
-    const uint32_t k0 = sv_key(p, b, tid, n), k1 = sv_key(p, b, tid + kSvThreads, n);
     st = p.state[(int64_t)d * p.batch + b];
     if (!st.done) {
+      const uint32_t k0 = sv_key(p, b, tid), k1 = sv_key(p, b, tid + kSvThreads);
+      const int n = d < p.L ? sv_count(p, b) : 0;
       // the node's children
       const int64_t r0 = (b * p.T + st.at) * p.V;
       const bool kid0 = k0 != kSvNoKey && (int)(k0 >> 22) == st.at;
@@ -438,8 +459,6 @@ __global__ __launch_bounds__(kSvThreads) void sv_step_kernel(SvParams p, int ste
       sh.key[tid + kSvThreads] = kid1 ? k1 : kSvNoKey;
       sh.w[tid] = kid0 ? row.weight(x0, t0) : 0.0;
       sh.w[tid + kSvThreads] = kid1 ? row.weight(x1, t1) : 0.0;
-      __syncthreads();
-      sv_unique<kSvThreads>(sh, n);
       __syncthreads();
       if (tid < kWave) sv_hit(sh, st.at, n, sv_uniform(p, b, d) * row.Z);
       __syncthreads();
@@ -628,8 +647,9 @@ __global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int st
   const int64_t b = blockIdx.x;
   const int tid = threadIdx.x;
   const SvHeat h = sv_heat(p, b);
+  uint32_t key = sv_key(p, b, tid);
   const int count = sv_count(p, b);
-  uint32_t key = sv_key(p, b, tid, count);
+  if (tid >= count) key = kSvNoKey;
   int node = 0, d = 0;
   if (p.stepped) {
     const SvState st = p.state[(int64_t)step * p.batch + b];
@@ -641,15 +661,18 @@ __global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int st
   const int par = (int)(key >> 22), tok = (int)(key & 0x3FFFFFu);
   const float x = key != kSvNoKey ? sv_logit<DT>(p.logits, (b * p.T + par) * p.V, tok) : 0.0f;
   if (tid < kSvMaxB) sh.key[tid] = key;
-  // the rows' maxima and sums: a wave takes a row (stepped: the node's only)
-  for (int r = p.stepped ? node : tid >> 6; r <= (p.stepped ? node : count); r += NT / kWave) {
-    const SvRow row = sv_combine(p.rec + sv_rec_at(p, b, r, d, p.T), p.S, h);
-    if ((tid & 63) == 0) {
+  // the rows' maxima and sums: a group of lanes takes a row (stepped: the
+  // node's only)
+  const int lanes = sv_lanes(p.S), first = p.stepped ? node : 0, end = p.stepped ? node : count;
+  for (int r0 = first; r0 <= end; r0 += NT / lanes) {  // uniform
+    const int r = r0 + tid / lanes;
+    const SvRow row =
+        sv_combine(p.rec + sv_rec_at(p, b, r <= end ? r : end, d, p.T), p.S, h, lanes);
+    if (r <= end && (tid & (lanes - 1)) == 0) {
       s_Z[r] = row.Z;
       s_M[r] = (float)row.M;
       s_arg[r] = row.arg;
     }
-    if (p.stepped) break;
   }
   __syncthreads();
   auto row_of = [&](int r) {
@@ -662,7 +685,6 @@ __global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int st
     return row;
   };
   if (tid < kSvMaxB) sh.w[tid] = key != kSvNoKey ? row_of(par).weight(x, tok) : 0.0;
-  sv_unique<NT>(sh, count);
   __syncthreads();
   if (tid < kWave) {
     for (;;) {
@@ -701,12 +723,8 @@ __global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int st
     const double at = sv_uniform(p, b, d) * row.Z - sh.edge;
     for (int c = tid; c < p.S; c += NT) {
       double s = rec[c].sum * sv_exp2(((double)rec[c].mx - row.M) * row.s);
-      for (int j = 0; j < count && n > 0; ++j) {
-        const uint32_t k = sh.key[j];
-        if (k != kSvNoKey && (int)(k >> 22) == node &&
-            ((int)(k & 0x3FFFFFu) + off) / (kSvThreads * kSvVecs * N) == c)
-          s -= sh.w[j];
-      }
+      for (int j = 0; j < n; ++j)
+        if ((sh.tok[j] + off) / (kSvThreads * kSvVecs * N) == c) s -= sh.part[j];
       dr.rest[c] = fmax(s, 0.0);
     }
     __syncthreads();
@@ -717,30 +735,30 @@ __global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int st
 }
 
 // ---- chains ----------------------------------------------------------------------
-// A chain's test of guess i: true where it stands. wt: its weight.
+// The tests of guesses, a pair of lane groups each: even groups combine the
+// target's row, odd ones the drafter's, and both form the test. i: this pair's
+// guess (an existing one).
 template <int DT>
-__device__ bool sv_stands(const SvParams& p, int64_t b, int i, int token, float xp, float xq,
-                          const SvRow& row, const SvRow& rowq, double& wt) {
-  wt = 0.0;
-  if (token < 0 || token >= p.V) return false;
-  const double wp = row.weight(xp, token), wq = rowq.weight(xq, token);
-  wt = wp;
-  // (a drafter's row with every token masked has q = 0)
-  return sv_uniform(p, b, i) * wq * row.Z < wp * (rowq.Z > 0.0 ? rowq.Z : 1.0);
-}
-
-// Guess i's test by one wave.
-template <int DT>
-__device__ bool sv_test(const SvParams& p, int64_t b, int i, const SvHeat& h, double& wt,
+__device__ bool sv_test(const SvParams& p, int64_t b, int i, const SvHeat& h, int lanes, double& wt,
                         SvRow& row) {
   const int P = p.T - 1;
+  const bool q = (threadIdx.x / lanes) & 1;
   const int token = p.tokens[b * P + i];
   const bool in = token >= 0 && token < p.V;
-  const float xp = in ? sv_logit<DT>(p.logits, (b * p.T + i) * p.V, token) : 0.0f;
-  const float xq = in ? sv_logit<DT>(p.draft, (b * P + i) * p.V, token) : 0.0f;
-  row = sv_combine(p.rec + sv_rec_at(p, b, i, i, p.T), p.S, h);
-  const SvRow rowq = sv_combine(p.rec_q + sv_rec_at(p, b, i, i, P), p.S, h);
-  return sv_stands<DT>(p, b, i, token, xp, xq, row, rowq, wt);
+  const float x = !in ? 0.0f
+                  : q ? sv_logit<DT>(p.draft, (b * P + i) * p.V, token)
+                      : sv_logit<DT>(p.logits, (b * p.T + i) * p.V, token);
+  const SvRow mine = sv_combine(q ? p.rec_q + sv_rec_at(p, b, i, i, P)
+                                  : p.rec + sv_rec_at(p, b, i, i, p.T),
+                                p.S, h, lanes);
+  const double w = in ? mine.weight(x, token) : 0.0;
+  const double wo = __shfl_xor(w, lanes), Zo = __shfl_xor(mine.Z, lanes);
+  const double wp = q ? wo : w, wq = q ? w : wo, Zp = q ? Zo : mine.Z, Zq = q ? mine.Z : Zo;
+  wt = wp;
+  row = mine;
+  row.Z = Zp;
+  // (a drafter's row with every token masked has q = 0)
+  return in && sv_uniform(p, b, i) * wq * Zp < wp * (Zq > 0.0 ? Zq : 1.0);
 }
 
 // One step of a chain for every request: the test of the guess whose rows'
@@ -753,6 +771,7 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_step_kernel(SvParams p, i
   if (q) c -= p.S;
   const SvHeat h = sv_heat(p, b);
   const int keep = sv_count(p, b);
+  const int pair = p.S <= 16 ? 16 : 32;  // two groups to a wave at least
   SvState st{0, 0, 0, 0};
   if (step > 0) {
     st = p.state[(int64_t)(step - 1) * p.batch + b];
@@ -761,7 +780,7 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_step_kernel(SvParams p, i
       SvRow row;
       if (st.at >= keep) {
         st.done = 1;
-      } else if (sv_test<DT>(p, b, st.at, h, wt, row)) {  // every wave for itself
+      } else if (sv_test<DT>(p, b, st.at, h, pair, wt, row)) {  // every pair the same
         if (first && p.logp) p.logp[b * (p.L + 1) + st.at] = sv_logp(wt, row.Z);
         st.at = st.depth = step;
       } else {
@@ -779,9 +798,11 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_step_kernel(SvParams p, i
 // Chains: the tests (all of them side by side, or stepped the last one), and
 // chunk sums of max(0, p - q) where a guess fell. Every workgroup of a request
 // forms the same state.
+constexpr int kSvRest = 512;
+
 template <int DT>
-__global__ __launch_bounds__(kSvThreads) void sv_chain_rest_kernel(SvParams p, int step) {
-  constexpr int N = SvVec<DT>::N, NW = kSvThreads / kWave;
+__global__ __launch_bounds__(kSvRest) void sv_chain_rest_kernel(SvParams p, int step) {
+  constexpr int N = SvVec<DT>::N, NW = kSvRest / kWave, VECS = kSvThreads * kSvVecs / kSvRest;
   __shared__ double s_s[NW];
   __shared__ float s_logp[DDT_MAX_L];
   __shared__ int s_ok[DDT_MAX_L];
@@ -792,21 +813,26 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_rest_kernel(SvParams p, i
   SvState st{0, 0, 0, 0};
   if (p.stepped) st = p.state[(int64_t)step * p.batch + b];
   if (!st.done) {
+    const int lanes = p.S <= 16 ? 16 : 32, pairs = kSvRest / (2 * lanes);
+    const int g = tid / (2 * lanes);
     const int i0 = p.stepped ? st.at : 0;
-    for (int i = i0 + (p.stepped ? 0 : wave); i < keep; i += p.stepped ? kSvMaxB : NW) {
+    // (stepped: the guess at the state's own row, whose records alone are there)
+    const int end = p.stepped && i0 < keep ? i0 + 1 : keep;
+    for (int j = i0; j < end; j += pairs) {  // uniform
+      const int i = j + g < end ? j + g : end - 1;
       double wt = 0.0;
       SvRow row;
-      const bool ok = sv_test<DT>(p, b, i, h, wt, row);
-      if ((tid & 63) == 0) {
+      const bool ok = sv_test<DT>(p, b, i, h, lanes, wt, row);
+      if ((tid & (2 * lanes - 1)) == 0 && j + g < end) {
         s_ok[i] = ok;
         s_logp[i] = sv_logp(wt, row.Z);
       }
     }
     __syncthreads();
     int at = i0;
-    while (at < keep && s_ok[at]) ++at;
+    while (at < end && s_ok[at]) ++at;
     if (c == 0 && p.logp)
-      for (int i = i0 + tid; i < at; i += kSvThreads) p.logp[b * (p.L + 1) + i] = s_logp[i];
+      for (int i = i0 + tid; i < at; i += kSvRest) p.logp[b * (p.L + 1) + i] = s_logp[i];
     st.at = st.depth = at;
     st.done = at < keep ? 2 : 1;
   }
@@ -815,24 +841,36 @@ __global__ __launch_bounds__(kSvThreads) void sv_chain_rest_kernel(SvParams p, i
   const int64_t rp = (b * p.T + st.at) * p.V, rq = (b * (p.T - 1) + st.at) * p.V;
   const int off = (int)(rp & (N - 1));
   const int64_t v0 = (int64_t)c * kSvThreads * kSvVecs;
-  SvVec<DT> x[kSvVecs], y[kSvVecs];
+  SvVec<DT> x[VECS], y[VECS];
 #pragma unroll
-  for (int i = 0; i < kSvVecs; ++i) {
-    const int64_t e0 = (v0 + i * kSvThreads + tid) * N - off;
+  for (int i = 0; i < VECS; ++i) {
+    const int64_t e0 = (v0 + i * kSvRest + tid) * N - off;
     x[i] = sv_load<DT>(p.logits, rp, e0, p.V);
     y[i] = sv_load<DT>(p.draft, rq, e0, p.V);
   }
   const SvRow row = sv_combine(p.rec + sv_rec_at(p, b, st.at, st.depth, p.T), p.S, h);
   const SvRow rowq = sv_combine(p.rec_q + sv_rec_at(p, b, st.at, st.depth, p.T - 1), p.S, h);
   const double zp = 1.0 / row.Z, zq = 1.0 / rowq.Z;
+  const double mp = row.M * h.s, mq = rowq.M * h.s;
   double z = 0.0;
+  if (fabs(mp) < 1024.0 && fabs(mq) < 1024.0) {
+    // as in sv_sum; a pair of least weights (2^-1000) adds nothing
 #pragma unroll
-  for (int i = 0; i < kSvVecs; ++i)
+    for (int i = 0; i < VECS; ++i)
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      z += fmax(sv_exp2(((double)x[i].at(e) - row.M) * h.s) * zp -
-                    sv_exp2(((double)y[i].at(e) - rowq.M) * h.s) * zq,
-                0.0);
+      for (int e = 0; e < N; ++e)
+        z += fmax(sv_exp2_fast(fma((double)x[i].raw(e), h.s, -mp)) * zp -
+                      sv_exp2_fast(fma((double)y[i].raw(e), h.s, -mq)) * zq,
+                  0.0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        z += fmax(sv_exp2(((double)x[i].at(e) - row.M) * h.s) * zp -
+                      sv_exp2(((double)y[i].at(e) - rowq.M) * h.s) * zq,
+                  0.0);
+  }
   z = wave_sum(z);
   if ((tid & 63) == 0) s_s[wave] = z;
   __syncthreads();

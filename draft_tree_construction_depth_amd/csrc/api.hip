@@ -587,8 +587,11 @@ SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bo
   SvPlan pl;
   pl.S = (int)((V + (V % N ? N - 1 : 0) + chunk - 1) / chunk);
   const int64_t rows = batch * T + (chain ? batch * (T - 1) : 0);
-  // Many rows: only the path's, one launch for each depth.
-  pl.stepped = rows * V * (int64_t)elem_size(dtype) > (L + 1) * ((int64_t)12 << 20);
+  // Many rows: only the path's, one launch for each depth (about 8 us each, the
+  // time of some 24 MB of rows). Trees of 65 rows of 152 k bf16 at L = 15: 8
+  // requests (10 MB a depth) 68 us for all rows, 115 us stepped; 16 (20 MB) 118
+  // and 123; 64 (79 MB) 376 and 150; at L = 5 8 requests (26 MB) 62 and 52.
+  pl.stepped = rows * V * (int64_t)elem_size(dtype) > (L + 1) * ((int64_t)24 << 20);
   const size_t rec = sizeof(ddt::SvRec);
   size_t o = 0;
   pl.rec = o;
@@ -896,10 +899,16 @@ int ddtree_compact_kv_paged(void* k_cache, void* v_cache, int64_t layers, int64_
   if (chk != DDT_OK) return chk;
   if (row_bytes % 16 != 0 || row_bytes > 1024 || L > DDT_MAX_L) return DDT_ENOTSUP;
   const int64_t per_block = ddt::kKvThreads / ddt::kWave;
-  if (batch > 0x7FFFFFFFLL || layers > 0x7FFFFFFFLL / batch ||
-      (layers * batch) > 0x7FFFFFFFLL * per_block / heads)
-    return DDT_ENOTSUP;
-  const int64_t blocks = (layers * batch * heads + per_block - 1) / per_block;
+  if (batch > 0x7FFFFFFFLL || layers > 0x7FFFFFFFLL / heads) return DDT_ENOTSUP;
+  const int64_t slices = layers * heads;
+  // one wave for each slice (layer and head) of a request until they fill the
+  // card, then up to 16 slices to a wave, which find the rows' pages once
+  int64_t each = slices * batch / 4096;
+  each = each < 1 ? 1 : (each > 16 ? 16 : each);
+  kp.waves = (int32_t)((slices + each - 1) / each);
+  kp.each = (int32_t)each;
+  if (batch > 0x7FFFFFFFLL / kp.waves) return DDT_ENOTSUP;
+  const int64_t blocks = (batch * kp.waves + per_block - 1) / per_block;
   kp.k = (unsigned char*)k_cache;
   kp.v = (unsigned char*)v_cache;
   kp.layers = layers;

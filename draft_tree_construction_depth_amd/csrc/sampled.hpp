@@ -34,8 +34,8 @@
 namespace ddt {
 
 constexpr int kSvThreads = 256;
-constexpr int kSvVecs = 8;       // 16-byte vectors per thread and chunk
-constexpr int kSvMaxS = 512;     // chunks per row
+constexpr int kSvVecs = 4;       // 16-byte vectors per thread and chunk
+constexpr int kSvMaxS = 1024;    // chunks per row
 constexpr int kSvMaxB = 512;     // nodes
 constexpr int kSvChunkMax = kSvThreads * kSvVecs * 8;  // elements (bf16)
 constexpr int kSvFinish = 1024;  // threads of the launches that end a walk

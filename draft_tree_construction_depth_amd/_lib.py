@@ -492,12 +492,12 @@ def _half_code(dtype) -> int:
 
 
 def _dev_arg(t, name, dtype, shape, dev):
-    """Device pointer of a contiguous tensor of this dtype and shape on device dev."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and \
-            t.device == dev and t.is_contiguous():
+    """Device pointer of a contiguous tensor of this dtype and shape on device number dev."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == dtype and \
+            t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     _arg(t, name, (dtype,), shape)
-    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    raise ValueError(f"{name} must be on device {dev}, got {t.device}")
 
 
 def _maybe_arg(t, name, dtype, shape, dev):
@@ -512,13 +512,13 @@ def _ws_arg(kind, size, ws, dev):
     if ws is not None:
         if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
             raise ValueError("ws must be a contiguous device tensor")
-        if ws.device != dev:
-            raise ValueError(f"ws must be on {dev}, got {ws.device}")
+        if ws.get_device() != dev:
+            raise ValueError(f"ws must be on device {dev}, got {ws.device}")
         return ws.data_ptr(), ws, ws.numel() * ws.element_size()
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
     else:
-        key = (kind, dev.index, _raw_stream(dev.index))
+        key = (kind, dev, _raw_stream(dev))
         ws = _workspaces.get(key)
         if ws is None or ws.numel() < size:
             ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
@@ -526,19 +526,20 @@ def _ws_arg(kind, size, ws, dev):
     return ws.data_ptr(), ws, ws.numel()
 
 
-class _OnDevice:
-    """Makes a device the current one if it is not: launches go to the current device."""
-
-    def __init__(self, dev):
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _call(name, dev, args, kind=None, size=0, ws=None):
+    """Calls the library with args, the workspace of `kind` if there is one and device dev's
+    current stream, dev being the current device meanwhile; raises on an error status."""
+    if torch.cuda.current_device() != dev:  # launches go to the current device
+        with torch.cuda.device(dev):
+            return _call(name, dev, args, kind, size, ws)
+    fn = getattr(lib(), name)
+    if kind is None:
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        wp, ws, size = _ws_arg(kind, size, ws, dev)
+        rc = fn(*args, wp, size, _raw_stream(dev))
+    if rc:
+        _check(name, rc)
 
 
 def _block_rows(t, name, dtype, batch, T, dh, dev):
@@ -547,13 +548,12 @@ def _block_rows(t, name, dtype, batch, T, dh, dev):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor (on the caches' device)")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [batch, T, heads, head_dim]")
-    b, n, heads, d = t.shape
-    if b != batch or n != T or d != dh:
-        raise ValueError(f"{name} must have shape ({batch}, {T}, heads, {dh}), got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev} like the caches, got {t.device}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != batch or shape[1] != T or shape[3] != dh:
+        raise ValueError(f"{name} must have shape ({batch}, {T}, heads, {dh}), got {tuple(shape)}")
+    heads = shape[2]
     s0, s1, s2, s3 = t.stride()
     step = s1 if T > 1 else (s0 if batch > 1 else heads * dh)
     if (s3 != 1 and dh > 1) or (heads > 1 and s2 != dh) or (batch > 1 and s0 != T * step):
@@ -563,25 +563,26 @@ def _block_rows(t, name, dtype, batch, T, dh, dev):
 
 def _paged_cache(k_cache, v_cache, page_table, batch, dims):
     """Check a cache [(layers,) pages, kv_heads, page_size, head_dim] and its page
-    table [batch, width]; (pointers, shape, width)."""
+    table [batch, width]; (pointers, shape, width, device number)."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != dims:
         raise ValueError(f"k_cache must be a {dims}-d tensor "
                          f"[{'layers, ' if dims == 5 else ''}pages, kv_heads, page_size, head_dim]")
-    shape, dev = k_cache.shape, k_cache.device
-    k = _dev_arg(k_cache, "k_cache", k_cache.dtype, shape, dev)
-    if not k_cache.is_cuda:
+    shape, dev, dtype = k_cache.shape, k_cache.get_device(), k_cache.dtype
+    if dev < 0:
         raise ValueError("k_cache must be a device tensor")
-    v = _dev_arg(v_cache, "v_cache", k_cache.dtype, shape, dev)
+    k = _dev_arg(k_cache, "k_cache", dtype, shape, dev)
+    v = _dev_arg(v_cache, "v_cache", dtype, shape, dev)
     if page_table is None:
         if shape[-4] != batch:
             raise ValueError(f"without a page table the cache must hold one page per request "
                              f"({batch}), got {shape[-4]}")
-        return k, v, None, shape, 1
+        return k, v, None, shape, 1, dev
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or \
             page_table.shape[0] != batch:
         raise ValueError(f"page_table must be a tensor of shape ({batch}, width)")
-    width = page_table.shape[1]
-    return k, v, _dev_arg(page_table, "page_table", torch.int32, (batch, width), dev), shape, width
+    table = page_table.shape
+    return (k, v, _dev_arg(page_table, "page_table", torch.int32, table, dev), shape, table[1],
+            dev)
 
 
 def ddtree_append_kv(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -599,8 +600,7 @@ def ddtree_append_kv(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     if dt not in _HALF:
         raise TypeError(f"k must have dtype {' or '.join(map(str, _HALF))}, got {dt}")
     batch, T, _, dh = k.shape
-    kc, vc, table, shape, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
-    dev = k_cache.device
+    kc, vc, table, shape, width, dev = _paged_cache(k_cache, v_cache, page_table, batch, 4)
     if k_cache.dtype != dt:
         raise TypeError(f"k_cache must have dtype {dt}, got {k_cache.dtype}")
     kp, kv_heads, ks = _block_rows(k, "k", dt, batch, T, dh, dev)
@@ -627,10 +627,7 @@ def ddtree_append_kv(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
             _maybe_arg(depths, "depths", torch.int32, (batch, T - 1), dev),
             _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev), table, width, pages,
             page_size, kc, vc, qo)
-    with _OnDevice(dev):
-        rc = lib().ddtree_append_kv(*args, _raw_stream(dev.index))
-    if rc:
-        _check("ddtree_append_kv", rc)
+    _call("ddtree_append_kv", dev, args)
     return q_out
 
 
@@ -653,8 +650,7 @@ def ddtree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if dt not in _HALF:
         raise TypeError(f"q must have dtype {' or '.join(map(str, _HALF))}, got {dt}")
     batch, T, q_heads, dh = q.shape
-    kc, vc, table, shape, width = _paged_cache(k_cache, v_cache, page_table, batch, 4)
-    dev = k_cache.device
+    kc, vc, table, shape, width, dev = _paged_cache(k_cache, v_cache, page_table, batch, 4)
     qp = _dev_arg(q, "q", dt, q.shape, dev)
     if k_cache.dtype != dt:
         raise TypeError(f"k_cache must have dtype {dt}, got {k_cache.dtype}")
@@ -665,21 +661,15 @@ def ddtree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         out = {"out": torch.empty_like(q)}
         if with_lse:
             out["lse"] = torch.empty((batch, T, q_heads), dtype=torch.float32, device=dev)
-    args = (_dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+    args = (qp, _half_code(dt), batch, T, q_heads, kv_heads, dh, kc, vc, table, width, pages,
+            page_size, _dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
             _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev),
             _maybe_arg(mask, "mask", torch.int64, (batch, T, (T + 63) // 64), dev),
             dh ** -0.5 if scale is None else float(scale),
             _dev_arg(out["out"], "out", dt, q.shape, dev),
             _maybe_arg(out.get("lse"), "lse", torch.float32, (batch, T, q_heads), dev))
-    with _OnDevice(dev):
-        size = 0 if ws is not None else _attention_ws(batch, T, q_heads, kv_heads, dh, width,
-                                                      page_size)
-        wp, ws, size = _ws_arg("attention", size, ws, dev)
-        rc = lib().ddtree_attention(qp, _half_code(dt), batch, T, q_heads, kv_heads, dh, kc, vc,
-                                    table, width, pages, page_size, *args, wp, size,
-                                    _raw_stream(dev.index))
-    if rc:
-        _check("ddtree_attention", rc)
+    size = _attention_ws(batch, T, q_heads, kv_heads, dh, width, page_size)
+    _call("ddtree_attention", dev, args, "attention", size, ws)
     return out
 
 
@@ -694,8 +684,7 @@ def ddtree_compact_kv_paged(k_cache: torch.Tensor, v_cache: torch.Tensor,
     batch = past_len.shape[0]
     if page_table is None:
         raise ValueError("page_table is required; ddtree_compact_kv takes contiguous caches")
-    kc, vc, table, shape, width = _paged_cache(k_cache, v_cache, page_table, batch, 5)
-    dev = k_cache.device
+    kc, vc, table, shape, width, dev = _paged_cache(k_cache, v_cache, page_table, batch, 5)
     layers, pages, heads, page_size, dh = shape
     if not isinstance(accepted_nodes, torch.Tensor) or accepted_nodes.dim() != 2:
         raise ValueError("accepted_nodes must be [batch, L]")
@@ -706,12 +695,9 @@ def ddtree_compact_kv_paged(k_cache: torch.Tensor, v_cache: torch.Tensor,
             _dev_arg(accepted_nodes, "accepted_nodes", torch.int32, (batch, L), dev),
             _dev_arg(accept_len, "accept_len", torch.int32, (batch,), dev), L,
             _dev_arg(new_len, "new_len", torch.int32, (batch,), dev))
-    with _OnDevice(dev):
-        rc = lib().ddtree_compact_kv_paged(kc, vc, layers, pages, heads, page_size,
+    _call("ddtree_compact_kv_paged", dev, (kc, vc, layers, pages, heads, page_size,
                                            dh * k_cache.element_size(), table, width, batch,
-                                           *args, _raw_stream(dev.index))
-    if rc:
-        _check("ddtree_compact_kv_paged", rc)
+                                           *args))
     return new_len
 
 
@@ -741,7 +727,7 @@ def ddtree_accept_sampled(tree_tokens: torch.Tensor, parents: torch.Tensor,
     accept_len, next_token, logp [batch, L+1]."""
     _arg(target_logits, "target_logits", _LOGITS)
     B = _rows_arg(tree_tokens, "tree_tokens", None)
-    batch, V, dev = tree_tokens.shape[0], target_logits.shape[-1], target_logits.device
+    batch, V, dev = tree_tokens.shape[0], target_logits.shape[-1], target_logits.get_device()
     L = _rows_arg(u, "u", batch) - 1
     dt = DDT_BF16 if target_logits.dtype == torch.bfloat16 else DDT_F32
     if out is None:
@@ -759,12 +745,7 @@ def ddtree_accept_sampled(tree_tokens: torch.Tensor, parents: torch.Tensor,
             _dev_arg(out["accept_len"], "accept_len", torch.int32, (batch,), dev),
             _dev_arg(out["next_token"], "next_token", torch.int32, (batch,), dev),
             _maybe_arg(out.get("logp"), "logp", torch.float32, (batch, L + 1), dev))
-    with _OnDevice(dev):
-        size = 0 if ws is not None else _accept_ws(batch, B, L, V, dt)
-        wp, ws, size = _ws_arg("accept_sampled", size, ws, dev)
-        rc = lib().ddtree_accept_sampled(*args, wp, size, _raw_stream(dev.index))
-    if rc:
-        _check("ddtree_accept_sampled", rc)
+    _call("ddtree_accept_sampled", dev, args, "accept_sampled", _accept_ws(batch, B, L, V, dt), ws)
     return out
 
 
@@ -777,7 +758,7 @@ def dspark_accept_sampled(tokens: torch.Tensor, target_logits: torch.Tensor,
     [batch, P+1] uniforms, keep [batch] -> accept_len, next_token, logp [batch, P+1]."""
     _arg(target_logits, "target_logits", _LOGITS)
     P = _rows_arg(tokens, "tokens", None)
-    batch, V, dev = tokens.shape[0], target_logits.shape[-1], target_logits.device
+    batch, V, dev = tokens.shape[0], target_logits.shape[-1], target_logits.get_device()
     dt = DDT_BF16 if target_logits.dtype == torch.bfloat16 else DDT_F32
     if out is None:
         i32 = torch.empty((2, batch), dtype=torch.int32, device=dev)
@@ -792,10 +773,6 @@ def dspark_accept_sampled(tokens: torch.Tensor, target_logits: torch.Tensor,
             _dev_arg(out["accept_len"], "accept_len", torch.int32, (batch,), dev),
             _dev_arg(out["next_token"], "next_token", torch.int32, (batch,), dev),
             _maybe_arg(out.get("logp"), "logp", torch.float32, (batch, P + 1), dev))
-    with _OnDevice(dev):
-        size = 0 if ws is not None else _chain_ws(batch, P, V, dt)
-        wp, ws, size = _ws_arg("chain_accept_sampled", size, ws, dev)
-        rc = lib().dspark_accept_sampled(*args, wp, size, _raw_stream(dev.index))
-    if rc:
-        _check("dspark_accept_sampled", rc)
+    _call("dspark_accept_sampled", dev, args, "chain_accept_sampled", _chain_ws(batch, P, V, dt),
+          ws)
     return out

@@ -491,11 +491,18 @@ AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_he
                         int32_t head_dim, int64_t cap) {
   AttnPlan pl;
   const int G = q_heads / kv_heads;
-  // up to 64 query rows of a key/value head: 16 to a wave, as many waves side
-  // by side as they fill (at head_dim 256 two or more: four groups' tiles
-  // would not leave registers for the next ones); more: 32 to a wave
+  // M query rows share a key/value head's pass. Up to 64: 16 to a wave, as many
+  // waves side by side as they fill; more: 32 to a wave (at head_dim 256 always
+  // 16, and two waves or more: 32 queries' state or four groups' tiles would
+  // not leave registers for the next tile). 32 requests x 4 heads over 4096
+  // rows, us at 16x1 / 16x2 / 16x4 / 32x4 queries x waves:
+  //   head_dim 128  M = 16: 63 / 66 / 71 / 79   32: 64 / 65 / 70 / 78
+  //                 64: 88 / 73 / 70 / 81       256: 248 / 191 / 136 / 114
+  //   head_dim 64   M = 16: 36 / 38 / 38 / 41   64: 53 / 47 / 41 / 44
+  //                 128: 85 / 71 / 53 / 55      256: 130 / 95 / 82 / 70
+  //   head_dim 256  M = 16: - / 135 / 147 / 276 128: - / 295 / 209 / 323
   const int64_t M = (int64_t)T * G;
-  pl.NQ = M <= 64 ? 16 : 32;
+  pl.NQ = M <= 64 || head_dim == 256 ? 16 : 32;
   pl.QW = M <= 16 && head_dim < 256 ? 1 : (M <= 32 ? 2 : 4);
   const int rows = pl.QW == 4 ? (head_dim <= 128 ? 64 : 32) : 32 * (4 / pl.QW);  // AttnTile::TR
   const int64_t steps = (cap + rows - 1) / rows;
@@ -536,11 +543,11 @@ int launch_attn_tile(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t 
 
 template <typename H, int DH>
 int launch_attn_waves(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
-  if (pl.NQ == 32) return launch_attn_tile<H, DH, 32, 4>(ap, pl, st);
-  if (pl.QW == 4) return launch_attn_tile<H, DH, 16, 4>(ap, pl, st);
   if constexpr (DH < 256) {
+    if (pl.NQ == 32) return launch_attn_tile<H, DH, 32, 4>(ap, pl, st);
     if (pl.QW == 1) return launch_attn_tile<H, DH, 16, 1>(ap, pl, st);
   }
+  if (pl.QW == 4) return launch_attn_tile<H, DH, 16, 4>(ap, pl, st);
   return launch_attn_tile<H, DH, 16, 2>(ap, pl, st);
 }
 
@@ -572,20 +579,24 @@ struct SvPlan {
   size_t rec, rec_q, state, rest, end;
 };
 
+// Chunks of a row (whose first vector may start before it).
+int64_t accept_chunks(int64_t V, int dtype) {
+  const int N = elems_per_vec(dtype);
+  const int64_t chunk = (int64_t)ddt::kSvThreads * ddt::kSvVecs * N;
+  return (V + (V % N ? N - 1 : 0) + chunk - 1) / chunk;
+}
+
 int accept_check(int dtype, int64_t batch, int32_t T, int32_t L, int64_t V) {
   if (!valid_dtype(dtype) || batch < 0 || T <= 1 || L <= 0 || V <= 0) return DDT_EINVAL;
   if (T > DDT_MAX_B + 1 || L > DDT_MAX_L || V > ((int64_t)1 << 22)) return DDT_ENOTSUP;
-  if (batch > 0x7FFFFFFFLL / (2 * ddt::kSvMaxS) ||
-      batch * T > 0x7FFFFFFFLL / (2 * ddt::kSvMaxS))  // workgroups of a launch
-    return DDT_ENOTSUP;
+  // workgroups of a launch: a chunk of every row, for chains of two
+  if (batch > 0x7FFFFFFFLL / (2 * T * accept_chunks(V, dtype))) return DDT_ENOTSUP;
   return DDT_OK;
 }
 
 SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bool chain) {
-  const int N = elems_per_vec(dtype);
-  const int64_t chunk = (int64_t)ddt::kSvThreads * ddt::kSvVecs * N;
   SvPlan pl;
-  pl.S = (int)((V + (V % N ? N - 1 : 0) + chunk - 1) / chunk);
+  pl.S = (int)accept_chunks(V, dtype);
   const int64_t rows = batch * T + (chain ? batch * (T - 1) : 0);
   // Many rows: only the path's, one launch for each depth (about 8 us each, the
   // time of some 24 MB of rows). Trees of 65 rows of 152 k bf16 at L = 15: 8

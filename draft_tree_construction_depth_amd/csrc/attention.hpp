@@ -769,7 +769,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
     if (t0 + 1 < t1) find(t0 + 1);
     const int end = t1 * C::TR < rq.len ? t1 * C::TR : rq.len;
     if (attn_mapped(p.rows, b, t0 * C::TR, end, s_any)) {
-      tm = rq.past / C::TR;
+      tm = (rq.past < rq.len ? rq.past : rq.len) / C::TR;
       tm = tm < t0 ? t0 : (tm > t1 ? t1 : tm);
     }
   }

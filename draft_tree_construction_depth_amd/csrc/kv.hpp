@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_compact_paged_kernel(KvPagedPar
     if (r >= p.rows.cap) return -1;
     const int page = page_of(p.rows, b, (int)r);
     if (page < 0) return -1;
-    return page * p.heads * head_bytes + (int64_t)row_in_page(p.rows, (int)r) * p.row_bytes;
+    return (int64_t)page * p.heads * head_bytes + (int64_t)row_in_page(p.rows, (int)r) * p.row_bytes;
   };
   if (lane < n) {
     const int node = p.accepted[b * p.L + lane];

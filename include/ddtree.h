@@ -364,7 +364,7 @@ int ddtree_compact_kv_paged(void* k_cache, void* v_cache, int64_t layers, int64_
  *               accepted, nor is a second sibling with the same token;
  * logp          [batch][L+1] float or NULL: log-probability of the i-th
  *               accepted token, next_token's at accept_len, 0 behind it.
- * Weights and sums are float64 with relative errors below 1e-13: a token
+ * Weights and sums are float64 with relative errors below 2e-13: a token
  * differs from exact arithmetic only where t comes that near a border.
  * Supported: B <= DDT_MAX_B, L <= DDT_MAX_L, V <= 2^22. Workspace:
  * ddtree_accept_sampled_workspace_size bytes, no zero-fill needed.

@@ -89,7 +89,9 @@ def test_tree_acceptance(case):
     heat[1::4] = 0.0
     nn = rng.integers(B // 2, B + 1, batch).astype(np.int32)
     u = rng.random((batch, L + 1), dtype=np.float32)
-    got = pkg.ddtree_accept_sampled(dev(tok), dev(par), dev(nn), xd, dev(heat), dev(u))
+    size = pkg.lib().ddtree_accept_sampled_workspace_size(batch, B, L, V, kind == "f32")
+    got = pkg.ddtree_accept_sampled(dev(tok), dev(par), dev(nn), xd, dev(heat), dev(u),
+                                    ws=torch.full((size,), 255, dtype=torch.uint8, device=DEV))
     want = O.accept_tree(tok, par, nn, xh, heat, u.astype(np.float64))
     same(got, want, TREE)
     if batch > 2:
@@ -183,8 +185,10 @@ def test_chain_acceptance(case):
     tok = (yh + heat[:, None, None] * noise).argmax(2).astype(np.int32)
     keep = rng.integers(0, P + 1, batch).astype(np.int32)
     u = rng.random((batch, P + 1), dtype=np.float32)
+    size = pkg.lib().dspark_accept_sampled_workspace_size(batch, P, V, kind == "f32")
     for k in (keep, None):
-        got = pkg.dspark_accept_sampled(dev(tok), xd, yd, dev(heat), dev(u), keep=dev(k))
+        got = pkg.dspark_accept_sampled(dev(tok), xd, yd, dev(heat), dev(u), keep=dev(k),
+                                        ws=torch.full((size,), 255, dtype=torch.uint8, device=DEV))
         want = O.accept_chain(tok, k, xh, yh, heat, u.astype(np.float64))
         same(got, want, CHAIN)
     if batch * P > 8:

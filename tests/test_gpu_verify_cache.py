@@ -248,6 +248,39 @@ def test_attention_of_a_padded_batch_and_node_counts():
         check_attention(q, kc, vc, past, None, nn, None)
 
 
+@pytest.mark.parametrize("longest", [300, 6000])
+def test_attention_of_many_requests(longest):
+    """More requests than a workgroup has threads: units dealt out whole, or (one of them far
+    longer than the others) cut; a workspace full of garbage."""
+    rng = np.random.default_rng(longest)
+    batch, ps = 300, 16
+    past = rng.integers(0, 301, batch).astype(np.int32)
+    past[[17, 290]] = -1
+    past[299] = longest
+    table, pool = paging(rng, batch, np.maximum(past, 0) + 1, ps)
+    q = rounded(rng, (batch, 1, 4, 64), BF)
+    kc, vc = rounded(rng, (pool, 4, ps, 64), BF), rounded(rng, (pool, 4, ps, 64), BF)
+    size = pkg.lib().ddtree_attention_workspace_size(batch, 1, 4, 4, 64, table.shape[1], ps)
+    check_attention(q, kc, vc, past, table, None, None,
+                    ws=torch.full((size,), 255, dtype=torch.uint8, device=DEV))
+
+
+def test_rows_that_the_cache_has_no_room_for():
+    """past + block beyond the table's rows: those rows are neither written nor seen."""
+    rng = np.random.default_rng(13)
+    T, ps = 9, 8
+    past = np.array([20, 27, 40, 500], np.int32)  # room for 32 rows
+    table = rng.permutation(16).astype(np.int32).reshape(4, 4)
+    q = rounded(rng, (4, T, 2, 64), BF)
+    kc, vc = rounded(rng, (16, 1, ps, 64), BF), rounded(rng, (16, 1, ps, 64), BF)
+    check_attention(q, kc, vc, past, table, None, None)
+    k = rounded(rng, (4, T, 1, 64), BF)
+    kd, vd = kc.to(DEV), vc.to(DEV)
+    pkg.ddtree_append_kv(None, k.to(DEV), k.to(DEV), kd, vd, dev(past), page_table=dev(table))
+    _, ke, ve = O.append(f64(k), f64(k), f64(k), f64(kc), f64(vc), past, table=table)
+    assert np.array_equal(f64(kd), ke) and np.array_equal(f64(vd), ve)
+
+
 def test_attention_is_deterministic_and_streams_keep_apart():
     rng = np.random.default_rng(11)
     past = np.array([900, 33, 2000], np.int32)

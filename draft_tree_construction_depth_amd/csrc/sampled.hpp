@@ -35,8 +35,9 @@ namespace ddt {
 
 constexpr int kSvThreads = 256;
 constexpr int kSvVecs = 4;       // 16-byte vectors per thread and chunk
-constexpr int kSvMaxS = 1024;    // chunks per row
+constexpr int kSvMaxS = 1025;    // chunks per row: 2^22 float32, whose first vector may start before it
 constexpr int kSvMaxB = 512;     // nodes
+constexpr float kSvTop = 3.402823466e38f;  // the largest finite value, which stands for +inf
 constexpr int kSvChunkMax = kSvThreads * kSvVecs * 8;  // elements (bf16)
 constexpr int kSvFinish = 1024;  // threads of the launches that end a walk
 
@@ -88,7 +89,7 @@ struct SvVec {
   }
   __device__ __forceinline__ float at(int e) const {
     const float x = raw(e);
-    return x == x ? fminf(x, 3.402823466e38f) : -INFINITY;
+    return x == x ? fminf(x, kSvTop) : -INFINITY;
   }
 };
 
@@ -270,9 +271,9 @@ __device__ __forceinline__ double sv_sum(const SvVec<DT> (&x)[kSvVecs], float m,
   constexpr int N = SvVec<DT>::N;
   const double ms = (double)m * h.s;
   double z[2] = {0.0, 0.0};
-  if (fabs(ms) < 1024.0) {
+  if (fabs(ms) < 1024.0 && m < kSvTop) {
     // (x - m) s as x s - m s is within 2^-43 then; NaN and -inf end at the
-    // least weight by the maximum in sv_exp2_fast
+    // least weight by the maximum in sv_exp2_fast, and there is no +inf
 #pragma unroll
     for (int i = 0; i < kSvVecs; ++i)
 #pragma unroll
@@ -306,7 +307,7 @@ __device__ __forceinline__ void sv_chunk(const void* base, int64_t r0, int64_t V
   for (int i = 0; i < kSvVecs; ++i)
 #pragma unroll
     for (int e = 0; e < N; ++e) m = fmaxf(m, x[i].raw(e));  // (passes NaN over)
-  m = wave_max(fminf(m, 3.402823466e38f));
+  m = wave_max(fminf(m, kSvTop));
   if ((tid & 63) == 0) s_m[w] = m;
   __syncthreads();
   m = s_m[0];
@@ -504,6 +505,7 @@ __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, c
   const double zp = 1.0 / row.Z, zq = PQ ? 1.0 / rowq.Z : 0.0;
   SvVec<DT> x[VECS], y[PQ ? VECS : 1];
   double incl[VECS];
+  uint32_t some = 0;  // vectors with any weight
   auto weight = [&](int i, int e) -> double {
     const int64_t id = (v0 + i * NT + tid) * N - off + e;
     if (id < 0 || id >= p.V) return 0.0;
@@ -531,6 +533,7 @@ __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, c
       if (a > 0.0) last = i * N + e;
     }
     incl[i] = wave_incl_scan_f64(sum);
+    some |= (sum > 0.0 ? 1u : 0u) << i;
     if (lane == 63) sh.seg[i][w] = incl[i];
   }
   __syncthreads();
@@ -549,8 +552,10 @@ __device__ int sv_draw_chunk(const SvParams& p, int64_t rp, int64_t rq, int c, c
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
         if (i != hit / NW) continue;
-        const uint64_t over = __ballot(run + incl[i] > t);
-        const int l = __builtin_ctzll(over);
+        // the scan's rounding may pass t at a vector without weight: the next
+        // one that has any, or the last
+        const uint64_t any = __ballot(some >> i & 1), over = __ballot(run + incl[i] > t) & any;
+        const int l = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(any);
         const double before = __shfl_up(incl[i], 1);
         if (lane == l) {
           double cum = run + (lane > 0 ? before : 0.0);
@@ -853,7 +858,7 @@ __global__ __launch_bounds__(kSvRest) void sv_chain_rest_kernel(SvParams p, int 
   const double zp = 1.0 / row.Z, zq = 1.0 / rowq.Z;
   const double mp = row.M * h.s, mq = rowq.M * h.s;
   double z = 0.0;
-  if (fabs(mp) < 1024.0 && fabs(mq) < 1024.0) {
+  if (fabs(mp) < 1024.0 && fabs(mq) < 1024.0 && row.M < kSvTop && rowq.M < kSvTop) {
     // as in sv_sum; a pair of least weights (2^-1000) adds nothing
 #pragma unroll
     for (int i = 0; i < VECS; ++i)

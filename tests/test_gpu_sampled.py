@@ -129,6 +129,51 @@ def test_tree_acceptance_of_odd_rows():
                 same(got, O.accept_tree(tok, par, counts, rows.astype(np.float64), heat, uu.astype(np.float64)), TREE)
 
 
+@pytest.mark.parametrize("V", [4194303, 4194304])
+def test_the_longest_rows(V):
+    """Rows whose last chunk holds a few elements or none, the next token their last one."""
+    rng = np.random.default_rng(V)
+    x = rng.standard_normal((1, 2, V), dtype=np.float32)
+    x[0, 0, 77] = x[0, 1, V - 1] = 40.0
+    xd, xh = held(x, "f32")
+    tok, par, u = np.full((1, 1), 77, np.int32), np.zeros((1, 1), np.int32), np.full((1, 2), 0.5, np.float32)
+    got = pkg.ddtree_accept_sampled(dev(tok), dev(par), None, xd, None, dev(u))
+    want = O.accept_tree(tok, par, None, xh, None, u.astype(np.float64))
+    same(got, want, TREE)
+    assert want[1][0] == 1 and want[2][0] == V - 1
+    y = x[:, :1].copy()
+    yd, yh = held(y, "f32")
+    got = pkg.dspark_accept_sampled(dev(tok), xd, yd, None, dev(u))
+    same(got, O.accept_chain(tok, None, xh, yh, None, u.astype(np.float64)), CHAIN)
+    y[0, 0, 77], y[0, 0, V - 2] = 0.0, 40.0  # the guess falls, what is left is drawn
+    yd, yh = held(y, "f32")
+    tok[0, 0] = V - 2
+    got = pkg.dspark_accept_sampled(dev(tok), xd, yd, None, dev(u))
+    same(got, O.accept_chain(tok, None, xh, yh, None, u.astype(np.float64)), CHAIN)
+
+
+def test_infinite_logits_at_great_temperatures():
+    """+inf counts as the largest finite value also where the temperature brings it near the others."""
+    rng = np.random.default_rng(8)
+    V, P = 5000, 3
+    heat = np.array([1e37, 1e38, 3e38, np.inf], np.float32)
+    x = (rng.standard_normal((4, P + 1, V)) * 1e37).astype(np.float32)
+    y = (rng.standard_normal((4, P, V)) * 1e37).astype(np.float32)
+    x[:, :, 11::700], y[:, :, 300::900] = np.inf, np.inf
+    x[:, :, 12::700], y[:, :, 301::900] = np.nan, -np.inf
+    tok = rng.integers(0, V, (4, P)).astype(np.int32)
+    tok[:, 1] = 11
+    par = np.array([[0, 0, 1]] * 4, np.int32)
+    for kind in ("f32", "bf16"):
+        (xd, xh), (yd, yh) = held(x, kind), held(y, kind)
+        for share in (0.0, 0.3, 0.7, 0.99):
+            u = np.full((4, P + 1), share, np.float32)
+            same(pkg.ddtree_accept_sampled(dev(tok), dev(par), None, xd, dev(heat), dev(u)),
+                 O.accept_tree(tok, par, None, xh, heat, u.astype(np.float64)), TREE)
+            same(pkg.dspark_accept_sampled(dev(tok), xd, yd, dev(heat), dev(u)),
+                 O.accept_chain(tok, None, xh, yh, heat, u.astype(np.float64)), CHAIN)
+
+
 def test_tree_acceptance_gives_the_target_distribution():
     """4096 requests with evenly spread numbers: every first token comes out 4096 p(v) times."""
     rng = np.random.default_rng(5)

@@ -574,8 +574,9 @@ int attn_check(int dtype, int64_t batch, int32_t T, int32_t q_heads, int32_t kv_
 
 // ---- acceptance at a temperature: schedule and workspace ------------------------
 struct SvPlan {
-  int S;         // chunks per row
-  bool stepped;  // records of the path's rows only, one launch per depth
+  int S;       // chunks per row
+  int depths;  // whose path rows have a launch of their own, before the one for all rows left
+  int slices;  // workgroups that share a request's rows in the latter
   size_t rec, rec_q, state, rest, end;
 };
 
@@ -598,17 +599,29 @@ SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bo
   SvPlan pl;
   pl.S = (int)accept_chunks(V, dtype);
   const int64_t rows = batch * T + (chain ? batch * (T - 1) : 0);
-  // Many rows: only the path's, one launch for each depth (about 8 us each, the
-  // time of some 24 MB of rows). Trees of 65 rows of 152 k bf16 at L = 15: 8
-  // requests (10 MB a depth) 68 us for all rows, 115 us stepped; 16 (20 MB) 118
-  // and 123; 64 (79 MB) 376 and 150; at L = 5 8 requests (26 MB) 62 and 52.
-  pl.stepped = rows * V * (int64_t)elem_size(dtype) > (L + 1) * ((int64_t)24 << 20);
-  const size_t rec = sizeof(ddt::SvRec);
+  // Many rows: for a third of the depths only the path's, one launch for each
+  // (about 8 us, the time of some 10 MB a depth), then all rows that walks still
+  // going on may come to. All rows at once against that, trees of 64 nodes with
+  // rows of 152 k bf16, us: L = 15, 4 requests (5 MB a depth) 47 / 57, 8 (9 MB)
+  // 70 / 70, 16 (19 MB) 121 / 80; L = 5, 4 requests (13 MB) 48 / 44, 8 (25 MB)
+  // 62 / 47; chains of 16 guesses, 16 requests (9 MB) 75 / 82, 32 (18 MB)
+  // 137 / 110. Depths with a launch of their own, 64 requests at L = 15, at 3 /
+  // 5 / 6 / 8 / 15: trees where 3 walks in 4 go on 155 / 128 / 126 / 134 / 159,
+  // where all do (5 / 6 / 8 / 15) 178 / 171 / 166 / 181, chains 157 / 154 / 157 /
+  // 163 / 191.
+  const bool many = rows * V * (int64_t)elem_size(dtype) > (L + 1) * ((int64_t)10 << 20);
+  pl.depths = !many ? 0 : (L <= 2 ? L : (L + 2) / 3 + 1);
+  // a workgroup per row and chunk, or some 8192 (64 requests after 3 depths, at
+  // 2048 / 4096 / 8192 / 16384: trees 217 / 170 / 155 / 153, chains 190 / 163 /
+  // 157 / 162)
+  const int64_t each = 8192 / (batch * pl.S) + 1, most = chain ? 2 * T - 1 : T;
+  pl.slices = (int)(each < most && many ? each : most);
+  const size_t rec = sizeof(ddt::SvRec), path = pl.depths > 0 ? 2 * (size_t)batch : 0;
   size_t o = 0;
   pl.rec = o;
-  o = align_up(o + (pl.stepped ? 2 * (size_t)batch : (size_t)batch * T) * pl.S * rec);
+  o = align_up(o + (path + (size_t)batch * T) * pl.S * rec);
   pl.rec_q = o;
-  if (chain) o = align_up(o + (pl.stepped ? 2 * (size_t)batch : (size_t)batch * (T - 1)) * pl.S * rec);
+  if (chain) o = align_up(o + (path + (size_t)batch * (T - 1)) * pl.S * rec);
   pl.state = o;
   o = align_up(o + (size_t)batch * (L + 2) * sizeof(ddt::SvState));
   pl.rest = o;
@@ -621,27 +634,24 @@ template <int DT, bool CHAIN>
 int accept_launch(const SvPlan& pl, const ddt::SvParams& sp, hipStream_t st) {
   const dim3 block(ddt::kSvThreads), finish(ddt::kSvFinish), each((unsigned)sp.batch);
   const unsigned chunks = (unsigned)(sp.batch * pl.S);
-  if (pl.stepped) {
-    for (int step = 0; step <= sp.L; ++step) {
-      if (CHAIN)
-        hipLaunchKernelGGL((ddt::sv_chain_step_kernel<DT>), dim3(2 * chunks), block, 0, st, sp,
-                           step);
-      else
-        hipLaunchKernelGGL((ddt::sv_step_kernel<DT>), dim3(chunks), block, 0, st, sp, step);
-      if (hipGetLastError() != hipSuccess) return DDT_EHIP;
-    }
-  } else {
-    const int64_t rows = sp.batch * sp.T + (CHAIN ? sp.batch * (sp.T - 1) : 0);
-    hipLaunchKernelGGL((ddt::sv_rows_kernel<DT, CHAIN>), dim3((unsigned)(rows * pl.S)), block, 0,
-                       st, sp);
+  for (int step = 0; step < pl.depths; ++step) {
+    if (CHAIN)
+      hipLaunchKernelGGL((ddt::sv_chain_step_kernel<DT>), dim3(2 * chunks), block, 0, st, sp, step);
+    else
+      hipLaunchKernelGGL((ddt::sv_step_kernel<DT>), dim3(chunks), block, 0, st, sp, step);
     if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   }
+  const dim3 rows((unsigned)(chunks * pl.slices));
+  if (CHAIN)
+    hipLaunchKernelGGL((ddt::sv_chain_rows_kernel<DT>), rows, block, 0, st, sp);
+  else
+    hipLaunchKernelGGL((ddt::sv_rows_kernel<DT>), rows, block, 0, st, sp);
+  if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   if (!CHAIN) {
-    hipLaunchKernelGGL((ddt::sv_finish_kernel<DT>), each, finish, 0, st, sp, sp.L);
+    hipLaunchKernelGGL((ddt::sv_finish_kernel<DT>), each, finish, 0, st, sp);
     return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
   }
-  hipLaunchKernelGGL((ddt::sv_chain_rest_kernel<DT>), dim3(chunks), dim3(ddt::kSvRest), 0, st, sp,
-                     sp.L);
+  hipLaunchKernelGGL((ddt::sv_chain_rest_kernel<DT>), dim3(chunks), dim3(ddt::kSvRest), 0, st, sp);
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   hipLaunchKernelGGL((ddt::sv_chain_finish_kernel<DT>), each, finish, 0, st, sp);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
@@ -1092,7 +1102,8 @@ int ddtree_accept_sampled(const int32_t* tree_tokens, const int32_t* parents,
   sp.next_token = next_token;
   sp.logp = logp;
   sp.S = pl.S;
-  sp.stepped = pl.stepped;
+  sp.depths = pl.depths;
+  sp.slices = pl.slices;
   sp.rec = (ddt::SvRec*)(ws + pl.rec);
   sp.state = (ddt::SvState*)(ws + pl.state);
   return dtype == DDT_BF16 ? accept_launch<0, false>(pl, sp, stream)
@@ -1136,7 +1147,8 @@ int dspark_accept_sampled(const int32_t* tokens, const int32_t* keep, const void
   sp.next_token = next_token;
   sp.logp = logp;
   sp.S = pl.S;
-  sp.stepped = pl.stepped;
+  sp.depths = pl.depths;
+  sp.slices = pl.slices;
   sp.rec = (ddt::SvRec*)(ws + pl.rec);
   sp.rec_q = (ddt::SvRec*)(ws + pl.rec_q);
   sp.state = (ddt::SvState*)(ws + pl.state);

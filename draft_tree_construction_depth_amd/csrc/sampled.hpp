@@ -24,9 +24,10 @@
 // The row sums (records) are formed by workgroups of 256 threads, each over a
 // chunk of 8 16-byte vectors per thread held in registers: its maximum, then
 // the sum of its weights against that maximum. Only the rows on the path
-// matter, but which they are is known only step by step; the host picks one
-// of two schedules (accept_plan in api.hip): all rows' records in one launch,
-// or those of the path's rows, one launch for each depth.
+// matter, but which they are is known only step by step: for the first depths
+// the path's rows' records are formed by a launch for each depth, then those of
+// all rows that the walks still going on may come to by one more (how many
+// depths: accept_plan in api.hip).
 #pragma once
 
 #include "common.hpp"
@@ -68,11 +69,12 @@ struct SvParams {
   int32_t* accept_len;
   int32_t* next_token;
   float* logp;  // [batch][L+1], may be null
-  int32_t S;    // chunks per row
-  int32_t stepped;
-  SvRec* rec;      // all rows: [batch][T][S]; stepped: [2][batch][S]
-  SvRec* rec_q;    // chains: the same of the drafter's rows
-  SvState* state;  // stepped: [L+2][batch]; else [1][batch]
+  int32_t S;      // chunks per row
+  int32_t depths;  // with a launch of their own
+  int32_t slices;  // workgroups that share a request's other rows
+  SvRec* rec;      // the path's rows [2][batch][S] (if depths > 0), all rows [batch][T][S]
+  SvRec* rec_q;    // chains: the same of the drafter's rows (T-1 of them)
+  SvState* state;  // [L+2][batch], after each launch
   double* rest;    // chains: [batch][S] sums of max(0, p - q)
 };
 
@@ -342,30 +344,15 @@ __device__ __forceinline__ void sv_chunk(const void* base, int64_t r0, int64_t V
   }
 }
 
-// Records of every row (of the drafter's rows too, for chains).
-template <int DT, bool CHAIN>
-__global__ __launch_bounds__(kSvThreads) void sv_rows_kernel(SvParams p) {
-  const int64_t id = blockIdx.x;
-  const int c = (int)(id % p.S);
-  int64_t row = id / p.S;
-  const bool q = CHAIN && row >= p.batch * p.T;
-  if (q) row -= p.batch * p.T;
-  const int per = q ? p.T - 1 : p.T;
-  const int64_t b = row / per;
-  const int i = (int)(row - b * per), n = sv_count(p, b);
-  if (i > n || (q && i >= n)) return;
-  sv_chunk<DT>(q ? p.draft : p.logits, row * p.V, p.V, c, sv_heat(p, b),
-               (q ? p.rec_q : p.rec) + row * p.S + c);
-}
-
 __device__ __forceinline__ float sv_logp(double w, double Z) {
   return Z > 0.0 ? (float)(log(w) - log(Z)) : -INFINITY;
 }
 
-// Where the records of a row lie: by row, or (stepped) by request and the
-// parity of the depth.
+// Where the records of a row lie: by request and the parity of the depth for
+// the first depths, by row for the others.
 __device__ __forceinline__ int64_t sv_rec_at(const SvParams& p, int64_t b, int at, int d, int per) {
-  return p.stepped ? ((int64_t)(d & 1) * p.batch + b) * p.S : (b * per + at) * p.S;
+  if (d < p.depths) return ((int64_t)(d & 1) * p.batch + b) * p.S;
+  return ((p.depths > 0 ? 2 * p.batch : 0) + b * per + at) * p.S;
 }
 
 // ---- trees: the line at a node ------------------------------------------------
@@ -433,52 +420,102 @@ __device__ __forceinline__ void sv_hit(SvTree& t, int node, int n, double at) {
   }
 }
 
-// One step of the walk for every request: the decision at the row whose
-// records the step before formed, then one chunk of the next row's records.
+// The walk's state after `step` decisions, the last of them made here from
+// the records of the launch before; every workgroup of a request makes the same
+// one, and the one for which `first` is set writes it down.
+template <int DT>
+__device__ __forceinline__ SvState sv_decide(const SvParams& p, int64_t b, int step,
+                                             const SvHeat& h, SvState st, bool first, SvTree& sh) {
+  if (!st.done) {
+    const int tid = threadIdx.x, d = step - 1;
+    const uint32_t k0 = sv_key(p, b, tid), k1 = sv_key(p, b, tid + kSvThreads);
+    const int n = d < p.L ? sv_count(p, b) : 0;
+    // the node's children
+    const int64_t r0 = (b * p.T + st.at) * p.V;
+    const bool kid0 = k0 != kSvNoKey && (int)(k0 >> 22) == st.at;
+    const bool kid1 = k1 != kSvNoKey && (int)(k1 >> 22) == st.at;
+    const int t0 = (int)(k0 & 0x3FFFFFu), t1 = (int)(k1 & 0x3FFFFFu);
+    const float x0 = kid0 ? sv_logit<DT>(p.logits, r0, t0) : 0.0f;
+    const float x1 = kid1 ? sv_logit<DT>(p.logits, r0, t1) : 0.0f;
+    const SvRow row = sv_combine(p.rec + sv_rec_at(p, b, st.at, d, p.T), p.S, h);
+    sh.key[tid] = kid0 ? k0 : kSvNoKey;
+    sh.key[tid + kSvThreads] = kid1 ? k1 : kSvNoKey;
+    sh.w[tid] = kid0 ? row.weight(x0, t0) : 0.0;
+    sh.w[tid + kSvThreads] = kid1 ? row.weight(x1, t1) : 0.0;
+    __syncthreads();
+    if (tid < kWave) sv_hit(sh, st.at, n, sv_uniform(p, b, d) * row.Z);
+    __syncthreads();
+    if (sh.pick >= 0) {
+      if (first && tid == 0) {
+        p.accepted[b * p.L + d] = sh.pick + 1;
+        if (p.logp) p.logp[b * (p.L + 1) + d] = sv_logp(sh.w[sh.pick], row.Z);
+      }
+      st.at = sh.pick + 1;
+      st.depth = step;
+    } else {
+      st.done = 1;
+    }
+  }
+  if (first && threadIdx.x == 0) p.state[(int64_t)step * p.batch + b] = st;
+  return st;
+}
+
+// One step of the walk for every request, then one chunk of the next row's
+// records.
 template <int DT>
 __global__ __launch_bounds__(kSvThreads) void sv_step_kernel(SvParams p, int step) {
   __shared__ SvTree sh;
   const int64_t b = blockIdx.x / p.S;
-  const int c = (int)(blockIdx.x - b * p.S), tid = threadIdx.x;
+  const int c = (int)(blockIdx.x - b * p.S);
   const SvHeat h = sv_heat(p, b);
   SvState st{0, 0, 0, 0};
-  if (step > 0) {
-    const int d = step - 1;
-    st = p.state[(int64_t)d * p.batch + b];
-    if (!st.done) {
-      const uint32_t k0 = sv_key(p, b, tid), k1 = sv_key(p, b, tid + kSvThreads);
-      const int n = d < p.L ? sv_count(p, b) : 0;
-      // the node's children
-      const int64_t r0 = (b * p.T + st.at) * p.V;
-      const bool kid0 = k0 != kSvNoKey && (int)(k0 >> 22) == st.at;
-      const bool kid1 = k1 != kSvNoKey && (int)(k1 >> 22) == st.at;
-      const int t0 = (int)(k0 & 0x3FFFFFu), t1 = (int)(k1 & 0x3FFFFFu);
-      const float x0 = kid0 ? sv_logit<DT>(p.logits, r0, t0) : 0.0f;
-      const float x1 = kid1 ? sv_logit<DT>(p.logits, r0, t1) : 0.0f;
-      const SvRow row = sv_combine(p.rec + sv_rec_at(p, b, st.at, d, p.T), p.S, h);
-      sh.key[tid] = kid0 ? k0 : kSvNoKey;
-      sh.key[tid + kSvThreads] = kid1 ? k1 : kSvNoKey;
-      sh.w[tid] = kid0 ? row.weight(x0, t0) : 0.0;
-      sh.w[tid + kSvThreads] = kid1 ? row.weight(x1, t1) : 0.0;
-      __syncthreads();
-      if (tid < kWave) sv_hit(sh, st.at, n, sv_uniform(p, b, d) * row.Z);
-      __syncthreads();
-      if (sh.pick >= 0) {
-        if (c == 0 && tid == 0) {
-          p.accepted[b * p.L + d] = sh.pick + 1;
-          if (p.logp) p.logp[b * (p.L + 1) + d] = sv_logp(sh.w[sh.pick], row.Z);
-        }
-        st.at = sh.pick + 1;
-        st.depth = step;
-      } else {
-        st.done = 1;
-      }
-    }
-  }
-  if (c == 0 && tid == 0) p.state[(int64_t)step * p.batch + b] = st;
+  if (step > 0)
+    st = sv_decide<DT>(p, b, step, h, p.state[(int64_t)(step - 1) * p.batch + b], c == 0, sh);
+  else if (c == 0 && threadIdx.x == 0)
+    p.state[b] = st;
   if (st.done) return;
   sv_chunk<DT>(p.logits, (b * p.T + st.at) * p.V, p.V, c, h,
-               p.rec + ((int64_t)(step & 1) * p.batch + b) * p.S + c);
+               p.rec + sv_rec_at(p, b, st.at, step, p.T) + c);
+}
+
+// Whether row r is node `node` or below it (parents come before their children).
+__device__ __forceinline__ bool sv_below(const int32_t* parent, int r, int node) {
+  while (r > node) r = parent[r - 1];
+  return r == node;
+}
+
+// The last step, then one chunk of the records of every row that the walk may
+// still come to: the node's and those below it, dealt to the request's
+// workgroups of this chunk in turn.
+template <int DT>
+__global__ __launch_bounds__(kSvThreads) void sv_rows_kernel(SvParams p) {
+  __shared__ SvTree sh;
+  __shared__ int32_t s_parent[kSvMaxB];
+  const int64_t id = blockIdx.x / p.S, b = id / p.slices;
+  const int c = (int)(blockIdx.x - id * p.S), slice = (int)(id - b * p.slices);
+  const bool first = c == 0 && slice == 0;
+  const SvHeat h = sv_heat(p, b);
+  const int n = sv_count(p, b);
+  SvState st{0, 0, 0, 0};
+  if (p.depths > 0) {
+    st = p.state[(int64_t)(p.depths - 1) * p.batch + b];
+    if (!st.done) {
+      for (int j = threadIdx.x; j < p.T - 1; j += kSvThreads) {
+        const int par = p.parents[b * (p.T - 1) + j];
+        s_parent[j] = par > j ? -1 : par;
+      }
+    }
+    st = sv_decide<DT>(p, b, p.depths, h, st, first, sh);
+    if (st.done) return;
+  }
+  const int last = st.depth < p.L ? n : st.at;
+  for (int r = st.at + slice; r <= last; r += p.slices) {  // uniform
+    if (p.depths > 0 && !sv_below(s_parent, r, st.at)) continue;
+    __syncthreads();  // the row before is done with sv_chunk's LDS
+    const int64_t row = b * p.T + r;
+    sv_chunk<DT>(p.logits, row * p.V, p.V, c, h,
+                 p.rec + sv_rec_at(p, b, r, p.depths, p.T) + c);
+  }
 }
 
 // ---- the draw of the next token --------------------------------------------------
@@ -638,11 +675,10 @@ __device__ void sv_tail(const SvParams& p, int64_t b, int depth, int token, doub
   }
 }
 
-// Trees: the walk (unless it was stepped) and the next token, one workgroup
-// per request. Every row's sums and every node's weight are formed
+// Trees: the rest of the walk and the next token, one workgroup per request. Every row's sums and every node's weight are formed
 // side by side first, so that the walk itself only reads LDS.
 template <int DT>
-__global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int step) {
+__global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p) {
   constexpr int NT = kSvFinish, N = SvVec<DT>::N;
   __shared__ SvTree sh;
   __shared__ SvDraw<NT> dr;
@@ -656,20 +692,23 @@ __global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int st
   const int count = sv_count(p, b);
   if (tid >= count) key = kSvNoKey;
   int node = 0, d = 0;
-  if (p.stepped) {
-    const SvState st = p.state[(int64_t)step * p.batch + b];
+  bool ended = false;
+  if (p.depths > 0) {
+    const SvState st = p.state[(int64_t)p.depths * p.batch + b];
     node = st.at;
     d = st.depth;
     // the walk has ended here; its node's line is formed again
-    if (key != kSvNoKey && (int)(key >> 22) != node) key = kSvNoKey;
+    ended = st.done != 0;
+    if (key != kSvNoKey && (ended ? (int)(key >> 22) != node : (int)(key >> 22) < node)) key = kSvNoKey;
   }
   const int par = (int)(key >> 22), tok = (int)(key & 0x3FFFFFu);
   const float x = key != kSvNoKey ? sv_logit<DT>(p.logits, (b * p.T + par) * p.V, tok) : 0.0f;
   if (tid < kSvMaxB) sh.key[tid] = key;
-  // the rows' maxima and sums: a group of lanes takes a row (stepped: the
-  // node's only)
-  const int lanes = sv_lanes(p.S), first = p.stepped ? node : 0, end = p.stepped ? node : count;
-  for (int r0 = first; r0 <= end; r0 += NT / lanes) {  // uniform
+  // the rows' maxima and sums: a group of lanes takes a row (a walk that has
+  // ended: the node's only; of the others those not below the node are old
+  // records, which no decision reads)
+  const int lanes = sv_lanes(p.S), end = ended || node > count ? node : count;
+  for (int r0 = node; r0 <= end; r0 += NT / lanes) {  // uniform
     const int r = r0 + tid / lanes;
     const SvRow row =
         sv_combine(p.rec + sv_rec_at(p, b, r <= end ? r : end, d, p.T), p.S, h, lanes);
@@ -693,7 +732,7 @@ __global__ __launch_bounds__(kSvFinish) void sv_finish_kernel(SvParams p, int st
   __syncthreads();
   if (tid < kWave) {
     for (;;) {
-      sv_hit(sh, node, d < p.L ? count : 0, p.stepped ? 1e300 : sv_uniform(p, b, d) * s_Z[node]);
+      sv_hit(sh, node, d < p.L ? count : 0, ended ? 1e300 : sv_uniform(p, b, d) * s_Z[node]);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       const int pick = sh.pick;
@@ -766,47 +805,78 @@ __device__ bool sv_test(const SvParams& p, int64_t b, int i, const SvHeat& h, in
   return in && sv_uniform(p, b, i) * wq * Zp < wp * (Zq > 0.0 ? Zq : 1.0);
 }
 
-// One step of a chain for every request: the test of the guess whose rows'
-// records the step before formed, then one chunk of the next rows' records.
+// As sv_decide: the state after the test of guess step - 1.
+template <int DT>
+__device__ __forceinline__ SvState sv_chain_decide(const SvParams& p, int64_t b, int step,
+                                                   const SvHeat& h, SvState st, int keep,
+                                                   bool first) {
+  const int pair = p.S <= 16 ? 16 : 32;  // two groups to a wave at least
+  if (!st.done) {
+    double wt = 0.0;
+    SvRow row;
+    if (st.at >= keep) {
+      st.done = 1;
+    } else if (sv_test<DT>(p, b, st.at, h, pair, wt, row)) {  // every pair the same
+      if (first && threadIdx.x == 0 && p.logp) p.logp[b * (p.L + 1) + st.at] = sv_logp(wt, row.Z);
+      st.at = st.depth = step;
+    } else {
+      st.done = 2;
+    }
+  }
+  if (first && threadIdx.x == 0) p.state[(int64_t)step * p.batch + b] = st;
+  return st;
+}
+
+// One step of a chain for every request, then one chunk of the next rows'
+// records.
 template <int DT>
 __global__ __launch_bounds__(kSvThreads) void sv_chain_step_kernel(SvParams p, int step) {
   const int64_t b = blockIdx.x / (2 * p.S);
   int c = (int)(blockIdx.x - b * 2 * p.S);
-  const bool q = c >= p.S, first = c == 0 && threadIdx.x == 0;
+  const bool q = c >= p.S, first = c == 0;
   if (q) c -= p.S;
   const SvHeat h = sv_heat(p, b);
   const int keep = sv_count(p, b);
-  const int pair = p.S <= 16 ? 16 : 32;  // two groups to a wave at least
   SvState st{0, 0, 0, 0};
-  if (step > 0) {
-    st = p.state[(int64_t)(step - 1) * p.batch + b];
-    if (!st.done) {
-      double wt = 0.0;
-      SvRow row;
-      if (st.at >= keep) {
-        st.done = 1;
-      } else if (sv_test<DT>(p, b, st.at, h, pair, wt, row)) {  // every pair the same
-        if (first && p.logp) p.logp[b * (p.L + 1) + st.at] = sv_logp(wt, row.Z);
-        st.at = st.depth = step;
-      } else {
-        st.done = 2;
-      }
-    }
-  }
-  if (first) p.state[(int64_t)step * p.batch + b] = st;
+  if (step > 0)
+    st = sv_chain_decide<DT>(p, b, step, h, p.state[(int64_t)(step - 1) * p.batch + b], keep,
+                             first);
+  else if (first && threadIdx.x == 0)
+    p.state[b] = st;
   if (st.done || (q && st.at >= keep)) return;
-  const int64_t row = b * (q ? p.T - 1 : p.T) + st.at;
-  sv_chunk<DT>(q ? p.draft : p.logits, row * p.V, p.V, c, h,
-               (q ? p.rec_q : p.rec) + ((int64_t)(step & 1) * p.batch + b) * p.S + c);
+  const int per = q ? p.T - 1 : p.T;
+  sv_chunk<DT>(q ? p.draft : p.logits, (b * per + st.at) * p.V, p.V, c, h,
+               (q ? p.rec_q : p.rec) + sv_rec_at(p, b, st.at, step, per) + c);
 }
 
-// Chains: the tests (all of them side by side, or stepped the last one), and
-// chunk sums of max(0, p - q) where a guess fell. Every workgroup of a request
+// The last step, then one chunk of the records of all rows left.
+template <int DT>
+__global__ __launch_bounds__(kSvThreads) void sv_chain_rows_kernel(SvParams p) {
+  const int64_t id = blockIdx.x / p.S, b = id / p.slices;
+  const int c = (int)(blockIdx.x - id * p.S), slice = (int)(id - b * p.slices);
+  const SvHeat h = sv_heat(p, b);
+  const int keep = sv_count(p, b);
+  SvState st{0, 0, 0, 0};
+  if (p.depths > 0) {
+    st = sv_chain_decide<DT>(p, b, p.depths, h, p.state[(int64_t)(p.depths - 1) * p.batch + b],
+                             keep, c == 0 && slice == 0);
+    if (st.done) return;
+  }
+  for (int j = slice; j <= 2 * (keep - st.at); j += p.slices) {  // uniform
+    const bool q = j & 1;
+    const int i = st.at + (j >> 1), per = q ? p.T - 1 : p.T;
+    __syncthreads();  // the row before is done with sv_chunk's LDS
+    sv_chunk<DT>(q ? p.draft : p.logits, (b * per + i) * p.V, p.V, c, h,
+                 (q ? p.rec_q : p.rec) + sv_rec_at(p, b, i, p.depths, per) + c);
+  }
+}
+
+// Chains: the tests that are left, all of them side by side, and chunk sums of max(0, p - q) where a guess fell. Every workgroup of a request
 // forms the same state.
 constexpr int kSvRest = 512;
 
 template <int DT>
-__global__ __launch_bounds__(kSvRest) void sv_chain_rest_kernel(SvParams p, int step) {
+__global__ __launch_bounds__(kSvRest) void sv_chain_rest_kernel(SvParams p) {
   constexpr int N = SvVec<DT>::N, NW = kSvRest / kWave, VECS = kSvThreads * kSvVecs / kSvRest;
   __shared__ double s_s[NW];
   __shared__ float s_logp[DDT_MAX_L];
@@ -816,26 +886,24 @@ __global__ __launch_bounds__(kSvRest) void sv_chain_rest_kernel(SvParams p, int 
   const SvHeat h = sv_heat(p, b);
   const int keep = sv_count(p, b);
   SvState st{0, 0, 0, 0};
-  if (p.stepped) st = p.state[(int64_t)step * p.batch + b];
+  if (p.depths > 0) st = p.state[(int64_t)p.depths * p.batch + b];
   if (!st.done) {
     const int lanes = p.S <= 16 ? 16 : 32, pairs = kSvRest / (2 * lanes);
     const int g = tid / (2 * lanes);
-    const int i0 = p.stepped ? st.at : 0;
-    // (stepped: the guess at the state's own row, whose records alone are there)
-    const int end = p.stepped && i0 < keep ? i0 + 1 : keep;
-    for (int j = i0; j < end; j += pairs) {  // uniform
-      const int i = j + g < end ? j + g : end - 1;
+    const int i0 = st.at;
+    for (int j = i0; j < keep; j += pairs) {  // uniform
+      const int i = j + g < keep ? j + g : keep - 1;
       double wt = 0.0;
       SvRow row;
       const bool ok = sv_test<DT>(p, b, i, h, lanes, wt, row);
-      if ((tid & (2 * lanes - 1)) == 0 && j + g < end) {
+      if ((tid & (2 * lanes - 1)) == 0 && j + g < keep) {
         s_ok[i] = ok;
         s_logp[i] = sv_logp(wt, row.Z);
       }
     }
     __syncthreads();
     int at = i0;
-    while (at < end && s_ok[at]) ++at;
+    while (at < keep && s_ok[at]) ++at;
     if (c == 0 && p.logp)
       for (int i = i0 + tid; i < at; i += kSvRest) p.logp[b * (p.L + 1) + i] = s_logp[i];
     st.at = st.depth = at;

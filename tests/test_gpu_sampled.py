@@ -240,6 +240,39 @@ def test_chain_acceptance(case):
         assert want[0].max() > 0
 
 
+@pytest.mark.parametrize("batch,L,V", [(60, 1, 60000), (24, 2, 60003), (40, 4, 40001), (40, 15, 40001)])
+def test_many_long_walks(batch, L, V):
+    """Many rows, walks of every length: ended before the first depths are over, there, behind
+    them and at the last; chains of as many guesses the same."""
+    rng = np.random.default_rng(L * V)
+    B = 4 * L
+    par, tok = random_trees(rng, batch, B, V)
+    par[::2, :L] = np.arange(L)  # some chains as deep as can be
+    x = rng.standard_normal((batch, B + 1, V), dtype=np.float32)
+    x = favour(favour(x, par, tok, rng, 5.0), par[:, :L], tok[:, :L], rng, 9.0)
+    xd, xh = held(x, "f32")
+    heat = np.where(np.arange(batch) % 5 == 3, 0.0, 1.0).astype(np.float32)
+    nn = rng.integers(0, B + 1, batch).astype(np.int32)
+    u = rng.random((batch, L + 1), dtype=np.float32)
+    for counts in (nn, None):
+        got = pkg.ddtree_accept_sampled(dev(tok), dev(par), dev(counts), xd, dev(heat), dev(u))
+        want = O.accept_tree(tok, par, counts, xh, heat, u.astype(np.float64))
+        same(got, want, TREE)
+    assert want[1].max() == L
+    del x, xd, xh
+    y = rng.standard_normal((batch, L, V), dtype=np.float32)
+    x = np.concatenate([y + rng.uniform(0.05, 0.4, (batch, 1, 1)).astype(np.float32) * rng.standard_normal(y.shape, dtype=np.float32),
+                        rng.standard_normal((batch, 1, V), dtype=np.float32)], 1)
+    (xd, xh), (yd, yh) = held(x, "f32"), held(y, "f32")
+    tok = (yh + heat[:, None, None] * rng.gumbel(size=yh.shape)).argmax(2).astype(np.int32)
+    keep = rng.integers(0, L + 1, batch).astype(np.int32)
+    for k in (keep, None):
+        got = pkg.dspark_accept_sampled(dev(tok), xd, yd, dev(heat), dev(u), keep=dev(k))
+        want = O.accept_chain(tok, k, xh, yh, heat, u.astype(np.float64))
+        same(got, want, CHAIN)
+    assert want[0].max() == L and want[0].min() < L
+
+
 def test_chain_acceptance_of_odd_rows():
     inf, nan = np.inf, np.nan
     V, P = 24, 3

@@ -34,6 +34,17 @@
 // stretch of it, from the lengths on the device (attn_plan). A unit cut by a
 // stretch's end leaves partial results in the workspace for
 // attn_merge_kernel.
+//
+// Measured per call (bf16, 32 query and 8 key/value heads of 128, unless said
+// otherwise). 64 single tokens over 4 to 8 k rows: 300 us, 1.61 GB at 5.4 TB/s,
+// bound by HBM reads. 64 trees of 129 rows over 1 to 2 k: 295 us, 166 GFLOP at
+// 0.56 PFLOP/s; with two waves on each SIMD (the accumulators and the next tile
+// fill the registers) the matrix units are busy 27%, the vector units 37% and
+// the LDS 33% of the time, and waves wait for one another's phases the rest;
+// tiles of 32 rows with three workgroups to a CU spill (499 us), workgroups of
+// eight waves take 335. 3 chains of 17 rows over 50 to 100 k (f16, heads of 64,
+// 40 and 8): 113 us, 461 MB at 4.1 TB/s. One tree of 65 rows over 1 k: 22 us,
+// of which the merge is 5 and the steps are 6: a chain of waits.
 #pragma once
 
 #include "paged.hpp"

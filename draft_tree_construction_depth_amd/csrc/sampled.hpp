@@ -22,12 +22,20 @@
 // in the sums, which the vector units bound (17 instructions a logit).
 //
 // The row sums (records) are formed by workgroups of 256 threads, each over a
-// chunk of 8 16-byte vectors per thread held in registers: its maximum, then
+// chunk of 4 16-byte vectors per thread held in registers: its maximum, then
 // the sum of its weights against that maximum. Only the rows on the path
 // matter, but which they are is known only step by step: for the first depths
 // the path's rows' records are formed by a launch for each depth, then those of
 // all rows that the walks still going on may come to by one more (how many
 // depths: accept_plan in api.hip).
+//
+// Measured per call, rows of 152 k bf16: one tree of 64 nodes 24 us (rows 12,
+// finish 15: chains of dependent loads); 64 trees 125 us: six launches of 8 to
+// 13 us (a full one reads 19 MB, 4 us, and has 4 us of float64 work, both behind
+// 3 us of dependent loads), 40 to 50 us for the rows left, 16 us for the draw.
+// 64 chains of 16 guesses 162 us: seven launches of 9 to 22 us, 23 for the rows
+// left, 28 for max(0, p - q), 14 for the draw. 8 chains of 5 guesses, 32 k
+// float32: 24 us.
 #pragma once
 
 #include "common.hpp"

@@ -496,11 +496,12 @@ AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_he
   // 16, and two waves or more: 32 queries' state or four groups' tiles would
   // not leave registers for the next tile). 32 requests x 4 heads over 4096
   // rows, us at 16x1 / 16x2 / 16x4 / 32x4 queries x waves:
-  //   head_dim 128  M = 16: 63 / 66 / 71 / 79   32: 64 / 65 / 70 / 78
-  //                 64: 88 / 73 / 70 / 81       256: 248 / 191 / 136 / 114
-  //   head_dim 64   M = 16: 36 / 38 / 38 / 41   64: 53 / 47 / 41 / 44
-  //                 128: 85 / 71 / 53 / 55      256: 130 / 95 / 82 / 70
-  //   head_dim 256  M = 16: - / 135 / 147 / 276 128: - / 295 / 209 / 323
+  //   head_dim 128  M = 16: 62 / 64 / 71 / 77   32: 65 / 63 / 67 / 75
+  //                 64: 87 / 74 / 69 / 77       256: 239 / 165 / 117 / 104
+  //   head_dim 64   M = 16: 36 / 37 / 39 / 42   64: 53 / 46 / 41 / 44
+  //                 128: 83 / 67 / 50 / 53      256: 129 / 85 / 77 / 66
+  //   head_dim 256  M = 16: - / 114 / 125 / 276 128: - / 289 / 180 / 323
+  // (the last column of 256 with tiles that went through registers)
   const int64_t M = (int64_t)T * G;
   pl.NQ = M <= 64 || head_dim == 256 ? 16 : 32;
   pl.QW = M <= 16 && head_dim < 256 ? 1 : (M <= 32 ? 2 : 4);

@@ -27,24 +27,27 @@
 // by the products and the LDS reads that feed them, so all four waves share
 // one staged tile, and 32 queries to a wave halve the LDS reads per product.
 //
-// The next tile's rows are in flight (global to registers) while the present
-// one is worked on. Work is cut evenly: all steps of all units (a unit: one
-// request's, key/value head's and query tile's pass over the cache) lie on one
-// axis, and each of the workgroups that the card holds at once takes an equal
-// stretch of it, from the lengths on the device (attn_plan). A unit cut by a
-// stretch's end leaves partial results in the workspace for
-// attn_merge_kernel.
+// The next tile's rows are in flight while the present one is worked on:
+// straight into a second LDS buffer where there is one (64 trees of the sizes
+// below 291 -> 280 us against registers on the way; 32 blocks of 32 rows, heads
+// of 256, 357 -> 330), else into registers. Work is cut evenly: all steps of
+// all units (a unit: one request's, key/value head's and query tile's pass over
+// the cache) lie on one axis, and each of the workgroups that the card holds at
+// once takes an equal stretch of it, from the lengths on the device
+// (attn_plan). A unit cut by a stretch's end leaves partial results in the
+// workspace for attn_merge_kernel.
 //
 // Measured per call (bf16, 32 query and 8 key/value heads of 128, unless said
-// otherwise). 64 single tokens over 4 to 8 k rows: 300 us, 1.61 GB at 5.4 TB/s,
-// bound by HBM reads. 64 trees of 129 rows over 1 to 2 k: 295 us, 166 GFLOP at
-// 0.56 PFLOP/s; with two waves on each SIMD (the accumulators and the next tile
-// fill the registers) the matrix units are busy 27%, the vector units 37% and
-// the LDS 33% of the time, and waves wait for one another's phases the rest;
-// tiles of 32 rows with three workgroups to a CU spill (499 us), workgroups of
-// eight waves take 335. 3 chains of 17 rows over 50 to 100 k (f16, heads of 64,
-// 40 and 8): 113 us, 461 MB at 4.1 TB/s. One tree of 65 rows over 1 k: 22 us,
-// of which the merge is 5 and the steps are 6: a chain of waits.
+// otherwise). 64 single tokens over 4 to 8 k rows: 305 us, 1.61 GB at 5.3 TB/s,
+// bound by HBM reads. 64 trees of 129 rows over 1 to 2 k: 280 us, 166 GFLOP at
+// 0.59 PFLOP/s; two waves on each SIMD (the accumulators, the queries and the
+// scores fill the registers) leave the matrix units busy 27%, the vector units
+// 37% and the LDS 33% of the time (counted with registers on the way), and
+// wait the rest; tiles of 32 rows with three workgroups to a CU spill (499 us),
+// workgroups of eight waves take 335. 3 chains of 17 rows over 50 to 100 k (f16,
+// heads of 64, 40 and 8): 113 to 124 us, 461 MB at 4 TB/s. One tree of 65 rows
+// over 1 k: 22 us, of which the merge is 5 and the steps are 6: a chain of
+// waits.
 #pragma once
 
 #include "paged.hpp"
@@ -674,6 +677,16 @@ __device__ __forceinline__ void attn_clear(const AttnParams& p, int64_t b, int r
     }
 }
 
+// 64 lanes' 16-byte pieces from global memory straight into 1 KiB of LDS at
+// `to`, lane by lane. The compiler does not know of the load: the step that
+// reads the tile waits for it.
+__device__ __forceinline__ void attn_to_lds(const char* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(to), "v"(from)
+               : "memory");
+}
+
 // Steps [t0, t1) of unit u of request b, into the output or workspace slot
 // `slot` (-1: the output).
 template <typename H, class C>
@@ -709,7 +722,14 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   constexpr int STEP = QW * kWave / C::CPR;
   const int gt = wq * kWave + lane, ld_row = gt / C::CPR, ld_c = gt % C::CPR;
   unsigned char* const tiles = lds + g * C::NBUF * 2 * C::TILE;
-  at_u32x4 kr[C::LOADS], vr[C::LOADS];
+  typedef __attribute__((address_space(3))) unsigned char lds_byte;
+  const uint32_t tiles_at = (uint32_t)__builtin_amdgcn_readfirstlane(
+      (int)((uint32_t)(uintptr_t)(lds_byte*)lds + g * C::NBUF * 2 * C::TILE + wq * kWave * 16));
+  // With two buffers (in the 64 KiB that m0 reaches) a tile goes straight into
+  // LDS, its chunks' order made by the lanes' addresses; otherwise it waits in
+  // registers.
+  constexpr bool DIRECT = C::NBUF == 2 && C::LDS <= 65536;
+  at_u32x4 kr[DIRECT ? 1 : C::LOADS], vr[DIRECT ? 1 : C::LOADS];
   // the entries of the next tile's pages, as read: a test here would wait for
   // them, and with them for the tile in flight
   int page[C::LOADS];
@@ -748,7 +768,28 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
     }
   };
   auto fetch = [&](int t) {
-    if (wide) {
+    if constexpr (DIRECT) {
+      const uint32_t kt = tiles_at + (t & 1) * 2 * C::TILE;
+#pragma unroll
+      for (int k = 0; k < C::LOADS; ++k) {
+        const int row = ld_row + k * STEP;
+        const uint32_t ck = attn_k_chunk<DH>(row, ld_c) * 16, cv = attn_v_chunk<DH>(row, ld_c) * 16;
+        uint64_t at;
+        if (wide) {  // (rows behind the request's last are on the page too)
+          uint32_t pg = (uint32_t)__builtin_amdgcn_readfirstlane(page[k]);
+          pg = pg < (uint32_t)p.rows.pages ? pg : 0;
+          at = (uint64_t)pg * page_bytes +
+               (uint64_t)(uint32_t)((t * C::TR + g * C::KT + k * STEP) & row_mask) * C::ROW;
+          attn_to_lds(kh + at + (uint32_t)(ld_row * C::ROW + ck), kt + k * STEP * C::ROW);
+          attn_to_lds(vh + at + (uint32_t)(ld_row * C::ROW + cv), kt + C::TILE + k * STEP * C::ROW);
+        } else {  // rows on no page: some row's values, taken out by the mask
+          const uint32_t pg = (uint32_t)page[k] < (uint32_t)p.rows.pages ? page[k] : 0;
+          at = (uint64_t)pg * page_bytes + (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW;
+          attn_to_lds(kh + at + ck, kt + k * STEP * C::ROW);
+          attn_to_lds(vh + at + cv, kt + C::TILE + k * STEP * C::ROW);
+        }
+      }
+    } else if (wide) {
 #pragma unroll
       for (int k = 0; k < C::LOADS; ++k) {
         uint32_t pg = (uint32_t)__builtin_amdgcn_readfirstlane(page[k]);
@@ -760,20 +801,21 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
         kr[k] = *(const at_u32x4*)(kh + at + lane_at);
         vr[k] = *(const at_u32x4*)(vh + at + lane_at);
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int k = 0; k < C::LOADS; ++k) {
-      // rows on no page: some row's values, taken out by the mask
-      const uint32_t pg = (uint32_t)page[k] < (uint32_t)p.rows.pages ? page[k] : 0;
-      const uint64_t at = (uint64_t)pg * page_bytes +
-                          (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW + ld_c * 16;
-      kr[k] = *(const at_u32x4*)(kh + at);
-      vr[k] = *(const at_u32x4*)(vh + at);
+      for (int k = 0; k < C::LOADS; ++k) {
+        // rows on no page: some row's values, taken out by the mask
+        const uint32_t pg = (uint32_t)page[k] < (uint32_t)p.rows.pages ? page[k] : 0;
+        const uint64_t at = (uint64_t)pg * page_bytes +
+                            (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW + ld_c * 16;
+        kr[k] = *(const at_u32x4*)(kh + at);
+        vr[k] = *(const at_u32x4*)(vh + at);
+      }
     }
   };
   // steps before tm see every row they hold
   int tm = t0;
+  if (DIRECT) __syncthreads();  // the piece before is done with the LDS
   if (t0 < t1) {
     find(t0);
     fetch(t0);
@@ -784,13 +826,18 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
       tm = tm < t0 ? t0 : (tm > t1 ? t1 : tm);
     }
   }
-  __syncthreads();  // the piece before is done with the LDS
+  if (!DIRECT) __syncthreads();
   auto step = [&](int t, auto is_masked) {
     constexpr bool MASKED = decltype(is_masked)::value;
     unsigned char* const kt = tiles + (C::NBUF == 2 ? (t & 1) * 2 * C::TILE : 0);
     unsigned char* const vt = kt + C::TILE;
+    if constexpr (DIRECT) {  // the tile, and the next one's pages
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int k = 0; k < C::LOADS; ++k) {
+      for (int k = 0; k < C::LOADS; ++k) asm volatile("" : "+v"(page[k]));
+    }
+#pragma unroll
+    for (int k = 0; k < (DIRECT ? 0 : C::LOADS); ++k) {
       const int row = ld_row + k * STEP;
       *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, ld_c) * 16) = kr[k];
       *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, ld_c) * 16) = vr[k];

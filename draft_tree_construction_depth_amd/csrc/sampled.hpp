@@ -30,10 +30,10 @@
 // depths: accept_plan in api.hip).
 //
 // Measured per call, rows of 152 k bf16: one tree of 64 nodes 24 us (rows 12,
-// finish 15: chains of dependent loads); 64 trees 125 us: six launches of 8 to
+// finish 16: chains of dependent loads); 64 trees 120 to 126 us: six launches of 8 to
 // 13 us (a full one reads 19 MB, 4 us, and has 4 us of float64 work, both behind
 // 3 us of dependent loads), 40 to 50 us for the rows left, 16 us for the draw.
-// 64 chains of 16 guesses 162 us: seven launches of 9 to 22 us, 23 for the rows
+// 64 chains of 16 guesses 149 to 165 us: seven launches of 9 to 22 us, 23 for the rows
 // left, 28 for max(0, p - q), 14 for the draw. 8 chains of 5 guesses, 32 k
 // float32: 24 us.
 #pragma once

@@ -537,7 +537,7 @@ int launch_attn_tile(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t 
                      dim3(ddt::kAtThreads), 0, st, ap);
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   if (!pl.merge) return DDT_OK;
-  hipLaunchKernelGGL((ddt::attn_merge_kernel<H, DH, NQ, QW>), dim3((unsigned)(pl.groups * QW * ddt::AttnTile<DH, NQ, QW>::PIECES / 4)),
+  hipLaunchKernelGGL((ddt::attn_merge_kernel<H, DH, NQ, QW>), dim3((unsigned)(pl.groups * QW * ddt::AttnTile<DH, NQ, QW>::PIECES / ddt::kAtMerge)),
                      dim3(ddt::kWave), 0, st, ap);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
 }

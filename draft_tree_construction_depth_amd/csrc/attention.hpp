@@ -46,7 +46,7 @@
 // wait the rest; tiles of 32 rows with three workgroups to a CU spill (499 us),
 // workgroups of eight waves take 335. 3 chains of 17 rows over 50 to 100 k (f16,
 // heads of 64, 40 and 8): 113 to 124 us, 461 MB at 4 TB/s. One tree of 65 rows
-// over 1 k: 22 us, of which the merge is 5 and the steps are 6: a chain of
+// over 1 k: 21 us, of which the merge is 4 and the steps are 6: a chain of
 // waits.
 #pragma once
 
@@ -56,6 +56,7 @@ namespace ddt {
 
 constexpr int kAtThreads = 256;
 constexpr int kAtWaves = kAtThreads / kWave;
+constexpr int kAtMerge = 2;       // 4-float pieces per lane of a merging wave
 constexpr float kAtSlack = 8.0f;  // log2 by which a score may pass the maximum in use
 
 typedef unsigned int at_u32x4 __attribute__((ext_vector_type(4)));
@@ -962,13 +963,15 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
 }
 
 // Merges the pieces of the unit that a workgroup's stretch began and did not
-// end: a wave per stretch, query wave and four 4-float pieces of its state, as
-// a workgroup of its own (with few units cut, the pieces' bytes have to come
-// in through as many CUs as there are).
+// end: a wave per stretch, query wave and kAtMerge pieces of its state, as a
+// workgroup of its own (with few units cut, the pieces' bytes have to come in
+// through as many CUs as there are; four pieces to a wave against two: 5.0 and
+// 4.0 us for one tree, 11.3 and 8.9 for 24 units in 512 pieces, 5.0 and 5.9 for
+// the 64 trees, where it finds nothing to merge).
 template <typename H, int DH, int NQ, int QW>
 __global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
   using C = AttnTile<DH, NQ, QW>;
-  constexpr int PP = 4, PER = C::PIECES / PP;  // waves of a state
+  constexpr int PP = kAtMerge, PER = C::PIECES / PP;  // waves of a state
   const int k = (int)(blockIdx.x / (QW * PER)), r = (int)(blockIdx.x % (QW * PER));
   const AttnPlace pl = p.place[k];
   if (pl.pieces == 0) return;

@@ -57,7 +57,19 @@ namespace ddt {
 constexpr int kAtThreads = 256;
 constexpr int kAtWaves = kAtThreads / kWave;
 constexpr int kAtMerge = 2;       // 4-float pieces per lane of a merging wave
-constexpr float kAtSlack = 8.0f;  // log2 by which a score may pass the maximum in use
+
+// Weights are 2^kBias at the maximum in use, which a score may pass by kSlack
+// (log2): up to 2^8 in bf16, whose relative precision is the same at any size.
+// A float16 weight loses bits below 2^-14 and is 0 below 2^-25, so its weights
+// use the type's whole range: 2^14 at the maximum, 2^15 at most (65504 is the
+// largest), full precision down to 2^-28 of the maximum in use and steps of
+// 2^-38 of it below (n keys there put the output off by at most n 2^-39 |V|).
+// The factor stays in the running sum and leaves with it.
+template <typename H>
+struct AttnWeight {
+  static constexpr float kBias = __is_same(H, __bf16) ? 0.0f : 14.0f;
+  static constexpr float kSlack = __is_same(H, __bf16) ? 8.0f : 1.0f;
+};
 
 typedef unsigned int at_u32x4 __attribute__((ext_vector_type(4)));
 typedef short at_s16x4 __attribute__((ext_vector_type(4)));
@@ -383,7 +395,7 @@ struct AttnState;
 template <int DH>
 struct AttnState<DH, 32> {
   static constexpr int PIECES = DH / 8, R = 16;  // registers of an accumulator
-  float m, mref, l;  // maximum in use (log2), the same or 0 while it is -inf, sum of weights
+  float m, mref, l;  // maximum in use (log2), the same less kBias or 0 while it is -inf, sum of weights
   at_f32x16 o[DH / 32];
   __device__ __forceinline__ at_f32x4 get(int j) const {
     const at_f32x16& x = o[j >> 2];
@@ -502,10 +514,10 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
 #pragma unroll
     for (int r = 0; r < R; ++r) top = fmaxf(top, s[t][r]);
   top = attn_max_across<NQ>(top) * scale2;
-  // The maximum moves only when a score passes it by 2^8: weights up to 256
-  // keep their relative precision in either type.
-  if (__ballot(top > st.m + kAtSlack) != 0) {
-    const float m = top > st.m + kAtSlack ? top : st.m;
+  // The maximum moves only when a score passes it by more than kSlack.
+  typedef AttnWeight<H> Weight;
+  if (__ballot(top > st.m + Weight::kSlack) != 0) {
+    const float m = top > st.m + Weight::kSlack ? top : st.m;
     const float keep = m > st.m ? __builtin_amdgcn_exp2f(st.m - m) : 1.0f;
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -513,7 +525,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
       for (int r = 0; r < R; ++r) st.o[d][r] *= keep;
     st.l *= keep;
     st.m = m;
-    st.mref = m > -INFINITY ? m : 0.0f;
+    st.mref = m > -INFINITY ? m - Weight::kBias : 0.0f;
   }
   // Rows that a query does not see have weight 0, but 0 times a NaN or an
   // infinity among their values is no 0: such values (garbage behind the
@@ -646,7 +658,8 @@ __device__ __forceinline__ void attn_store(const AttnParams& p, int64_t row, int
     *(uint64_t*)(out + AttnState<DH, NQ>::element(j0 + j, lane)) = __builtin_bit_cast(uint64_t, x);
   }
   if (p.lse && lane < NQ && j0 == 0)
-    p.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    p.lse[row] =
+        none ? -INFINITY : (m + (log2f(l) - AttnWeight<H>::kBias)) * 0.6931471805599453f;
 }
 
 // Whether cache rows [r0, r1) of request b lie on pages of the pool; every

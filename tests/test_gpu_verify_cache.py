@@ -197,6 +197,32 @@ def test_attention_of_a_strongly_peaked_softmax():
     assert torch.isfinite(got["lse"]).all()
 
 
+# T * Hq / Hkv rows share a key/value head: one size for each arrangement of waves
+TILES = [(1, 2), (3, 8), (9, 6), (33, 3)]
+
+
+@pytest.mark.parametrize("every", [False, True], ids=["one", "many"])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("T,G", TILES, ids=[f"{t * g}rows" for t, g in TILES])
+def test_attention_of_float16_keys_far_below_one_that_adds_nothing(T, G, dh, every):
+    """One key whose value is 0 (or one in every 32), thousands 16 to 18 nats below it with values:
+    all of the output comes from weights of 1e-7 to 1e-8 of the largest, which float16 would hold as
+    0 or with a few bits if the largest were held as 1."""
+    rng = np.random.default_rng(T * dh)
+    past = np.array([4991, 300], np.int32)
+    n = int(past.max()) + T
+    q = torch.zeros((2, T, 2 * G, dh), dtype=HF)
+    q[..., 0] = 1.0
+    kc, vc = torch.zeros((2, 2, n, dh), dtype=HF), torch.ones((2, 2, n, dh), dtype=HF)
+    kc[..., 0] = torch.from_numpy(rng.uniform(2.0, 4.0, (2, 2, n))).to(HF)
+    if every:
+        vc *= 256.0
+        kc[:, :, 3::32, 0], vc[:, :, 3::32] = 20.0, 0.0
+    kc[:, :, 70, 0], vc[:, :, 70] = 20.0, 0.0
+    got = check_attention(q, kc, vc, past, None, None, None, scale=1.0)
+    assert (got["out"][0] > 5e-5).all()
+
+
 def test_attention_with_garbage_where_nothing_is_seen():
     """NaN and infinities in rows behind the block, on unmapped pages, in pages of
     others, and in a sibling's row do not reach the rows that do not see them."""

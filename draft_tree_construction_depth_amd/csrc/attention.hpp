@@ -527,6 +527,19 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     st.m = m;
     st.mref = m > -INFINITY ? m - Weight::kBias : 0.0f;
   }
+  // The weights' exponents score * scale2 - maximum are formed by an FMA, whose
+  // product is not rounded, while the maximum's was. Past 2^20 that difference
+  // (2^-5 there, whole powers of two from 2^25 on) would be the largest score's
+  // weight, so those products are rounded first, as the maximum's.
+  const bool far = __ballot(fabsf(st.mref) > 0x1p20f) != 0;
+  if (far) {
+#pragma clang fp contract(off)
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[t][r] *= scale2;
+  }
+  const float factor = far ? 1.0f : scale2;
   // Rows that a query does not see have weight 0, but 0 times a NaN or an
   // infinity among their values is no 0: such values (garbage behind the
   // block, on unmapped pages, or in other nodes' rows) are taken out of the
@@ -548,7 +561,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
   };
   float sum[2] = {0.0f, 0.0f};
   auto weigh = [&](int u, int i) {
-    const float w = __builtin_amdgcn_exp2f(fmaf(score(u, i), scale2, -st.mref));
+    const float w = __builtin_amdgcn_exp2f(fmaf(score(u, i), factor, -st.mref));
     if (NQ == 32)
       s[u >> 1][(8 * (u & 1) + i) % R] = w;
     else

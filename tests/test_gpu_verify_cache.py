@@ -223,6 +223,33 @@ def test_attention_of_float16_keys_far_below_one_that_adds_nothing(T, G, dh, eve
     assert (got["out"][0] > 5e-5).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,G", TILES, ids=[f"{t * g}rows" for t, g in TILES])
+def test_attention_of_scores_beyond_what_float32_steps_resolve(T, G, dtype):
+    """Scores near 2^36, where a float32 step is 4096: the largest takes all the weight, equal ones
+    share it, however scale and score are multiplied."""
+    rng = np.random.default_rng(T)
+    dh, n, past = 128, 200 + T, np.array([200, 9], np.int32)
+    big = 2.0 ** 15
+    q = torch.zeros((2, T, 2 * G, dh), dtype=dtype)
+    q[..., 0] = big
+    kc, vc = torch.zeros((2, 2, n, dh), dtype=dtype), rounded(rng, (2, 2, n, dh), dtype)
+    # 128 values that both types hold, each a part in 128 or more from the next
+    kc[..., 0] = torch.from_numpy(rng.integers(128, 255, (2, 2, n)) * big / 256).to(dtype)
+    top = big * 255 / 256
+    kc[0, :, 5, 0] = kc[0, :, 190, 0] = kc[1, :, 0, 0] = top
+    scale = 77.7  # no power of two: scores are not held as they are
+    got = pkg.ddtree_attention(q.to(DEV), kc.to(DEV), vc.to(DEV), dev(past), scale=scale, with_lse=True)
+    vd = vc.to(DEV)
+    mean = (vd[0, :, 5].double() + vd[0, :, 190].double()) / 2
+    want = torch.stack([mean, vd[1, :, 0].double()])[:, None, :, None].expand(2, T, 2, G, dh)
+    out = got["out"].double().view(2, T, 2, G, dh)
+    # weights of 1 and 1/2 are exact: the output is rounded once
+    assert ((out - want).abs() <= torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -25).all()
+    lse = scale * big * top
+    assert ((got["lse"].double() - lse).abs() <= 2.0 ** -21 * lse).all()
+
+
 def test_attention_with_garbage_where_nothing_is_seen():
     """NaN and infinities in rows behind the block, on unmapped pages, in pages of
     others, and in a sibling's row do not reach the rows that do not see them."""

@@ -409,7 +409,8 @@ __device__ __forceinline__ void sv_hit(SvTree& t, int node, int n, double at) {
     kids = __ballot(kid);
     const double w = kid ? t.w[j] : 0.0;
     const double cum = base + wave_incl_scan_f64(w);
-    const uint64_t hit = __ballot(kid && at < cum);
+    // (the scan's rounding may pass `at` at a child without weight)
+    const uint64_t hit = __ballot(kid && w > 0.0 && at < cum);
     if (kid) {
       t.tok[kept + lanes_below(kids)] = tok;
       t.part[kept + lanes_below(kids)] = w;

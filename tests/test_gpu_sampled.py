@@ -174,6 +174,36 @@ def test_infinite_logits_at_great_temperatures():
                  O.accept_chain(tok, None, xh, yh, heat, u.astype(np.float64)), CHAIN)
 
 
+# Eight logits (in steps of 2^-10) and the place among their children of one without weight, such that
+# half the row's sum lies between the children's running sums before and behind that place: the float64
+# scan over lanes rounds differently from lane to lane, so the latter is a step larger.
+BORDERS = [
+    (8, [366, 1422, 993, 432, 808, 3269, 3609, 249]),
+    (8, [2510, 1047, 1620, 3342, 3550, 123, 3174, 1055]),
+    (8, [743, 2201, 1327, 3954, 4, 619, 578, 3046]),
+    (8, [3686, 392, 230, 3320, 2637, 3691, 572, 2991]),
+    (8, [183, 686, 93, 3085, 3636, 1636, 640, 4006]),
+    (8, [3692, 1355, 3318, 577, 146, 874, 61, 2968]),
+    (8, [188, 2180, 386, 1589, 1929, 4065, 2830, 3728]),
+    (8, [2118, 98, 229, 3710, 4081, 302, 3040, 212]),
+]
+
+
+def test_a_child_without_weight_is_never_accepted():
+    """A masked child behind others: however sums round, no number falls on it."""
+    batch, B, V = len(BORDERS), 9, 20
+    x = np.full((batch, B + 1, V), -np.inf, np.float32)
+    tok = np.zeros((batch, B), np.int32)
+    for b, (at, steps) in enumerate(BORDERS):
+        x[b, :, :8] = x[b, :, 8:16] = np.array(steps) / 1024
+        tok[b] = np.insert(np.arange(8), at, 16)
+    par, u = np.zeros((batch, B), np.int32), np.full((batch, 2), 0.5, np.float32)
+    got = pkg.ddtree_accept_sampled(dev(tok), dev(par), None, dev(x), None, dev(u))
+    path, n, last, logp = (got[k].cpu().numpy() for k in TREE)
+    taken = np.where(n > 0, tok[np.arange(batch), np.maximum(path[:, 0], 1) - 1], last)
+    assert (taken < 16).all() and (last < 16).all() and np.isfinite(logp).all()
+
+
 def test_tree_acceptance_gives_the_target_distribution():
     """4096 requests with evenly spread numbers: every first token comes out 4096 p(v) times."""
     rng = np.random.default_rng(5)

@@ -124,7 +124,8 @@ __global__ __launch_bounds__(kKvThreads) void kv_compact_paged_kernel(KvPagedPar
   const int past = p.past_len[b];
   int n = p.accept_len[b];
   n = n < 0 ? 0 : (n > p.L ? p.L : n);
-  if (part == 0 && lane == 0 && p.new_len) p.new_len[b] = past + n + 1;
+  // (a request taken out stays out)
+  if (part == 0 && lane == 0 && p.new_len) p.new_len[b] = past < 0 ? past : past + n + 1;
   if (past < 0 || n == 0) return;
   const int64_t head_bytes = (int64_t)p.rows.page_size * p.row_bytes;
   // byte offset of cache row r in a layer's head 0, -1 where no page holds it

@@ -252,7 +252,8 @@ int ddtree_compact_kv(void* k_cache, void* v_cache, int64_t layers, int64_t batc
  * rows 0..num_nodes[b] take part (num_nodes NULL: all; values are clamped
  * into [0, T - 1]). T = 1 is plain decoding. A negative past_len[b] takes the
  * request out: nothing is written for it, and its attention is that of rows
- * that see nothing.
+ * that see nothing. (ddtree_compact_kv, on contiguous caches, knows no such
+ * requests: its new_len is past_len + accept_len + 1 for every request.)
  */
 
 /*
@@ -329,8 +330,9 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
  * i = 1..accept_len[b], take the rows at past_len[b] + accepted_nodes[b][i-1]
  * in every layer and head, in place; every other row is left as it was. Rows
  * whose source or destination no page holds are skipped, as is a request with
- * a negative past_len. new_len, row_bytes, L and alignment as in
- * ddtree_compact_kv; page_table is required here.
+ * a negative past_len, whose new_len is that past_len: it stays taken out.
+ * Otherwise new_len, and row_bytes, L and alignment, as in ddtree_compact_kv;
+ * page_table is required here.
  */
 int ddtree_compact_kv_paged(void* k_cache, void* v_cache, int64_t layers, int64_t pages,
                             int32_t heads, int32_t page_size, int32_t row_bytes,

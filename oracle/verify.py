@@ -9,7 +9,8 @@ Readings: the block's row j (0 the root) lies at cache row past + j and stands
 at text position past + depth(j); a request's row r lies on page
 table[r // page_size] (none where that entry is outside the pool); row i of
 the block sees every committed row and the block's rows whose bit is set in
-its mask row (no mask: j <= i). A negative past takes the request out.
+its mask row (no mask: j <= i). A negative past takes the request out, and it
+stays out: the compaction's new length is that past.
 """
 
 from __future__ import annotations
@@ -124,7 +125,7 @@ def compact_paged(k, v, table, past_len, accepted, accept_len):
                 k2[:, d[0], :, d[1]] = k[:, s[0], :, s[1]]
                 v2[:, d[0], :, d[1]] = v[:, s[0], :, s[1]]
     n = np.clip(accept_len, 0, accepted.shape[1])
-    return k2, v2, (past_len + n + 1).astype(np.int32)
+    return k2, v2, np.where(past_len < 0, past_len, past_len + n + 1).astype(np.int32)
 
 
 # ---- acceptance at a temperature --------------------------------------------

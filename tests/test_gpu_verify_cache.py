@@ -400,6 +400,26 @@ def test_compact_paged(case):
     assert np.array_equal(nl.cpu().numpy(), ne)
 
 
+def test_a_request_taken_out_stays_out_from_round_to_round():
+    """Two rounds of append and compaction, each from the lengths that the one before gave: a
+    request taken out, whatever its accept_len, keeps its length and its old pages' rows."""
+    rng = np.random.default_rng(15)
+    T, ps, dh, batch = 5, 8, 64, 4
+    past = np.array([6, -1, 11, -3], np.int32)
+    table = rng.permutation(batch * 4).astype(np.int32).reshape(batch, 4)
+    kc, vc = (rounded(rng, (1, batch * 4, 2, ps, dh), BF) for _ in range(2))
+    kd, vd, pd = kc.to(DEV), vc.to(DEV), dev(past)
+    acc = np.tile(np.array([1, 3, 4], np.int32), (batch, 1))
+    for n in (np.array([2, 0, 3, 2], np.int32), np.array([0, 3, 1, 99], np.int32)):
+        k, v = rounded(rng, (batch, T, 2, dh), BF), rounded(rng, (batch, T, 2, dh), BF)
+        pkg.ddtree_append_kv(None, k.to(DEV), v.to(DEV), kd[0], vd[0], pd, page_table=dev(table))
+        pd = pkg.ddtree_compact_kv_paged(kd, vd, dev(table), pd, dev(acc), dev(n))
+        past = np.where(past < 0, past, past + np.minimum(n, 3) + 1)
+        assert np.array_equal(pd.cpu().numpy(), past)
+    for b in (1, 3):
+        assert torch.equal(kd[0, table[b]].cpu(), kc[0, table[b]]) and torch.equal(vd[0, table[b]].cpu(), vc[0, table[b]])
+
+
 # ---- refusals of the binding ------------------------------------------------------
 def test_binding_refusals():
     q = torch.zeros((2, 3, 4, 64), dtype=BF, device=DEV)

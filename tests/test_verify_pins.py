@@ -119,6 +119,14 @@ def test_paged_compaction_equals_contiguous():
     assert np.array_equal(nl, pl)
 
 
+def test_a_request_taken_out_stays_out_of_the_compaction():
+    k = np.arange(2.0 * 4 * 8).reshape(1, 2, 1, 8, 4)
+    table, acc = np.array([[0], [1]]), np.array([[2, 3], [1, 2]], np.int32)
+    for past in (-1, -2 ** 31):
+        k2, _, nl = O.compact_paged(k, k, table, np.array([3, past], np.int32), acc, np.array([2, 2], np.int32))
+        assert nl.tolist() == [6, past] and np.array_equal(k2[0, 1], k[0, 1])
+
+
 # ---- acceptance -----------------------------------------------------------------
 def test_tree_line_gives_the_target_distribution():
     """Over evenly spread numbers every first token comes out N p(v) times, whatever the tree."""

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import os
+import threading
 
 import torch
 
@@ -148,15 +149,34 @@ def _check(fn, rc):
         raise DDTreeError(fn, rc)
 
 
-_workspaces: dict = {}
+class _Workspaces(threading.local):
+    """The calling thread's own workspaces. A call into the library releases the interpreter
+    lock and enqueues several launches, so two threads' launches on one stream (the default one
+    is every thread's) may lie between one another's: they must not share a workspace. A
+    thread's buffers go with it; the allocator keeps their next use behind the stream's work."""
+
+    def __init__(self):
+        self.held: dict = {}
+
+    def get(self, key):
+        return self.held.get(key)
+
+    def __setitem__(self, key, ws):
+        self.held[key] = ws
+
+    def __iter__(self):
+        return iter(self.held)
+
+
+_workspaces = _Workspaces()
 
 
 def workspace(kind: str, size: int, device, key) -> torch.Tensor:
-    """Scratch buffer cached per (kind, device, stream, shape key).
+    """Scratch buffer cached per thread and (kind, device, stream, shape key).
 
     The library ignores a workspace's contents on entry, so one buffer per
     shape is reused across calls; calls on different streams may overlap and
-    so get buffers of their own.
+    those of different threads interleave, and so get buffers of their own.
     """
     k = (kind, str(device), torch.cuda.current_stream(device).cuda_stream, key)
     ws = _workspaces.get(k)
@@ -505,10 +525,10 @@ def _maybe_arg(t, name, dtype, shape, dev):
 
 
 def _ws_arg(kind, size, ws, dev):
-    """Pointer and size of the workspace of one call: the caller's, or the
-    stream's own of this kind (grown as needed), or, under graph capture, one of
-    the graph's, so that no two graphs and no eager call share it. The second
-    return value keeps it alive until the call is enqueued."""
+    """Pointer and size of the workspace of one call: the caller's, or this
+    thread's own for the stream and kind (grown as needed), or, under graph
+    capture, one of the graph's, so that no two graphs and no eager call share
+    it. The second return value keeps it alive until the call is enqueued."""
     if ws is not None:
         if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
             raise ValueError("ws must be a contiguous device tensor")

@@ -23,6 +23,38 @@ def L():
     return _lib.lib()
 
 
+def test_threads_have_workspaces_of_their_own(monkeypatch):
+    """The binding's hidden workspaces on one stream: one for each thread, kept from call to call
+    and grown, whichever of the two ways a call asks for it."""
+    import threading
+    import types
+
+    import torch
+    monkeypatch.setattr(_lib, "_raw_stream", lambda dev: 77)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    cpu, got, all_here = torch.device("cpu"), {}, threading.Barrier(3)
+
+    def calls(me):
+        first = [_lib._ws_arg("a thread's", 100, None, cpu)[1] for _ in range(2)]
+        first += [_lib.workspace("a thread's", 100, cpu, (1, 2)) for _ in range(2)]
+        all_here.wait(30)  # every thread's workspaces are held at this moment
+        grown = _lib._ws_arg("a thread's", 200, None, cpu)[1]
+        got[me] = (first, grown)
+        all_here.wait(30)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert len(got) == 3
+    for (a, b, c, d), grown in got.values():
+        assert a is b and c is d and grown is not a and grown.numel() >= 200
+    assert len({first[k].data_ptr() for first, _ in got.values() for k in (0, 2)}) == 6
+    assert not any(k[0] == "a thread's" for k in _lib._workspaces)  # nothing in this thread
+
+
 def declared_functions():
     text = open(HEADER).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)

@@ -11,6 +11,8 @@ the output is rounded once. lse: the score's error, the sum's, and 2^-22 of
 its value and of the largest exponent argument's.
 """
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -352,6 +354,42 @@ def test_attention_is_deterministic_and_streams_keep_apart():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, ref[i]) for o in got[i])
+
+
+def test_threads_on_one_stream_keep_apart():
+    """Several host threads on the default stream at once, attention and acceptance with the
+    binding's own workspaces: every result is that of the call made alone."""
+    rng = np.random.default_rng(14)
+    sets = []
+    for i in range(4):
+        past = np.array([700 + 400 * i, 2000 - 300 * i, 33], np.int32)
+        table, pool = paging(rng, 3, past + 5, 32)
+        att = [rounded(rng, s, BF).to(DEV) for s in ((3, 5, 8, 128), (pool, 2, 32, 128), (pool, 2, 32, 128))]
+        par = dev(np.array([[0, 0, 1, 2, 2, 4]] * 3, np.int32))
+        tok = dev(rng.permutation(5000)[:18].astype(np.int32).reshape(3, 6))
+        sets.append((att, dev(past), dev(table), tok, par,
+                     dev(rng.standard_normal((3, 7, 20000), dtype=np.float32)), dev(rng.random((3, 5), dtype=np.float32))))
+
+    def run(s):
+        att, past, table, tok, par, x, u = s
+        return (pkg.ddtree_attention(*att, past, page_table=table)["out"],
+                *pkg.ddtree_accept_sampled(tok, par, None, x, None, u).values())
+    ref = [run(s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[] for _ in sets]
+
+    def calls(i):
+        for _ in range(30):
+            got[i].append(run(sets[i]))
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for want, outs in zip(ref, got):
+        assert len(outs) == 30
+        assert all(torch.equal(g, w) for out in outs for g, w in zip(out, want))
 
 
 def test_attention_offsets_beyond_32_bits():

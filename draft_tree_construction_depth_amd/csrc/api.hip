@@ -467,6 +467,9 @@ int paged_rows(const int32_t* table, int64_t width, int64_t batch, int64_t pages
   return DDT_OK;
 }
 
+// Whether one launch takes `blocks` workgroups: it has fewer than 2^32 threads.
+bool launchable(int64_t blocks, int threads) { return blocks <= 0xFFFFFFFFLL / threads; }
+
 bool valid_half(int dtype) { return dtype == DDT_BF16 || dtype == DDT_F16; }
 
 template <typename H>
@@ -568,7 +571,7 @@ int attn_check(int dtype, int64_t batch, int32_t T, int32_t q_heads, int32_t kv_
   if (q_heads % kv_heads != 0) return DDT_EINVAL;
   if (T > DDT_MAX_B + 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return DDT_ENOTSUP;
-  // query rows (and with them the launches' workgroups) are counted in 31 bits
+  // keeps the plan's counts far below 63 bits; the launch itself is tested with the plan
   if (batch > 0x1FFFFFFFLL || batch * T > 0x1FFFFFFFLL / q_heads) return DDT_ENOTSUP;
   return DDT_OK;
 }
@@ -579,6 +582,7 @@ struct SvPlan {
   int depths;  // whose path rows have a launch of their own, before the one for all rows left
   int slices;  // workgroups that share a request's rows in the latter
   size_t rec, rec_q, state, rest, end;
+  bool fits;  // each of the launches takes its workgroups
 };
 
 // Chunks of a row (whose first vector may start before it).
@@ -591,7 +595,7 @@ int64_t accept_chunks(int64_t V, int dtype) {
 int accept_check(int dtype, int64_t batch, int32_t T, int32_t L, int64_t V) {
   if (!valid_dtype(dtype) || batch < 0 || T <= 1 || L <= 0 || V <= 0) return DDT_EINVAL;
   if (T > DDT_MAX_B + 1 || L > DDT_MAX_L || V > ((int64_t)1 << 22)) return DDT_ENOTSUP;
-  // workgroups of a launch: a chunk of every row, for chains of two
+  // chunks of all rows, for chains of two, are counted in 31 bits
   if (batch > 0x7FFFFFFFLL / (2 * T * accept_chunks(V, dtype))) return DDT_ENOTSUP;
   return DDT_OK;
 }
@@ -628,6 +632,10 @@ SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bo
   pl.rest = o;
   if (chain) o = align_up(o + (size_t)batch * pl.S * sizeof(double));
   pl.end = o;
+  const int64_t chunks = batch * pl.S;
+  pl.fits = launchable((chain ? 2 : 1) * chunks, ddt::kSvThreads) &&
+            launchable(chunks * pl.slices, ddt::kSvThreads) &&
+            (!chain || launchable(chunks, ddt::kSvRest)) && launchable(batch, ddt::kSvFinish);
   return pl;
 }
 
@@ -932,6 +940,7 @@ int ddtree_compact_kv_paged(void* k_cache, void* v_cache, int64_t layers, int64_
   kp.each = (int32_t)each;
   if (batch > 0x7FFFFFFFLL / kp.waves) return DDT_ENOTSUP;
   const int64_t blocks = (batch * kp.waves + per_block - 1) / per_block;
+  if (!launchable(blocks, ddt::kKvThreads)) return DDT_ENOTSUP;
   kp.k = (unsigned char*)k_cache;
   kp.v = (unsigned char*)v_cache;
   kp.layers = layers;
@@ -977,7 +986,7 @@ int ddtree_append_kv(const void* q, const void* k, const void* v, int dtype, int
     return DDT_ENOTSUP;
   if ((q_heads > 0 && q_stride % 8 != 0) || k_stride % 8 != 0 || v_stride % 8 != 0)
     return DDT_ENOTSUP;
-  if (batch > 0x7FFFFFFFLL / T) return DDT_ENOTSUP;
+  if (batch > 0x7FFFFFFFLL / T || !launchable(batch * T, ddt::kApThreads)) return DDT_ENOTSUP;
   ap.q = q;
   ap.k = k;
   ap.v = v;
@@ -1013,7 +1022,8 @@ size_t ddtree_attention_workspace_size(int64_t batch, int32_t T, int32_t q_heads
   const int64_t cap = pages_per_request > 0x7FFFFFFFLL / page_size
                           ? 0x7FFFFFFFLL
                           : pages_per_request * page_size;
-  return attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap).end;
+  const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap);
+  return launchable(pl.grid, ddt::kAtThreads) ? pl.end : 0;
 }
 
 int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
@@ -1038,6 +1048,7 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   if (ap.rows.cap > (1 << 27) ||  // the plan counts steps in 32 bits
       (page_table && (int64_t)kv_heads * page_size > (((int64_t)1 << 32) - 1) / (2 * head_dim)))
     return DDT_ENOTSUP;  // ... and a page's bytes are addressed in 32
+  if (!launchable(pl.grid, ddt::kAtThreads)) return DDT_ENOTSUP;
   if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
   ap.q = q;
   ap.k_cache = k_cache;
@@ -1067,7 +1078,8 @@ size_t ddtree_accept_sampled_workspace_size(int64_t batch, int32_t B, int32_t L,
                                             int dtype) {
   if (batch <= 0 || B <= 0 || B > DDT_MAX_B || accept_check(dtype, batch, B + 1, L, V) != DDT_OK)
     return 0;
-  return accept_plan(batch, B + 1, L, V, dtype, false).end;
+  const SvPlan pl = accept_plan(batch, B + 1, L, V, dtype, false);
+  return pl.fits ? pl.end : 0;
 }
 
 int ddtree_accept_sampled(const int32_t* tree_tokens, const int32_t* parents,
@@ -1085,6 +1097,7 @@ int ddtree_accept_sampled(const int32_t* tree_tokens, const int32_t* parents,
     return DDT_EINVAL;
   if (((uintptr_t)target_logits | (uintptr_t)workspace) & 15) return DDT_EINVAL;
   const SvPlan pl = accept_plan(batch, B + 1, L, V, dtype, false);
+  if (!pl.fits) return DDT_ENOTSUP;
   if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
   char* ws = (char*)workspace;
   ddt::SvParams sp{};
@@ -1114,7 +1127,8 @@ int ddtree_accept_sampled(const int32_t* tree_tokens, const int32_t* parents,
 size_t dspark_accept_sampled_workspace_size(int64_t batch, int32_t P, int64_t V, int dtype) {
   if (batch <= 0 || P <= 0 || P > DDT_MAX_L || accept_check(dtype, batch, P + 1, P, V) != DDT_OK)
     return 0;
-  return accept_plan(batch, P + 1, P, V, dtype, true).end;
+  const SvPlan pl = accept_plan(batch, P + 1, P, V, dtype, true);
+  return pl.fits ? pl.end : 0;
 }
 
 int dspark_accept_sampled(const int32_t* tokens, const int32_t* keep, const void* target_logits,
@@ -1131,6 +1145,7 @@ int dspark_accept_sampled(const int32_t* tokens, const int32_t* keep, const void
   if (((uintptr_t)target_logits | (uintptr_t)draft_logits | (uintptr_t)workspace) & 15)
     return DDT_EINVAL;
   const SvPlan pl = accept_plan(batch, P + 1, P, V, dtype, true);
+  if (!pl.fits) return DDT_ENOTSUP;
   if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
   char* ws = (char*)workspace;
   ddt::SvParams sp{};

@@ -254,6 +254,11 @@ int ddtree_compact_kv(void* k_cache, void* v_cache, int64_t layers, int64_t batc
  * request out: nothing is written for it, and its attention is that of rows
  * that see nothing. (ddtree_compact_kv, on contiguous caches, knows no such
  * requests: its new_len is past_len + accept_len + 1 for every request.)
+ *
+ * No launch has 2^32 threads or more: batches beyond that (from 2^24 rows of
+ * all blocks on for the append; pairs of a single-token request and a key/value
+ * head for the attention) are refused with DDT_ENOTSUP, here and by the
+ * acceptance at a temperature below.
  */
 
 /*

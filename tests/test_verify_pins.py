@@ -262,6 +262,44 @@ def test_paged_compaction_refusals(L):
     assert call(batch=0) == call(layers=0) == call(heads=0) == 0
 
 
+def test_calls_of_more_than_a_launch_are_refused(L):
+    """A launch has fewer than 2^32 threads. One request more than fits, or far more: refused by
+    size on the host, and no workspace is asked for."""
+    def append(batch, T=1):
+        return L.ddtree_append_kv(None, FAKE, FAKE, 0, batch, T, 0, 1, 8, 0, 8, 8, None, 0, 0, 0, FAKE, None, None,
+                                  FAKE, 1, 16, 16, FAKE, FAKE, None, None)
+    for batch in (1 << 24, 1 << 30):
+        assert append(batch) == -2, batch
+    assert append(32705, 513) == -2  # 256 * 32705 * 513: just past 2^32
+
+    def attend(batch, T, Hq, Hkv):
+        n = L.ddtree_attention_workspace_size(batch, T, Hq, Hkv, 64, 1, 16)
+        return n, L.ddtree_attention(FAKE, 0, batch, T, Hq, Hkv, 64, FAKE, FAKE, FAKE, 1, 16, 16, FAKE, None, None,
+                                     0.1, FAKE, None, FAKE, 1 << 60, None)
+    for args in ((1 << 24, 1, 1, 1), (1 << 21, 1, 8, 8), (1 << 26, 1, 8, 8), (1 << 18, 513, 8, 8)):
+        assert attend(*args) == (0, -2), args
+
+    def compact(batch, layers=1):
+        return L.ddtree_compact_kv_paged(FAKE, FAKE, layers, 16, 1, 16, 16, FAKE, 1, batch, FAKE, FAKE, FAKE, 1, None,
+                                         None)
+    for args in ((1 << 26, 1), (1 << 22, 256), (1 << 30, 1)):
+        assert compact(*args) == -2, args
+
+    def tree(batch, B, V):
+        n = L.ddtree_accept_sampled_workspace_size(batch, B, 32, V, 0)
+        return n, L.ddtree_accept_sampled(FAKE, FAKE, None, FAKE, 0, None, FAKE, batch, B, 32, V, FAKE, FAKE, FAKE,
+                                          None, FAKE, 1 << 60, None)
+
+    def chain(batch, P, V):
+        n = L.dspark_accept_sampled_workspace_size(batch, P, V, 0)
+        return n, L.dspark_accept_sampled(FAKE, None, FAKE, FAKE, 0, None, FAKE, batch, P, V, FAKE, FAKE, None, FAKE,
+                                          1 << 60, None)
+    for args in ((1 << 22, 1, 1), (1 << 28, 1, 1), (1 << 16, 512, 1)):
+        assert tree(*args) == (0, -2), args
+    for args in ((1 << 22, 1, 1), (1 << 28, 1, 1), (1 << 19, 32, 1)):
+        assert chain(*args) == (0, -2), args
+
+
 def test_acceptance_refusals(L):
     size = L.ddtree_accept_sampled_workspace_size
     assert size(4, 64, 15, 151936, 0) > 0 and size(4, 513, 15, 151936, 0) == 0

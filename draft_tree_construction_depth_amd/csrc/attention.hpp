@@ -163,6 +163,23 @@ struct AttnPos {
   int b, u, s;
 };
 
+// attn_plan's shared memory.
+struct AttnScratch {
+  int64_t part[kAtWaves][2];
+  int longest[kAtWaves];
+  AttnPos pos[2];
+};
+
+// A workgroup's shared memory, all of it in one object, so that the tiles lie
+// at its start: loads straight into LDS go to the 64 KiB that m0's 16 bits
+// reach, which the tiles may fill.
+template <class C>
+struct AttnLds {
+  alignas(256) unsigned char tiles[C::LDS];
+  int any[kAtWaves];
+  AttnScratch plan;
+};
+
 // The cut of the axis: end e of n stretches lies at total * e / n.
 struct AttnCut {
   int64_t n, total, range, extra, slack;
@@ -205,11 +222,8 @@ __device__ __forceinline__ int64_t attn_near(const AttnCut& c, int64_t s, int st
 // < 0): the units' cache rows are then read by a key/value head's query tiles
 // at the same time, and the hardware deals the units out as they end.
 template <class C>
-__device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnCut& cut, AttnPos& from,
-                          AttnPos& to) {
-  __shared__ int64_t s_part[kAtWaves][2];
-  __shared__ int s_long[kAtWaves];
-  __shared__ AttnPos s_pos[2];
+__device__ bool attn_plan(const AttnParams& p, AttnScratch& sh, int w, int& k, AttnCut& cut,
+                          AttnPos& from, AttnPos& to) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   auto axis = [&](int64_t b, int64_t& units, int& steps) {
     units = 0;
@@ -235,17 +249,17 @@ __device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnCut& cut, Attn
     all_units = attn_wave_scan(all_units);
     longest = wave_max(longest);
     if (lane == 63) {
-      s_part[wave][0] = total;
-      s_part[wave][1] = all_units;
-      s_long[wave] = longest;
+      sh.part[wave][0] = total;
+      sh.part[wave][1] = all_units;
+      sh.longest[wave] = longest;
     }
     __syncthreads();
     total = all_units = 0;
 #pragma unroll
     for (int i = 0; i < kAtWaves; ++i) {
-      total += s_part[i][0];
-      all_units += s_part[i][1];
-      longest = s_long[i] > longest ? s_long[i] : longest;
+      total += sh.part[i][0];
+      all_units += sh.part[i][1];
+      longest = sh.longest[i] > longest ? sh.longest[i] : longest;
     }
   }
   const bool whole = all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
@@ -290,25 +304,25 @@ __device__ bool attn_plan(const AttnParams& p, int w, int& k, AttnCut& cut, Attn
       axis(b, units, steps);
       const int64_t mine = whole ? units : units * steps;
       int64_t incl = attn_wave_scan(mine);
-      __syncthreads();  // s_part's readers before this round
-      if (lane == 63) s_part[wave][0] = incl;
+      __syncthreads();  // sh.part's readers before this round
+      if (lane == 63) sh.part[wave][0] = incl;
       __syncthreads();
       int64_t all = 0;
 #pragma unroll
       for (int i = 0; i < kAtWaves; ++i) {
-        incl += i < wave ? s_part[i][0] : 0;
-        all += s_part[i][0];
+        incl += i < wave ? sh.part[i][0] : 0;
+        all += sh.part[i][0];
       }
       const int64_t before = base + incl - mine;
-      if (x0 >= before && x0 < before + mine) place(k, before, (int)b, s_pos[0]);
+      if (x0 >= before && x0 < before + mine) place(k, before, (int)b, sh.pos[0]);
       // (the axis' own end belongs to the last request)
-      if (x1 > before && x1 <= before + mine) place(k + 1, before, (int)b, s_pos[1]);
+      if (x1 > before && x1 <= before + mine) place(k + 1, before, (int)b, sh.pos[1]);
       base += all;
       if (base >= x1) break;  // uniform
     }
     __syncthreads();
-    from = attn_uniform(s_pos[0]);
-    to = attn_uniform(s_pos[1]);
+    from = attn_uniform(sh.pos[0]);
+    to = attn_uniform(sh.pos[1]);
   }
   return true;
 }
@@ -705,13 +719,13 @@ __device__ __forceinline__ void attn_clear(const AttnParams& p, int64_t b, int r
 }
 
 // 64 lanes' 16-byte pieces from global memory straight into 1 KiB of LDS at
-// `to`, lane by lane. The compiler does not know of the load: the step that
-// reads the tile waits for it.
+// `to` (whole KiB below 64 KiB: m0 has 16 bits for it), lane by lane. The
+// compiler does not know of the load: the step that reads the tile waits for it.
 __device__ __forceinline__ void attn_to_lds(const char* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(to), "v"(from)
-               : "memory");
+               : "memory", "m0");
 }
 
 // Steps [t0, t1) of unit u of request b, into the output or workspace slot
@@ -752,7 +766,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   typedef __attribute__((address_space(3))) unsigned char lds_byte;
   const uint32_t tiles_at = (uint32_t)__builtin_amdgcn_readfirstlane(
       (int)((uint32_t)(uintptr_t)(lds_byte*)lds + g * C::NBUF * 2 * C::TILE + wq * kWave * 16));
-  // With two buffers (in the 64 KiB that m0 reaches) a tile goes straight into
+  // With two buffers (in the first 64 KiB) a tile goes straight into
   // LDS, its chunks' order made by the lanes' addresses; otherwise it waits in
   // registers.
   constexpr bool DIRECT = C::NBUF == 2 && C::LDS <= 65536;
@@ -944,14 +958,14 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
 template <typename H, int DH, int NQ, int QW>
 __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(AttnParams p) {
   using C = AttnTile<DH, NQ, QW>;
-  __shared__ __align__(256) unsigned char lds[C::LDS];
-  __shared__ int s_any[kAtWaves];
+  __shared__ AttnLds<C> sh;
+  static_assert(offsetof(AttnLds<C>, tiles) == 0, "the tiles at LDS address 0");
   AttnPos at, to;
   const int id = (int)blockIdx.x;
   AttnPlace mark{};
   AttnCut cut;
   int k = id;
-  if (attn_plan<C>(p, id, k, cut, at, to)) {
+  if (attn_plan<C>(p, sh.plan, id, k, cut, at, to)) {
     const bool whole = to.x < 0;
     AttnReq rq = attn_request<C>(p, at.b);
     do {  // uniform; no stretch is empty but for ends moved onto one another
@@ -976,7 +990,7 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
         }
         mark = AttnPlace{(int)(e - k), at.b, at.u, rq.rows, rq.waves, rq.tiles, {0, 0}};
       }
-      attn_piece<H, C>(p, lds, s_any, at.b, at.u, rq, at.s, t1,
+      attn_piece<H, C>(p, sh.tiles, sh.any, at.b, at.u, rq, at.s, t1,
                        begins && ends ? -1 : 2 * k + (begins ? 1 : 0));
       if (ends && (at.u + 1) % rq.tiles == 0 && rq.rows < p.T)
         attn_clear<H, DH>(p, at.b, rq.rows, at.u / rq.tiles);

@@ -1039,7 +1039,7 @@ int ddtree_attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t
   if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out |
        (uintptr_t)workspace) & 15)
     return DDT_EINVAL;
-  if (!(scale > 0.0f && scale < INFINITY)) return DDT_EINVAL;
+  if (!(scale > 0.0f && scale * ddt::kLog2e < INFINITY)) return DDT_EINVAL;
   ddt::AttnParams ap;
   const int chk2 = paged_rows(page_table, table_width, batch, pages, page_size, ap.rows);
   if (chk2 == DDT_EINVAL) return chk2;

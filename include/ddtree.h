@@ -312,7 +312,8 @@ int ddtree_append_kv(const void* q, const void* k, const void* v, int dtype, int
  * dtype for its product with V (DDT_F16: to 11 bits where it is at least 2^-28
  * of the row's largest, to a multiple of 2^-38 of that below).
  * Supported: head_dim 64, 128 or 256, q_heads a multiple of kv_heads
- * (DDT_EINVAL otherwise), T <= DDT_MAX_B + 1, 0 < scale < inf (DDT_EINVAL),
+ * (DDT_EINVAL otherwise), T <= DDT_MAX_B + 1, scale > 0 with scale * log2(e)
+ * finite in float32 (DDT_EINVAL),
  * at most 2^27 cache rows per request (table_width * page_size), pages of a
  * layer below 4 GiB.
  * The workspace (ddtree_attention_workspace_size bytes, no zero-fill needed;

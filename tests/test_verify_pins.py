@@ -250,6 +250,15 @@ def test_attention_refusals(L):
     assert call(batch=0) == 0
 
 
+def test_attention_refuses_scales_beyond_float32_in_powers_of_two(L):
+    """Scores are counted in powers of two: scale * log2(e) has to be finite."""
+    def call(scale):  # -3, a workspace too small, where the scale is taken
+        return L.ddtree_attention(FAKE, 0, 2, 9, 8, 2, 128, FAKE, FAKE, FAKE, 4, 16, 16, FAKE, None, None, scale,
+                                  FAKE, None, FAKE, 0, None)
+    assert call(3.4e38) == call(2.4e38) == -1
+    assert call(2.3e38) == call(1e-45) == -3
+
+
 def test_paged_compaction_refusals(L):
     def call(k=FAKE, layers=2, pages=16, heads=4, ps=16, row=256, table=FAKE, width=4, batch=3, past=FAKE, depth=15):
         return L.ddtree_compact_kv_paged(k, FAKE, layers, pages, heads, ps, row, table, width, batch, past, FAKE,

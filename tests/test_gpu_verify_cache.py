@@ -293,6 +293,82 @@ def test_attention_with_garbage_where_nothing_is_seen():
             assert torch.equal(o[0, rest], got["out"][0, rest]) and torch.equal(o[1:], got["out"][1:])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("T,G", TILES, ids=[f"{t * g}rows" for t, g in TILES])
+def test_every_arrangement_over_short_and_long_caches(T, G, dh, dtype):
+    """Each arrangement of waves in each type and head size: trees and chains, a cache that ends in
+    its first tile beside one that is cut over many workgroups and merged."""
+    rng = np.random.default_rng(T * dh + 1)
+    past, ps = np.array([5, 4200, 0], np.int32), 16
+    table, pool = paging(rng, 3, past + T, ps)
+    q = rounded(rng, (3, T, 2 * G, dh), dtype, 2.0)
+    kc, vc = rounded(rng, (pool, 2, ps, dh), dtype), rounded(rng, (pool, 2, ps, dh), dtype)
+    nn = np.array([T - 1, T // 2, T - 1], np.int32)
+    mask = OR.mask(trees(rng, 3, T - 1)[0], nn, T - 1).view(np.int64) if T > 1 else None
+    check_attention(q, kc, vc, past, table, nn, mask)
+    check_attention(q, kc, vc, past, table, None, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("T,G", [(5, 2), (9, 3), (12, 4), (40, 3)], ids=["10rows", "27rows", "48rows", "120rows"])
+def test_garbage_in_every_arrangement(T, G, dh, dtype):
+    """As above for each arrangement of waves: NaN and infinities behind the block, on an unmapped
+    page, on others' pages and in a sibling's row reach only the rows that see them."""
+    rng = np.random.default_rng(T * dh + 2)
+    ps = 16
+    past = np.array([61, 130], np.int32)
+    nn = np.array([T - 1, T // 2], np.int32)
+    mask = OR.mask(np.zeros((2, T - 1), np.int32), nn, T - 1).view(np.int64)  # all nodes are siblings
+    table, pool = paging(rng, 2, past + T, ps)
+    table[1, 2] = -1  # rows 32..47 of request 1 are on no page
+    q = rounded(rng, (2, T, 2 * G, dh), dtype)
+    kc, vc = rounded(rng, (pool, 2, ps, dh), dtype), rounded(rng, (pool, 2, ps, dh), dtype)
+    used = np.zeros((pool, ps), bool)
+    for b in range(2):
+        for r in range(int(past[b]) + int(nn[b]) + 1):
+            at = O.slot(table, pool, ps, b, r)
+            if at is not None:
+                used[at] = True
+    kg, vg = kc.clone(), vc.clone()
+    junk = torch.from_numpy(~used)
+    kg.permute(0, 2, 1, 3)[junk] = float("nan")
+    vg.permute(0, 2, 1, 3)[junk] = torch.from_numpy(rng.choice([np.nan, np.inf, -np.inf, 1.0], (int(junk.sum()), 2, dh))).to(dtype)
+    got = check_attention(q, kg, vg, past, table, nn, mask, clean=(kc, vc))
+    page, row = O.slot(table, pool, ps, 0, 61 + 4)  # node 4 of request 0
+    rest = [i for i in range(T) if i != 4]
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        vb, kb = vg.clone(), kg.clone()
+        vb[page, :, row, 3] = bad  # one element of a head
+        kb[page, :, row] = bad
+        for k2, v2 in ((kg, vb), (kb, vg)):
+            o = pkg.ddtree_attention(q.to(DEV), k2.to(DEV), v2.to(DEV), dev(past), page_table=dev(table),
+                                     num_nodes=dev(nn), mask=dev(mask))["out"]
+            assert torch.equal(o[0, rest], got["out"][0, rest]) and torch.equal(o[1], got["out"][1])
+            if v2 is vb:
+                own, was = o[0, 4].float(), got["out"][0, 4]
+                assert torch.equal(own[:, 3].isnan(), torch.full_like(own[:, 3], bad, device=DEV).isnan())
+                assert not own[:, 3].isfinite().any() and (own[:, 3] != -bad).all()
+                keep = [e for e in range(dh) if e != 3]
+                assert torch.equal(o[0, 4][:, keep], was[:, keep])
+
+
+def test_attention_of_a_round_of_the_operators():
+    """The attention in a verification round, on the tree, mask and caches that the operators before
+    it left on the device."""
+    from test_gpu_sampled import make_round
+    r = make_round(7)
+    Hq, Hkv, dh = r["dims"]
+    t = pkg.ddtree_build(r["draft"], r["B"])
+    for layer, qkv in enumerate(r["qkv"]):
+        q, k, v = qkv.split([Hq, Hkv, Hkv], 2)
+        q = pkg.ddtree_append_kv(q, k, v, r["k"][layer], r["v"][layer], r["past"], rope=r["rope"],
+                                 page_table=r["table"], depths=t["depths"], num_nodes=t["num_nodes"])
+        check_attention(q.cpu(), r["k"][layer].cpu(), r["v"][layer].cpu(), r["past"].cpu().numpy(),
+                        r["table"].cpu().numpy(), t["num_nodes"].cpu().numpy(), t["mask"].cpu().numpy())
+
+
 def test_attention_of_a_padded_batch_and_node_counts():
     """Requests taken out, node counts outside the range, and no counts at all."""
     rng = np.random.default_rng(10)

@@ -613,7 +613,8 @@ def ddtree_append_kv(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     """Verified block into one layer's cache: q [batch, T, q_heads, dh] (or None), k / v
     [batch, T, kv_heads, dh] (bf16/f16; slices of a fused projection are read in place), caches
     [pages, kv_heads, page_size, dh], rope [positions, rope_dim] float32 (cosines, then sines),
-    depths [batch, T-1]; writes the caches and returns the rotated queries q_out (None for q None)."""
+    depths [batch, T-1]; writes the caches and returns the rotated queries q_out (None for q None).
+    Without q_out a new one is made and cleared first, a launch of its own."""
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be [batch, T, kv_heads, head_dim]")
     dt = k.dtype

@@ -611,9 +611,10 @@ SvPlan accept_plan(int64_t batch, int32_t T, int32_t L, int64_t V, int dtype, bo
   // 70 / 70, 16 (19 MB) 121 / 80; L = 5, 4 requests (13 MB) 48 / 44, 8 (25 MB)
   // 62 / 47; chains of 16 guesses, 16 requests (9 MB) 75 / 82, 32 (18 MB)
   // 137 / 110. Depths with a launch of their own, 64 requests at L = 15, at 3 /
-  // 5 / 6 / 8 / 15: trees where 3 walks in 4 go on 155 / 128 / 126 / 134 / 159,
-  // where all do (5 / 6 / 8 / 15) 178 / 171 / 166 / 181, chains 157 / 154 / 157 /
-  // 163 / 191.
+  // 5 / 6 / 8 / 15: trees whose nodes' children hold 3/4 of the weight (walks of
+  // 1.6 nodes) 155 / 128 / 126 / 134 / 159, all of it (3.6 nodes; 5 / 6 / 8 / 15)
+  // 178 / 171 / 166 / 181, chains 157 / 154 / 157 / 163 / 191. (Walks that all take
+  // every level cost 335 to 354 at 6: the rule is for walks that end.)
   const bool many = rows * V * (int64_t)elem_size(dtype) > (L + 1) * ((int64_t)10 << 20);
   pl.depths = !many ? 0 : (L <= 2 ? L : (L + 2) / 3 + 1);
   // a workgroup per row and chunk, or some 8192 (64 requests after 3 depths, at

@@ -15,7 +15,7 @@
 // for all its heads; a thread takes eight pairs (two 16-byte vectors and 64
 // bytes of angles, which stay in L1 for the row's other heads) or one
 // 16-byte vector to copy. 64 blocks of 129 rows (32 query and 8 key/value heads
-// of 128, bf16): 27 us, 153 MB at 5.6 TB/s (a large copy: 4.7). One token: 2.7 us, the launch.
+// of 128, bf16): 28 us, 153 MB at 5.5 TB/s (a large copy: 4.7). One token: 2.6 us, the launch.
 #pragma once
 
 #include "paged.hpp"

@@ -29,7 +29,7 @@
 //
 // The next tile's rows are in flight while the present one is worked on:
 // straight into a second LDS buffer where there is one (64 trees of the sizes
-// below 291 -> 280 us against registers on the way; 32 blocks of 32 rows, heads
+// below 291 -> 280 us, on one box, against registers on the way; 32 blocks of 32 rows, heads
 // of 256, 357 -> 330), else into registers. Work is cut evenly: all steps of
 // all units (a unit: one request's, key/value head's and query tile's pass over
 // the cache) lie on one axis, and each of the workgroups that the card holds at
@@ -37,17 +37,19 @@
 // (attn_plan). A unit cut by a stretch's end leaves partial results in the
 // workspace for attn_merge_kernel.
 //
-// Measured per call (bf16, 32 query and 8 key/value heads of 128, unless said
-// otherwise). 64 single tokens over 4 to 8 k rows: 305 us, 1.61 GB at 5.3 TB/s,
-// bound by HBM reads. 64 trees of 129 rows over 1 to 2 k: 280 us, 166 GFLOP at
-// 0.59 PFLOP/s; two waves on each SIMD (the accumulators, the queries and the
-// scores fill the registers) leave the matrix units busy 27%, the vector units
-// 37% and the LDS 33% of the time (counted with registers on the way), and
-// wait the rest; tiles of 32 rows with three workgroups to a CU spill (499 us),
-// workgroups of eight waves take 335. 3 chains of 17 rows over 50 to 100 k (f16,
-// heads of 64, 40 and 8): 113 to 124 us, 461 MB at 4 TB/s. One tree of 65 rows
-// over 1 k: 21 us, of which the merge is 4 and the steps are 6: a chain of
-// waits.
+// Measured per call, by box and day (bf16, 32 query and 8 key/value heads of
+// 128, unless said otherwise). 64 single tokens over 4 to 8 k rows: 304 to 314
+// us, 1.61 GB at 5.1 to 5.3 TB/s, bound by HBM reads. 64 trees of 129 rows over
+// 1 to 2 k: 275 to 289 us (f16 290 to 302), 166 GFLOP at 0.57 to 0.60 PFLOP/s;
+// two waves on each SIMD (the accumulators, the queries and the scores fill
+// the registers) leave the matrix units busy 26%, the vector units 35% and the
+// LDS 24% of the time, and wait 38% of theirs; tiles of 32 rows with three
+// workgroups to a CU spill (499 us), workgroups of eight waves take 335. 3
+// chains of 17 rows over 50 to 100 k (f16, heads of 64, 40 and 8): 115 to 122 us,
+// 461 MB at 3.8 to 4 TB/s. One tree of 65 rows over 1 k: 20 to 21 us, of which
+// the merge is 4 and the steps are 6: a chain of waits. 32 blocks of 32 rows
+// with 16 heads of 256 on 4 over 2 to 4 k: 194 us; 2 pieces of a prompt of 513
+// rows over 4 to 8 k: 180 us.
 #pragma once
 
 #include "paged.hpp"

@@ -29,13 +29,17 @@
 // all rows that the walks still going on may come to by one more (how many
 // depths: accept_plan in api.hip).
 //
-// Measured per call, rows of 152 k bf16: one tree of 64 nodes 24 us (rows 12,
-// finish 16: chains of dependent loads); 64 trees 120 to 126 us: six launches of 8 to
-// 13 us (a full one reads 19 MB, 4 us, and has 4 us of float64 work, both behind
-// 3 us of dependent loads), 40 to 50 us for the rows left, 16 us for the draw.
-// 64 chains of 16 guesses 149 to 165 us: seven launches of 9 to 22 us, 23 for the rows
-// left, 28 for max(0, p - q), 14 for the draw. 8 chains of 5 guesses, 32 k
-// float32: 24 us.
+// Measured per call, by box, rows of 152 k bf16 (parts: medians under the
+// profiler, where launches take longer than in an unprofiled call). One tree of
+// 64 nodes: 24 to 27 us (rows 12, finish 15: chains of dependent loads), 39 where
+// the walk takes all 15 levels. 64 trees whose walks take 1.6 nodes on
+// average (one in eight, greedy, 15): 120 to 128 us, six launches of 8 to 14 us
+// (a full one reads 19 MB, 4 us, and has 4 us of float64 work, both behind 3 us
+// of dependent loads), 47 us for the rows left, 17 us for the draw; where walks
+// take 3.6 nodes 167, where every one takes all 15 levels 335 to 354, most of it
+// for the rows that the last launch finds within reach. 64 chains of 16 guesses:
+// 150 to 165 us, seven launches of 8 to 20 us, 21 for the rows left, 25 for
+// max(0, p - q), 13 for the draw. 8 chains of 5 guesses, 32 k float32: 24 to 25 us.
 #pragma once
 
 #include "common.hpp"
@@ -135,8 +139,7 @@ __device__ __forceinline__ float sv_logit(const void* base, int64_t r0, int64_t 
 }
 
 // 2^y for y <= 0 (anything below -1100, and NaN, gives 0): 2^k times the
-// Taylor polynomial of exp on [-ln2/2, ln2/2], whose first term left out is
-// below 7e-15 of the result.
+// Taylor polynomial of exp on [-ln2/2, ln2/2], within 9e-15 of the result.
 __device__ __forceinline__ double sv_exp2(double y) {
   y = fmax(y, -1100.0);
   const double k = rint(y);
@@ -158,8 +161,8 @@ __device__ __forceinline__ double sv_exp2(double y) {
 
 // The same for the sums: y within [-1000, 0] (what is below counts as 2^-1000),
 // 2^f by the polynomial through its values at the ten Chebyshev nodes of
-// [-1/2, 1/2], its constant 1.0000000000000135 set to 1 (within 3.3e-14 of
-// it), 2^k added to the exponent's bits.
+// [-1/2, 1/2], its constant 1.0000000000000135 set to 1 (within 3.8e-14 of
+// the result), 2^k added to the exponent's bits.
 __device__ __forceinline__ double sv_exp2_fast(double y) {
   y = fmax(y, -1000.0);
   const double big = 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits are k

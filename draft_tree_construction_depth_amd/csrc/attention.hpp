@@ -544,18 +544,21 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     st.mref = m > -INFINITY ? m - Weight::kBias : 0.0f;
   }
   // The weights' exponents score * scale2 - maximum are formed by an FMA, whose
-  // product is not rounded, while the maximum's was. Past 2^20 that difference
-  // (2^-5 there, whole powers of two from 2^25 on) would be the largest score's
-  // weight, so those products are rounded first, as the maximum's.
-  const bool far = __ballot(fabsf(st.mref) > 0x1p20f) != 0;
-  if (far) {
+  // product is not rounded, while the maximum's was: a factor that all weights
+  // share, below 2^0.5 up to a maximum of 2^24. Beyond, where it (and the
+  // rounding of maximum less kBias) could take them out of range, the products
+  // are rounded first, as the maximum's was, and kBias comes last.
+  float factor = scale2, ref = st.mref;
+  if (__ballot(fabsf(st.mref) > 0x1p24f - 16.0f) != 0) {
 #pragma clang fp contract(off)
+    const float m = st.m > -INFINITY ? st.m : 0.0f;
 #pragma unroll
     for (int t = 0; t < NB; ++t)
 #pragma unroll
-      for (int r = 0; r < R; ++r) s[t][r] *= scale2;
+      for (int r = 0; r < R; ++r) s[t][r] = s[t][r] * scale2 - m;
+    factor = 1.0f;
+    ref = -Weight::kBias;
   }
-  const float factor = far ? 1.0f : scale2;
   // Rows that a query does not see have weight 0, but 0 times a NaN or an
   // infinity among their values is no 0: such values (garbage behind the
   // block, on unmapped pages, or in other nodes' rows) are taken out of the
@@ -577,7 +580,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
   };
   float sum[2] = {0.0f, 0.0f};
   auto weigh = [&](int u, int i) {
-    const float w = __builtin_amdgcn_exp2f(fmaf(score(u, i), factor, -st.mref));
+    const float w = __builtin_amdgcn_exp2f(fmaf(score(u, i), factor, -ref));
     if (NQ == 32)
       s[u >> 1][(8 * (u & 1) + i) % R] = w;
     else

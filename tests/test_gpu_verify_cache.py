@@ -252,6 +252,46 @@ def test_attention_of_scores_beyond_what_float32_steps_resolve(T, G, dtype):
     assert ((got["lse"].double() - lse).abs() <= 2.0 ** -21 * lse).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("size", [2.0 ** 21, 2.0 ** 23, 2.0 ** 25], ids=["2p21", "2p23", "2p25"])
+@pytest.mark.parametrize("T,G", TILES, ids=[f"{t * g}rows" for t, g in TILES])
+def test_attention_of_small_differences_between_large_scores(T, G, size, dtype):
+    """Scores that share a large part and differ by a few: float32 holds each of them exactly, so up
+    to 2^24 powers of two the differences come through; beyond, to a float32 step of the score."""
+    rng = np.random.default_rng(T)
+    dh, n, past = 64, 200 + T, np.array([200], np.int32)
+    q, kc = torch.zeros((1, T, 2 * G, dh), dtype=dtype), torch.zeros((1, 2, n, dh), dtype=dtype)
+    q[..., 0], q[..., 1] = size / 2.0 ** 11, 1.0
+    kc[..., 0] = 2.0 ** 11
+    step = max(size / 2.0 ** 23, 0.5)  # float32's at the size (half of it below), which the sum keeps
+    kc[..., 1] = torch.from_numpy(rng.integers(-12, 13, (1, 2, n)) * step).to(dtype)
+    vc = rounded(rng, (1, 2, n, dh), dtype)
+    got = pkg.ddtree_attention(q.to(DEV), kc.to(DEV), vc.to(DEV), dev(past), scale=1.0, with_lse=True)
+    out, lse, spread, _ = O.attend(f64(q), f64(kc), f64(vc), past, None, None, None, 1.0)
+    half = torch.finfo(dtype).eps / 2
+    # a weight's exponent is off by 2^-23 of at most 20 powers of two, or by a step of the score
+    off = 2.0 ** -18 if 1.4427 * size + 32 < 2.0 ** 24 else np.expm1(np.spacing(np.float32(1.45 * size)) * np.log(2))
+    tol = half * np.abs(out) + spread * (1 + half) * (half + 2 * off + 2.0 ** -14)
+    assert np.all(np.abs(f64(got["out"]) - out) <= tol + 2.0 ** -25)
+    assert np.all(np.abs(f64(got["lse"]) - lse) <= 2.0 ** -21 * np.abs(lse))
+
+
+@pytest.mark.parametrize("T,G", TILES, ids=[f"{t * g}rows" for t, g in TILES])
+def test_attention_of_one_query_with_large_scores_among_others(T, G):
+    """Large scores of one query change nothing for those beside it, nor for rows that see nothing."""
+    rng = np.random.default_rng(T + 5)
+    dh, past = 64, np.array([0, 90], np.int32)
+    q = rounded(rng, (2, T, 2 * G, dh), BF)
+    kc, vc = rounded(rng, (2, 2, 100 + T, dh), BF), rounded(rng, (2, 2, 100 + T, dh), BF)
+    q[:, 0, 1] *= 2.0 ** 40
+    mask = None
+    if T > 1:
+        mask = OR.mask(np.zeros((2, T - 1), np.int32), np.full(2, T - 1, np.int32), T - 1).view(np.int64)
+        mask[0, -1] = 0  # sees nothing: no past, no bit
+    got = check_attention(q, kc, vc, past, None, None, mask)
+    assert got["out"].isfinite().all()
+
+
 def test_attention_with_garbage_where_nothing_is_seen():
     """NaN and infinities in rows behind the block, on unmapped pages, in pages of
     others, and in a sibling's row do not reach the rows that do not see them."""

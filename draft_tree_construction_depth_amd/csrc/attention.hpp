@@ -40,7 +40,7 @@
 // Measured per call, by box and day (bf16, 32 query and 8 key/value heads of
 // 128, unless said otherwise). 64 single tokens over 4 to 8 k rows: 304 to 314
 // us, 1.61 GB at 5.1 to 5.3 TB/s, bound by HBM reads. 64 trees of 129 rows over
-// 1 to 2 k: 275 to 289 us (f16 290 to 302), 166 GFLOP at 0.57 to 0.60 PFLOP/s;
+// 1 to 2 k: 272 to 294 us (f16 286 to 302), 166 GFLOP at 0.56 to 0.61 PFLOP/s;
 // two waves on each SIMD (the accumulators, the queries and the scores fill
 // the registers) leave the matrix units busy 26%, the vector units 35% and the
 // LDS 24% of the time, and wait 38% of theirs; tiles of 32 rows with three

@@ -38,7 +38,7 @@
 // of dependent loads), 47 us for the rows left, 17 us for the draw; where walks
 // take 3.6 nodes 167, where every one takes all 15 levels 335 to 354, most of it
 // for the rows that the last launch finds within reach. 64 chains of 16 guesses:
-// 150 to 165 us, seven launches of 8 to 20 us, 21 for the rows left, 25 for
+// 149 to 167 us, seven launches of 8 to 20 us, 21 for the rows left, 25 for
 // max(0, p - q), 13 for the draw. 8 chains of 5 guesses, 32 k float32: 24 to 25 us.
 #pragma once
 

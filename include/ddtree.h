@@ -310,7 +310,9 @@ int ddtree_append_kv(const void* q, const void* k, const void* v, int dtype, int
  *        may be NULL.
  * Scores, maxima, sums and accumulators are float32; a weight is rounded to
  * dtype for its product with V (DDT_F16: to 11 bits where it is at least 2^-28
- * of the row's largest, to a multiple of 2^-38 of that below).
+ * of the row's largest, to a multiple of 2^-38 of that below). Sums of values
+ * are formed before they are divided by the weights' sum, so DDT_BF16 values
+ * beyond 2^92 can leave float32's range there.
  * Supported: head_dim 64, 128 or 256, q_heads a multiple of kv_heads
  * (DDT_EINVAL otherwise), T <= DDT_MAX_B + 1, scale > 0 with scale * log2(e)
  * finite in float32 (DDT_EINVAL),

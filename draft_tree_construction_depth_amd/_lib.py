@@ -19,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libddtree.so")
 
 DDT_OK, DDT_EINVAL, DDT_ENOTSUP, DDT_EWORKSPACE, DDT_EHIP = 0, -1, -2, -3, -4
-DDT_BF16, DDT_F32, DDT_F16 = 0, 1, 2
+DDT_BF16, DDT_F32, DDT_F16, DDT_E4M3, DDT_I8 = 0, 1, 2, 3, 4
 
 _lib = None
 
@@ -90,6 +90,26 @@ def lib() -> C.CDLL:
         L.ddtree_compact_kv_paged.restype = C.c_int
         L.ddtree_compact_kv_paged.argtypes = [p, p, i64, i64, i32, i32, i32, p, i64, i64, p, p, p,
                                               i32, p, p]
+        L.ddtree_append_kv8.restype = C.c_int
+        L.ddtree_append_kv8.argtypes = [p, p, p, C.c_int, i64, i32, i32, i32, i32, i64, i64, i64, p,
+                                        i64, i32, i32, p, p, p, p, i64, i64, i32, C.c_int, p, p, p,
+                                        p, p, p]
+        L.ddtree_attention_kv8_workspace_size.restype = sz
+        L.ddtree_attention_kv8_workspace_size.argtypes = [i64, i32, i32, i32, i32, i64, i32, i32]
+        L.ddtree_attention_kv8.restype = C.c_int
+        L.ddtree_attention_kv8.argtypes = [p, C.c_int, i64, i32, i32, i32, i32, C.c_int, p, p, p, p,
+                                           p, i64, i64, i32, p, p, p, p, C.c_float, p, p, p, sz, p]
+        L.ddtree_attention_shared_workspace_size.restype = sz
+        L.ddtree_attention_shared_workspace_size.argtypes = [i64, i32, i32, i32, i32, i64, i32]
+        L.ddtree_attention_shared.restype = C.c_int
+        L.ddtree_attention_shared.argtypes = [p, C.c_int, i64, i32, i32, i32, i32, p, p, p, i64, i64,
+                                              i32, p, p, p, p, C.c_float, p, p, p, sz, p]
+        L.ddtree_compact_kv8.restype = C.c_int
+        L.ddtree_compact_kv8.argtypes = [p, p, p, p, i64, i64, i32, i32, i32, p, i64, i64, p, p, p,
+                                         i32, p, p]
+        L.ddtree_read_kv8.restype = C.c_int
+        L.ddtree_read_kv8.argtypes = [C.c_int, p, p, p, p, i32, i32, p, i64, i64, i32, i64, p, p,
+                                      i32, C.c_int, p, p, p]
         L.ddtree_accept_sampled_workspace_size.restype = sz
         L.ddtree_accept_sampled_workspace_size.argtypes = [i64, i32, i32, i64, C.c_int]
         L.ddtree_accept_sampled.restype = C.c_int
@@ -720,6 +740,208 @@ def ddtree_compact_kv_paged(k_cache: torch.Tensor, v_cache: torch.Tensor,
                                            dh * k_cache.element_size(), table, width, batch,
                                            *args))
     return new_len
+
+
+# ---- caches of 8-bit rows, shared rows -----------------------------------------
+_CODES = {torch.float8_e4m3fn: DDT_E4M3, torch.int8: DDT_I8}
+
+
+def _code_cache(k_cache, v_cache, k_scale, v_scale, page_table, batch, dims):
+    """Check a cache of codes [(layers,) pages, kv_heads, page_size, head_dim], its scales (the
+    same without head_dim, float32) and its page table; (k, v, k_scale, v_scale, table, shape,
+    width, device number, code type)."""
+    if isinstance(k_cache, torch.Tensor) and k_cache.dtype not in _CODES:
+        raise TypeError(f"k_cache must have dtype {' or '.join(map(str, _CODES))}, "
+                        f"got {k_cache.dtype}")
+    k, v, table, shape, width, dev = _paged_cache(k_cache, v_cache, page_table, batch, dims)
+    ks = _dev_arg(k_scale, "k_scale", torch.float32, shape[:-1], dev)
+    vs = _dev_arg(v_scale, "v_scale", torch.float32, shape[:-1], dev)
+    return k, v, ks, vs, table, shape, width, dev, _CODES[k_cache.dtype]
+
+
+def ddtree_append_kv8(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                      past_len: torch.Tensor, *, rope: torch.Tensor | None = None,
+                      interleaved: bool = False, page_table: torch.Tensor | None = None,
+                      depths: torch.Tensor | None = None, num_nodes: torch.Tensor | None = None,
+                      q_out: torch.Tensor | None = None):
+    """ddtree_append_kv into a cache of 8-bit rows, quantised on the way: codes [pages, kv_heads,
+    page_size, dh] (float8_e4m3fn or int8), scales [pages, kv_heads, page_size] (float32)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be [batch, T, kv_heads, head_dim]")
+    dt = k.dtype
+    if dt not in _HALF:
+        raise TypeError(f"k must have dtype {' or '.join(map(str, _HALF))}, got {dt}")
+    batch, T, _, dh = k.shape
+    kc, vc, ks, vs, table, shape, width, dev, code = _code_cache(k_cache, v_cache, k_scale, v_scale,
+                                                                 page_table, batch, 4)
+    kp, kv_heads, k_step = _block_rows(k, "k", dt, batch, T, dh, dev)
+    vp, hv, v_step = _block_rows(v, "v", dt, batch, T, dh, dev)
+    pages, hc, page_size, dc = shape
+    if hv != kv_heads or hc != kv_heads or dc != dh:
+        raise ValueError("k, v and the caches must have the same heads and head_dim")
+    qp, q_heads, q_step, qo = None, 0, 0, None
+    if q is None:
+        q_out = None
+    else:
+        qp, q_heads, q_step = _block_rows(q, "q", dt, batch, T, dh, dev)
+        if q_out is None:
+            q_out = torch.zeros((batch, T, q_heads, dh), dtype=dt, device=dev)
+        qo = _dev_arg(q_out, "q_out", dt, (batch, T, q_heads, dh), dev)
+    rp, rope_len, rot = None, 0, 0
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+            raise ValueError("rope must be [positions, rope_dim]")
+        rope_len, rot = rope.shape
+        rp = _dev_arg(rope, "rope", torch.float32, (rope_len, rot), dev)
+    args = (qp, kp, vp, _half_code(dt), batch, T, q_heads, kv_heads, dh, q_step, k_step, v_step, rp,
+            rope_len, rot, 1 if interleaved else 0,
+            _dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+            _maybe_arg(depths, "depths", torch.int32, (batch, T - 1), dev),
+            _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev), table, width, pages,
+            page_size, code, kc, vc, ks, vs, qo)
+    _call("ddtree_append_kv8", dev, args)
+    return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_kv8_ws(*sizes) -> int:
+    return lib().ddtree_attention_kv8_workspace_size(*sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_shared_ws(*sizes) -> int:
+    return lib().ddtree_attention_shared_workspace_size(*sizes)
+
+
+def _attention_out(q, with_lse, out):
+    """The queries' [batch, T, q_heads, dh] and the outputs, made where none are given."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [batch, T, q_heads, head_dim]")
+    if q.dtype not in _HALF:
+        raise TypeError(f"q must have dtype {' or '.join(map(str, _HALF))}, got {q.dtype}")
+    if out is None:
+        out = {"out": torch.empty_like(q)}
+        if with_lse:
+            out["lse"] = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    return q.shape, out
+
+
+def ddtree_attention_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         k_scale: torch.Tensor, v_scale: torch.Tensor, past_len: torch.Tensor, *,
+                         page_table: torch.Tensor | None = None,
+                         num_nodes: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                         shared_len: torch.Tensor | None = None, scale: float | None = None,
+                         with_lse: bool = False, out: dict | None = None,
+                         ws: torch.Tensor | None = None) -> dict:
+    """ddtree_attention over a cache of 8-bit rows (ddtree_append_kv8's). shared_len [1] int32:
+    the rows that all requests' pages share, attended to once (ddtree_attention_shared)."""
+    (batch, T, q_heads, dh), out = _attention_out(q, with_lse, out)
+    kc, vc, ks, vs, table, shape, width, dev, code = _code_cache(k_cache, v_cache, k_scale, v_scale,
+                                                                 page_table, batch, 4)
+    pages, kv_heads, page_size, dc = shape
+    if dc != dh:
+        raise ValueError(f"the caches must have head_dim {dh}, got {dc}")
+    if shared_len is not None and page_table is None:
+        raise ValueError("shared_len needs a page_table")
+    args = (_dev_arg(q, "q", q.dtype, q.shape, dev), _half_code(q.dtype), batch, T, q_heads,
+            kv_heads, dh, code, kc, vc, ks, vs, table, width, pages, page_size,
+            _dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+            _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev),
+            _maybe_arg(mask, "mask", torch.int64, (batch, T, (T + 63) // 64), dev),
+            _maybe_arg(shared_len, "shared_len", torch.int32, (1,), dev),
+            dh ** -0.5 if scale is None else float(scale),
+            _dev_arg(out["out"], "out", q.dtype, q.shape, dev),
+            _maybe_arg(out.get("lse"), "lse", torch.float32, (batch, T, q_heads), dev))
+    size = _attention_kv8_ws(batch, T, q_heads, kv_heads, dh, width, page_size,
+                             int(shared_len is not None))
+    _call("ddtree_attention_kv8", dev, args, "attention", size, ws)
+    return out
+
+
+def ddtree_attention_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            past_len: torch.Tensor, shared_len: torch.Tensor,
+                            page_table: torch.Tensor, *, num_nodes: torch.Tensor | None = None,
+                            mask: torch.Tensor | None = None, scale: float | None = None,
+                            with_lse: bool = False, out: dict | None = None,
+                            ws: torch.Tensor | None = None) -> dict:
+    """ddtree_attention of a batch whose requests share their first shared_len [1] (int32) rows:
+    page_table maps them to the same pages for every request with past_len >= 0, and the
+    attention over them is computed once."""
+    (batch, T, q_heads, dh), out = _attention_out(q, with_lse, out)
+    if page_table is None:
+        raise ValueError("page_table is required: contiguous caches share no rows")
+    kc, vc, table, shape, width, dev = _paged_cache(k_cache, v_cache, page_table, batch, 4)
+    if k_cache.dtype != q.dtype:
+        raise TypeError(f"k_cache must have dtype {q.dtype}, got {k_cache.dtype}")
+    pages, kv_heads, page_size, dc = shape
+    if dc != dh:
+        raise ValueError(f"the caches must have head_dim {dh}, got {dc}")
+    args = (_dev_arg(q, "q", q.dtype, q.shape, dev), _half_code(q.dtype), batch, T, q_heads,
+            kv_heads, dh, kc, vc, table, width, pages, page_size,
+            _dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+            _maybe_arg(num_nodes, "num_nodes", torch.int32, (batch,), dev),
+            _maybe_arg(mask, "mask", torch.int64, (batch, T, (T + 63) // 64), dev),
+            _dev_arg(shared_len, "shared_len", torch.int32, (1,), dev),
+            dh ** -0.5 if scale is None else float(scale),
+            _dev_arg(out["out"], "out", q.dtype, q.shape, dev),
+            _maybe_arg(out.get("lse"), "lse", torch.float32, (batch, T, q_heads), dev))
+    size = _attention_shared_ws(batch, T, q_heads, kv_heads, dh, width, page_size)
+    _call("ddtree_attention_shared", dev, args, "attention", size, ws)
+    return out
+
+
+def ddtree_compact_kv8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                       v_scale: torch.Tensor, page_table, past_len: torch.Tensor,
+                       accepted_nodes: torch.Tensor, accept_len: torch.Tensor,
+                       new_len: torch.Tensor | None = None) -> torch.Tensor:
+    """In place: caches of 8-bit rows [layers, pages, heads, page_size, head_dim] and their scales
+    keep the accepted path's rows (page_table None: contiguous caches, pages = batch); returns
+    new_len [batch]."""
+    if not isinstance(past_len, torch.Tensor) or past_len.dim() != 1:
+        raise ValueError("past_len must be [batch]")
+    batch = past_len.shape[0]
+    kc, vc, ks, vs, table, shape, width, dev, _ = _code_cache(k_cache, v_cache, k_scale, v_scale,
+                                                              page_table, batch, 5)
+    layers, pages, heads, page_size, dh = shape
+    L = _rows_arg(accepted_nodes, "accepted_nodes", batch)
+    if new_len is None:
+        new_len = torch.empty((batch,), dtype=torch.int32, device=dev)
+    args = (kc, vc, ks, vs, layers, pages, heads, page_size, dh, table, width, batch,
+            _dev_arg(past_len, "past_len", torch.int32, (batch,), dev),
+            _dev_arg(accepted_nodes, "accepted_nodes", torch.int32, (batch, L), dev),
+            _dev_arg(accept_len, "accept_len", torch.int32, (batch,), dev), L,
+            _dev_arg(new_len, "new_len", torch.int32, (batch,), dev))
+    _call("ddtree_compact_kv8", dev, args)
+    return new_len
+
+
+def ddtree_read_kv8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                    v_scale: torch.Tensor, first: torch.Tensor, count, n: int, *,
+                    dtype: torch.dtype = torch.bfloat16, page_table: torch.Tensor | None = None,
+                    out: dict | None = None) -> dict:
+    """Rows first[b] .. first[b] + min(count[b], n) - 1 of each request of a cache of 8-bit rows,
+    read back: k and v [batch, n, kv_heads, dh] of dtype (bf16, f16 or f32), 0 behind them (count
+    None: n rows of every request)."""
+    if not isinstance(first, torch.Tensor) or first.dim() != 1:
+        raise ValueError("first must be [batch]")
+    batch = first.shape[0]
+    if dtype not in _HALF and dtype != torch.float32:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    kc, vc, ks, vs, table, shape, width, dev, code = _code_cache(k_cache, v_cache, k_scale, v_scale,
+                                                                 page_table, batch, 4)
+    pages, kv_heads, page_size, dh = shape
+    to = (batch, n, kv_heads, dh)
+    if out is None:
+        out = {x: torch.empty(to, dtype=dtype, device=dev) for x in "kv"}
+    args = (code, kc, vc, ks, vs, kv_heads, dh, table, width, pages, page_size, batch,
+            _dev_arg(first, "first", torch.int32, (batch,), dev),
+            _maybe_arg(count, "count", torch.int32, (batch,), dev), n,
+            DDT_F32 if dtype == torch.float32 else _half_code(dtype),
+            _dev_arg(out["k"], "out['k']", dtype, to, dev),
+            _dev_arg(out["v"], "out['v']", dtype, to, dev))
+    _call("ddtree_read_kv8", dev, args)
+    return out
 
 
 @functools.lru_cache(maxsize=1024)

@@ -13,7 +13,7 @@
 #include "walk.hpp"
 #include "kv.hpp"
 #include "append.hpp"
-#include "attention.hpp"
+#include "verify.hpp"
 #include "sampled.hpp"
 #include "sparkling.hpp"
 #include "dspark.hpp"
@@ -22,8 +22,15 @@
 
 namespace {
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+using ddt::align_up;
+using ddt::attn_check;
+using ddt::attn_plan_host;
+using ddt::AttnPlan;
+using ddt::kAlign;
+using ddt::launch_attn;
+using ddt::launchable;
+using ddt::paged_rows;
+using ddt::valid_half;
 
 int elems_per_vec(int dtype) { return dtype == DDT_BF16 ? 8 : 4; }
 size_t elem_size(int dtype) { return dtype == DDT_BF16 ? 2 : 4; }
@@ -444,34 +451,6 @@ int build_launch(const void* logits, int dtype, int64_t batch, int32_t L, int64_
                        num_nodes, mask, stream);
 }
 
-// ---- paged caches -------------------------------------------------------------
-// A layer's cache of `pages` pages and the table that maps `batch` requests'
-// rows onto it (null: page b is request b's). Page sizes behind a table are
-// powers of two, so that no row needs a division.
-int paged_rows(const int32_t* table, int64_t width, int64_t batch, int64_t pages,
-               int64_t page_size, ddt::PagedRows& r) {
-  if (pages <= 0 || page_size <= 0 || (table && width <= 0)) return DDT_EINVAL;
-  if (!table && pages != batch) return DDT_EINVAL;
-  if (pages > 0x7FFFFFFFLL || page_size > 0x7FFFFFFFLL || width > 0x7FFFFFFFLL) return DDT_ENOTSUP;
-  if (table && (page_size & (page_size - 1))) return DDT_ENOTSUP;
-  r.table = table;
-  r.width = table ? width : 1;
-  r.pages = pages;
-  r.page_size = (int32_t)page_size;
-  r.shift = 31;
-  if (table)
-    for (r.shift = 0; ((int64_t)1 << r.shift) < page_size; ++r.shift) {
-    }
-  r.cap = r.width * page_size;
-  if (r.cap > 0x7FFFFFFFLL) r.cap = 0x7FFFFFFFLL;  // lengths are 32-bit
-  return DDT_OK;
-}
-
-// Whether one launch takes `blocks` workgroups: it has fewer than 2^32 threads.
-bool launchable(int64_t blocks, int threads) { return blocks <= 0xFFFFFFFFLL / threads; }
-
-bool valid_half(int dtype) { return dtype == DDT_BF16 || dtype == DDT_F16; }
-
 template <typename H>
 void launch_append(const ddt::AppendParams& ap, int64_t blocks, int interleaved, hipStream_t st) {
   if (interleaved)
@@ -480,100 +459,6 @@ void launch_append(const ddt::AppendParams& ap, int64_t blocks, int interleaved,
   else
     hipLaunchKernelGGL((ddt::append_kernel<H, false>), dim3((unsigned)blocks),
                        dim3(ddt::kApThreads), 0, st, ap);
-}
-
-// ---- attention: waves along the queries, workgroups, workspace -------------------
-struct AttnPlan {
-  int NQ, QW;  // queries of a wave, waves side by side
-  int64_t groups, least, grid;
-  bool merge;  // a unit can be cut
-  size_t part, ml, end;
-};
-
-AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
-                        int32_t head_dim, int64_t cap) {
-  AttnPlan pl;
-  const int G = q_heads / kv_heads;
-  // M query rows share a key/value head's pass. Up to 64: 16 to a wave, as many
-  // waves side by side as they fill; more: 32 to a wave (at head_dim 256 always
-  // 16, and two waves or more: 32 queries' state or four groups' tiles would
-  // not leave registers for the next tile). 32 requests x 4 heads over 4096
-  // rows, us at 16x1 / 16x2 / 16x4 / 32x4 queries x waves:
-  //   head_dim 128  M = 16: 62 / 64 / 71 / 77   32: 65 / 63 / 67 / 75
-  //                 64: 87 / 74 / 69 / 77       256: 239 / 165 / 117 / 104
-  //   head_dim 64   M = 16: 36 / 37 / 39 / 42   64: 53 / 46 / 41 / 44
-  //                 128: 83 / 67 / 50 / 53      256: 129 / 85 / 77 / 66
-  //   head_dim 256  M = 16: - / 114 / 125 / 276 128: - / 289 / 180 / 323
-  // (the last column of 256 with tiles that went through registers)
-  const int64_t M = (int64_t)T * G;
-  pl.NQ = M <= 64 || head_dim == 256 ? 16 : 32;
-  pl.QW = M <= 16 && head_dim < 256 ? 1 : (M <= 32 ? 2 : 4);
-  const int rows = pl.QW == 4 ? (head_dim <= 128 ? 64 : 32) : 32 * (4 / pl.QW);  // AttnTile::TR
-  const int64_t steps = (cap + rows - 1) / rows;
-  const int64_t tiles = (M + pl.NQ * pl.QW - 1) / (pl.NQ * pl.QW);
-  pl.least = 2;
-  // two workgroups on each of 256 CUs (one where a tile fills the LDS or the
-  // registers), fewer for little work
-  pl.groups = head_dim == 256 ? 256 : 512;
-  const int64_t axis = steps > ((int64_t)1 << 31) / (kv_heads * tiles) / batch
-                           ? (int64_t)1 << 31
-                           : batch * kv_heads * tiles * steps;
-  const int64_t want = ((axis + pl.least - 1) / pl.least + 7) & ~(int64_t)7;
-  if (want < pl.groups) pl.groups = want;
-  // or one for each unit, where there are many (attn_plan decides)
-  const int64_t units = (batch * kv_heads * tiles + 7) & ~(int64_t)7;
-  pl.grid = units >= 2 * pl.groups ? units : pl.groups;
-  pl.merge = steps > 1;
-  const int64_t slots = pl.merge ? 2 * pl.groups : 0;
-  size_t o = align_up((size_t)pl.groups * sizeof(ddt::AttnPlace));
-  pl.part = o;
-  o = align_up(o + (size_t)slots * pl.QW * pl.NQ * head_dim * sizeof(float));
-  pl.ml = o;
-  o = align_up(o + (size_t)slots * pl.QW * 64 * 2 * sizeof(float));
-  pl.end = o;
-  return pl;
-}
-
-template <typename H, int DH, int NQ, int QW>
-int launch_attn_tile(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
-  hipLaunchKernelGGL((ddt::attn_kernel<H, DH, NQ, QW>), dim3((unsigned)pl.grid),
-                     dim3(ddt::kAtThreads), 0, st, ap);
-  if (hipGetLastError() != hipSuccess) return DDT_EHIP;
-  if (!pl.merge) return DDT_OK;
-  hipLaunchKernelGGL((ddt::attn_merge_kernel<H, DH, NQ, QW>), dim3((unsigned)(pl.groups * QW * ddt::AttnTile<DH, NQ, QW>::PIECES / ddt::kAtMerge)),
-                     dim3(ddt::kWave), 0, st, ap);
-  return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
-}
-
-template <typename H, int DH>
-int launch_attn_waves(const ddt::AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
-  if constexpr (DH < 256) {
-    if (pl.NQ == 32) return launch_attn_tile<H, DH, 32, 4>(ap, pl, st);
-    if (pl.QW == 1) return launch_attn_tile<H, DH, 16, 1>(ap, pl, st);
-  }
-  if (pl.QW == 4) return launch_attn_tile<H, DH, 16, 4>(ap, pl, st);
-  return launch_attn_tile<H, DH, 16, 2>(ap, pl, st);
-}
-
-template <typename H>
-int launch_attn(const ddt::AttnParams& ap, const AttnPlan& pl, int head_dim, hipStream_t st) {
-  switch (head_dim) {
-    case 64: return launch_attn_waves<H, 64>(ap, pl, st);
-    case 128: return launch_attn_waves<H, 128>(ap, pl, st);
-    default: return launch_attn_waves<H, 256>(ap, pl, st);
-  }
-}
-
-int attn_check(int dtype, int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
-               int32_t head_dim) {
-  if (!valid_half(dtype) || batch < 0 || T <= 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0)
-    return DDT_EINVAL;
-  if (q_heads % kv_heads != 0) return DDT_EINVAL;
-  if (T > DDT_MAX_B + 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
-    return DDT_ENOTSUP;
-  // keeps the plan's counts far below 63 bits; the launch itself is tested with the plan
-  if (batch > 0x1FFFFFFFLL || batch * T > 0x1FFFFFFFLL / q_heads) return DDT_ENOTSUP;
-  return DDT_OK;
 }
 
 // ---- acceptance at a temperature: schedule and workspace ------------------------

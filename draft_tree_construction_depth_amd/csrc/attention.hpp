@@ -78,18 +78,24 @@ typedef short at_s16x4 __attribute__((ext_vector_type(4)));
 typedef float at_f32x4 __attribute__((ext_vector_type(4)));
 typedef float at_f32x16 __attribute__((ext_vector_type(16)));
 
-template <int DH_, int NQ_, int QW_>
+// What a cache holds: elements of the queries' type, or 8-bit codes and a
+// float32 scale for each row of a head.
+enum { kAtSame, kAtE4M3, kAtI8 };
+
+template <int DH_, int NQ_, int QW_, int CACHE_ = kAtSame>
 struct AttnTile {
-  static constexpr int DH = DH_, NQ = NQ_, QW = QW_;
+  static constexpr int DH = DH_, NQ = NQ_, QW = QW_, CACHE = CACHE_;
   static constexpr int NG = kAtWaves / QW;                 // groups over cache rows
   static constexpr int KT = QW == 4 && DH <= 128 ? 64 : 32;  // rows of a group's tile
   static constexpr int TR = NG * KT;                       // rows of a workgroup's step
-  static constexpr int ROW = DH * 2;                       // bytes of a row
-  static constexpr int CPR = DH / 8;                       // 16-byte chunks of a row
+  static constexpr int ROW = DH * 2;                       // bytes of a row in LDS
+  static constexpr int CROW = CACHE == kAtSame ? ROW : DH;  // ... in the cache
+  static constexpr int CPR = CROW / 16;                    // 16-byte chunks of a row there
   static constexpr int LOADS = KT * CPR / (QW * kWave);    // chunks per thread, K and V each
   static constexpr int NBUF = QW == 1 ? 1 : 2;             // one wave needs no second buffer
   static constexpr int TILE = KT * ROW;                    // bytes of K (or V) of a tile
   static constexpr int LDS = NG * NBUF * 2 * TILE;
+  static constexpr int SCALES = CACHE == kAtSame ? 0 : NG * NBUF * 2 * KT;  // floats in LDS
   static constexpr int PIECES = DH * NQ / (4 * kWave);     // 4-float pieces of O per lane
 };
 
@@ -122,7 +128,22 @@ struct AttnParams {
   AttnPlace* place;  // [groups]
   float* part;       // [slot][QW] of PIECES x 64 lanes x 4 floats, two slots a workgroup
   float* part_ml;    // [slot][QW][64 lanes][2]: running maximum (log2) and sum
+  const float* k_scale;  // [pages][kv_heads][page_size], of caches of codes
+  const float* v_scale;
+  // A batch that shares its first rows (EXT kernels): kAtPrefix forms all
+  // requests' block rows' state over those, as one request of batch * T rows;
+  // kAtRest each request's over the rows behind, joined with that state.
+  int32_t mode;
+  int32_t requests;           // of the batch, for kAtPrefix (batch is 1 there)
+  const int32_t* shared_len;  // [1]
+  int32_t* prefix;            // [1], the shared rows in use: written by kAtPrefix
+  float* pre_o;               // [batch][T][q_heads][head_dim], divided by the sums
+  float* pre_ml;              // [batch][T][q_heads][2]: maximum (log2) and sum
+  int32_t shared;             // *prefix, in the kernel
 };
+
+enum { kAtAlone, kAtPrefix, kAtRest };
+constexpr int kAtShare = 128;  // shared rows are used in multiples of every tile's TR
 
 // One request's work: rows [0, rows) of its block see anything (0: the
 // request is taken out); its waves of NQ query rows per key/value head are
@@ -131,9 +152,18 @@ struct AttnReq {
   int past, rows, len, steps, waves, tiles;
 };
 
-template <class C>
+template <class C, bool EXT>
 __device__ __forceinline__ AttnReq attn_request(const AttnParams& p, int64_t b) {
+  static_assert(kAtShare % C::TR == 0, "shared rows are whole steps");
   AttnReq r;
+  if (EXT && p.mode == kAtPrefix) {
+    r.past = r.len = p.shared;
+    r.rows = p.T;
+    r.steps = r.len / C::TR;
+    r.waves = (r.rows * p.G + C::NQ - 1) / C::NQ;
+    r.tiles = (r.waves + C::QW - 1) / C::QW;
+    return r;
+  }
   r.past = p.past_len[b];
   int nodes = p.num_nodes ? p.num_nodes[b] : p.T - 1;
   nodes = nodes < 0 ? 0 : (nodes > p.T - 1 ? p.T - 1 : nodes);
@@ -142,6 +172,10 @@ __device__ __forceinline__ AttnReq attn_request(const AttnParams& p, int64_t b) 
   r.len = r.past < 0 ? 0 : (int)(n < p.rows.cap ? n : p.rows.cap);
   // one step for an empty request: its rows are cleared
   r.steps = r.len > C::TR ? (r.len + C::TR - 1) / C::TR : 1;
+  if (EXT) {  // (len >= shared where a request has rows)
+    r.steps -= p.shared / C::TR;
+    r.steps = r.steps > 1 ? r.steps : 1;
+  }
   r.waves = (r.rows * p.G + C::NQ - 1) / C::NQ;
   r.tiles = r.waves > C::QW ? (r.waves + C::QW - 1) / C::QW : 1;
   return r;
@@ -180,6 +214,7 @@ struct AttnLds {
   alignas(256) unsigned char tiles[C::LDS];
   int any[kAtWaves];
   AttnScratch plan;
+  alignas(16) float scale[C::SCALES ? C::SCALES : 1];  // [NG][NBUF]: K's times scale2, then V's
 };
 
 // The cut of the axis: end e of n stretches lies at total * e / n.
@@ -223,7 +258,7 @@ __device__ __forceinline__ int64_t attn_near(const AttnCut& c, int64_t s, int st
 // With many units, none of them long, each workgroup takes a whole one (to.x
 // < 0): the units' cache rows are then read by a key/value head's query tiles
 // at the same time, and the hardware deals the units out as they end.
-template <class C>
+template <class C, bool EXT>
 __device__ bool attn_plan(const AttnParams& p, AttnScratch& sh, int w, int& k, AttnCut& cut,
                           AttnPos& from, AttnPos& to) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -231,7 +266,7 @@ __device__ bool attn_plan(const AttnParams& p, AttnScratch& sh, int w, int& k, A
     units = 0;
     steps = 0;
     if (b >= p.batch) return;
-    const AttnReq r = attn_request<C>(p, b);
+    const AttnReq r = attn_request<C, EXT>(p, b);
     units = (int64_t)r.tiles * p.kv_heads;
     steps = r.steps;
   };
@@ -285,7 +320,7 @@ __device__ bool attn_plan(const AttnParams& p, AttnScratch& sh, int w, int& k, A
       at = AttnPos{-1, b, (int)(e - before), 0};
       return;
     }
-    const AttnReq r = attn_request<C>(p, b);
+    const AttnReq r = attn_request<C, EXT>(p, b);
     const int64_t x = attn_end(cut, e) - before;
     int64_t u = attn_div(x, r.steps), s = x - u * r.steps;
     if (e > 0 && e < n) s = attn_near(cut, s, r.steps);
@@ -396,6 +431,33 @@ __device__ __forceinline__ uint32_t attn_finite_only(uint32_t two) {
   return (two >> 16 & e) == e ? two & 0xFFFFu : two;
 }
 
+// The values of 16 codes, in order: all of them have exact values in H.
+template <typename H, int CACHE>
+__device__ __forceinline__ void attn_values(at_u32x4 codes, at_u32x4 (&x)[2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    if constexpr (CACHE == kAtE4M3) {
+      if constexpr (__is_same(H, __bf16)) {
+        lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], 1.0f, false));
+        hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], 1.0f, true));
+      } else {
+        lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.0f, false));
+        hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.0f, true));
+      }
+    } else {
+      H h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = (H)(float)(int8_t)(codes[i] >> (8 * e));
+      const uint2 two = __builtin_bit_cast(uint2, h);
+      lo = two.x;
+      hi = two.y;
+    }
+    x[i >> 1][2 * (i & 1)] = lo;
+    x[i >> 1][2 * (i & 1) + 1] = hi;
+  }
+}
+
 struct AttnFalse {
   static constexpr bool value = false;
 };
@@ -412,6 +474,7 @@ template <int DH>
 struct AttnState<DH, 32> {
   static constexpr int PIECES = DH / 8, R = 16;  // registers of an accumulator
   float m, mref, l;  // maximum in use (log2), the same less kBias or 0 while it is -inf, sum of weights
+  float vref, vinv;  // of float16 weights for caches of codes: o is in units of vref, 1 / vref
   at_f32x16 o[DH / 32];
   __device__ __forceinline__ at_f32x4 get(int j) const {
     const at_f32x16& x = o[j >> 2];
@@ -432,6 +495,7 @@ template <int DH>
 struct AttnState<DH, 16> {
   static constexpr int PIECES = DH / 16, R = 4;
   float m, mref, l;
+  float vref, vinv;
   at_f32x4 o[DH / 16];
   __device__ __forceinline__ at_f32x4 get(int j) const { return o[j]; }
   __device__ __forceinline__ void set(int j, at_f32x4 v) { o[j] = v; }
@@ -463,9 +527,13 @@ __device__ __forceinline__ uint64_t attn_visible(const AttnParams& p, int64_t b,
   return v & held;
 }
 
-// One staged tile. k, v: its rows in LDS; MASKED: vis says which are seen.
-template <typename H, int DH, int NQ, int KT, bool MASKED>
+// One staged tile. k, v: its rows in LDS; MASKED: vis says which are seen. Of a
+// cache of codes the tile holds the codes' values, and ks, vs their scales: a
+// score is multiplied by its key's, a weight by its value's before it is
+// rounded, so that the codes enter the products as they are.
+template <typename H, int DH, int NQ, int KT, bool MASKED, int CACHE>
 __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned char* v,
+                                          const float* ks, const float* vs,
                                           const at_u32x4 (&q)[DH * NQ / 512], float scale2,
                                           uint64_t vis, AttnState<DH, NQ>& st, int lane) {
   typedef AttnState<DH, NQ> State;
@@ -494,6 +562,17 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     if (c + kAhead < kF) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
   // s[t][r] is row NQ t + 4 Z (r / 4) + 4 z + r % 4
+  if constexpr (CACHE != kAtSame) {
+    scale2 = 1.0f;  // ks holds it
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+#pragma unroll
+      for (int r = 0; r < R; r += 4) {
+        const at_f32x4 a = *(const at_f32x4*)(ks + NQ * t + Z * r + 4 * z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][r + e] *= a[e];
+      }
+  }
   if (MASKED) {
 #pragma unroll
     for (int t = 0; t < NB; ++t) {
@@ -559,6 +638,35 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     factor = 1.0f;
     ref = -Weight::kBias;
   }
+  // Float16 weights take their values' scales in units of vref, which is at
+  // least the largest scale that the query has seen (twice what passed it).
+  constexpr bool kUnits = CACHE != kAtSame && !__is_same(H, __bf16);
+  if constexpr (kUnits) {
+    float most = 0.0f;
+#pragma unroll
+    for (int r = 0; r < KT; r += 4 * Z) {
+      const at_f32x4 a = *(const at_f32x4*)(vs + r + 4 * z);
+      const uint32_t bits = (uint32_t)(vis >> (r + 4 * z));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = fabsf(a[e]);
+        const bool on = x < INFINITY && (!MASKED || (bits >> e & 1));  // no NaN
+        most = fmaxf(most, on ? x : 0.0f);
+      }
+    }
+    most = attn_max_across<NQ>(most);
+    if (__ballot(most > st.vref) != 0) {
+      const bool more = most > st.vref;
+      const float to = fminf(fmaxf(2.0f * most, 0x1p-126f), 0x1p126f);
+      const float keep = more ? st.vref / to : 1.0f;
+      st.vinv = more ? 1.0f / to : st.vinv;
+      st.vref = more ? to : st.vref;
+#pragma unroll
+      for (int d = 0; d < DH / NQ; ++d)
+#pragma unroll
+        for (int r = 0; r < R; ++r) st.o[d][r] *= keep;
+    }
+  }
   // Rows that a query does not see have weight 0, but 0 times a NaN or an
   // infinity among their values is no 0: such values (garbage behind the
   // block, on unmapped pages, or in other nodes' rows) are taken out of the
@@ -567,7 +675,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
   if (MASKED) {
     bool bad = false;
     if (lane < KT)
-      for (int c = 0; c < CPR; ++c) {
+      for (int c = 0; c < (CACHE == kAtI8 ? 0 : CPR); ++c) {
         const at_u32x4 x = *(const at_u32x4*)(v + lane * ROW + c * 16);
         bad |= attn_not_finite<H>(x[0]) || attn_not_finite<H>(x[1]) || attn_not_finite<H>(x[2]) ||
                attn_not_finite<H>(x[3]);
@@ -595,8 +703,23 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     const int u = c / D, d = c % D;
     if (d == 0) {
       H w8[8];
+      if constexpr (CACHE == kAtSame) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w8[i] = (H)score(u, i);
+        for (int i = 0; i < 8; ++i) w8[i] = (H)score(u, i);
+      } else {
+        const float* at = vs + 8 * Z * u + 4 * z;
+        const uint32_t bits = (uint32_t)(vis >> (8 * Z * u + 4 * z));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const at_f32x4 a = *(const at_f32x4*)(at + 4 * Z * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float w = score(u, 4 * h + e) * (kUnits ? a[e] * st.vinv : a[e]);
+            if (MASKED && !(bits >> (4 * Z * h + e) & 1)) w = 0.0f;  // (the scale may be NaN)
+            w8[4 * h + e] = (H)w;
+          }
+        }
+      }
       pb = __builtin_bit_cast(at_u32x4, w8);
     }
     if (MASKED && dirty)
@@ -676,9 +799,31 @@ __device__ __forceinline__ AttnQuery attn_query(const AttnParams& p, const AttnR
 }
 
 // Pieces [j0, j0 + NP) of an output row.
-template <typename H, int DH, int NQ, int NP>
+template <typename H, int DH, int NQ, int NP, bool EXT>
 __device__ __forceinline__ void attn_store(const AttnParams& p, int64_t row, int j0, float m,
-                                           float l, const at_f32x4 (&o)[NP], int lane) {
+                                           float l, at_f32x4 (&o)[NP], int lane) {
+  if (EXT && p.mode == kAtPrefix) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+      *(at_f32x4*)(p.pre_o + row * DH + AttnState<DH, NQ>::element(j0 + j, lane)) = o[j] * inv;
+    if (lane < NQ && j0 == 0) *(float2*)(p.pre_ml + row * 2) = float2{m, l};
+    return;
+  }
+  if (EXT && p.mode == kAtRest && p.shared > 0) {
+    const float2 ml = *(const float2*)(p.pre_ml + row * 2);
+    const float top = fmaxf(m, ml.x);
+    const float a = (ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - top) : 0.0f) * ml.y;
+    const float b = m > -INFINITY ? __builtin_amdgcn_exp2f(m - top) : 0.0f;
+    m = top;
+    l = a + l * b;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const at_f32x4 x =
+          *(const at_f32x4*)(p.pre_o + row * DH + AttnState<DH, NQ>::element(j0 + j, lane));
+      o[j] = x * a + o[j] * b;
+    }
+  }
   const bool none = l == 0.0f;  // (a NaN stays one)
   const float inv = none ? 0.0f : 1.0f / l;
   H* out = (H*)p.out + row * DH;
@@ -735,10 +880,10 @@ __device__ __forceinline__ void attn_to_lds(const char* from, uint32_t to) {
 
 // Steps [t0, t1) of unit u of request b, into the output or workspace slot
 // `slot` (-1: the output).
-template <typename H, class C>
-__device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* lds, int* s_any,
-                                           int b, int u, const AttnReq& rq, int t0, int t1,
-                                           int slot) {
+template <typename H, class C, bool EXT>
+__device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* lds, float* s_scale,
+                                           int* s_any, int b, int u, const AttnReq& rq, int t0,
+                                           int t1, int slot) {
   constexpr int DH = C::DH, NQ = C::NQ, QW = C::QW;
   const int tid = attn_tid(), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -748,6 +893,10 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   const int i = me.i;
   const bool live = me.live;
   const bool busy = __ballot(live) != 0;  // a wave without queries only carries rows
+  if (EXT && p.mode == kAtRest) {  // steps behind the shared rows
+    t0 += p.shared / C::TR;
+    t1 += p.shared / C::TR;
+  }
   if (rq.len == 0) t1 = t0;
   constexpr int NF = DH * NQ / 512;  // Q fragments of 16 bytes
   at_u32x4 q[NF];
@@ -760,7 +909,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   }
   AttnState<DH, NQ> st;
   st.m = -INFINITY;
-  st.mref = st.l = 0.0f;
+  st.mref = st.l = st.vref = st.vinv = 0.0f;
 #pragma unroll
   for (int j = 0; j < C::PIECES; ++j) st.set(j, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 
@@ -774,17 +923,18 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   // With two buffers (in the first 64 KiB) a tile goes straight into
   // LDS, its chunks' order made by the lanes' addresses; otherwise it waits in
   // registers.
-  constexpr bool DIRECT = C::NBUF == 2 && C::LDS <= 65536;
+  constexpr bool CODES = C::CACHE != kAtSame;
+  constexpr bool DIRECT = !CODES && C::NBUF == 2 && C::LDS <= 65536;
   at_u32x4 kr[DIRECT ? 1 : C::LOADS], vr[DIRECT ? 1 : C::LOADS];
   // the entries of the next tile's pages, as read: a test here would wait for
   // them, and with them for the tile in flight
   int page[C::LOADS];
   const bool paged = p.rows.table != nullptr;
   const int32_t* const table = p.rows.table + (int64_t)b * p.rows.width;
-  const uint32_t page_bytes = (uint32_t)p.kv_heads * (uint32_t)p.rows.page_size * C::ROW;
+  const uint32_t page_bytes = (uint32_t)p.kv_heads * (uint32_t)p.rows.page_size * C::CROW;
   const int row_mask = paged ? p.rows.page_size - 1 : 0x7FFFFFFF;
   const int64_t base =
-      ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size * C::ROW;
+      ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size * C::CROW;
   const char* const kh = (const char*)p.k_cache + base;
   const char* const vh = (const char*)p.v_cache + base;
   auto row_of = [&](int t, int k) {  // the cache row that chunk k is of, clamped into the request
@@ -795,10 +945,23 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   // once lie on one page, so its address is scalar. (The entry still comes by
   // a vector load: a scalar one would make every LDS wait a full one.)
   const bool wide = paged && p.rows.page_size >= STEP;
-  const uint32_t lane_at = (uint32_t)(ld_row * C::ROW + ld_c * 16);
+  const uint32_t lane_at = (uint32_t)(ld_row * C::CROW + ld_c * 16);
   int zero = 0;
   asm volatile("" : "+v"(zero));
+  // scales of a tile: the group's thread gt has that of K's row gt, or of V's row gt - KT
+  const bool scaler = CODES && gt < 2 * C::KT;
+  const int s_row = gt % C::KT;
+  const float* const scales =
+      CODES ? (gt < C::KT ? p.k_scale : p.v_scale) + base / C::CROW : nullptr;
+  float* const scale_to = s_scale + g * C::NBUF * 2 * C::KT + (scaler ? gt : 0);
+  int s_page = 0;
+  float s_value = 0.0f;
+  auto scale_row = [&](int t) {
+    const int r = t * C::TR + g * C::KT + s_row;
+    return r < rq.len ? r : rq.len - 1;
+  };
   auto find = [&](int t) {
+    if (scaler && paged) s_page = table[scale_row(t) >> p.rows.shift];
     if (wide) {
 #pragma unroll
       for (int k = 0; k < C::LOADS; ++k) {
@@ -814,6 +977,10 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
     }
   };
   auto fetch = [&](int t) {
+    if (scaler) {  // (rows on no page: some row's, taken out by the mask)
+      const uint32_t pg = (uint32_t)s_page < (uint32_t)p.rows.pages && paged ? s_page : 0;
+      s_value = scales[(uint64_t)pg * (page_bytes / C::CROW) + (uint32_t)(scale_row(t) & row_mask)];
+    }
     if constexpr (DIRECT) {
       const uint32_t kt = tiles_at + (t & 1) * 2 * C::TILE;
 #pragma unroll
@@ -843,7 +1010,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
         // (rows behind the request's last are on the page too)
         const uint64_t at =
             (uint64_t)pg * page_bytes +
-            (uint64_t)(uint32_t)((t * C::TR + g * C::KT + k * STEP) & row_mask) * C::ROW;
+            (uint64_t)(uint32_t)((t * C::TR + g * C::KT + k * STEP) & row_mask) * C::CROW;
         kr[k] = *(const at_u32x4*)(kh + at + lane_at);
         vr[k] = *(const at_u32x4*)(vh + at + lane_at);
       }
@@ -853,7 +1020,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
         // rows on no page: some row's values, taken out by the mask
         const uint32_t pg = (uint32_t)page[k] < (uint32_t)p.rows.pages ? page[k] : 0;
         const uint64_t at = (uint64_t)pg * page_bytes +
-                            (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW + ld_c * 16;
+                            (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::CROW + ld_c * 16;
         kr[k] = *(const at_u32x4*)(kh + at);
         vr[k] = *(const at_u32x4*)(vh + at);
       }
@@ -885,9 +1052,21 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
 #pragma unroll
     for (int k = 0; k < (DIRECT ? 0 : C::LOADS); ++k) {
       const int row = ld_row + k * STEP;
-      *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, ld_c) * 16) = kr[k];
-      *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, ld_c) * 16) = vr[k];
+      if constexpr (CODES) {
+        at_u32x4 x[2];
+        attn_values<H, C::CACHE>(kr[k], x);
+        *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, 2 * ld_c) * 16) = x[0];
+        *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, 2 * ld_c + 1) * 16) = x[1];
+        attn_values<H, C::CACHE>(vr[k], x);
+        *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, 2 * ld_c) * 16) = x[0];
+        *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, 2 * ld_c + 1) * 16) = x[1];
+      } else {
+        *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, ld_c) * 16) = kr[k];
+        *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, ld_c) * 16) = vr[k];
+      }
     }
+    const int s_buf = C::NBUF == 2 ? (t & 1) * 2 * C::KT : 0;
+    if (scaler) scale_to[s_buf] = gt < C::KT ? s_value * p.scale2 : s_value;
     if (QW > 1) {
       __syncthreads();
     } else {  // the tile is the wave's own: its LDS operations take effect in order
@@ -907,7 +1086,9 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
         const bool held = lane < C::KT && r < rq.len && page_of(p.rows, b, r) >= 0;
         vis = attn_visible<C::KT>(p, b, rq.past, r0, i, live, __ballot(held));
       }
-      attn_tile<H, DH, NQ, C::KT, MASKED>(kt, vt, q, p.scale2, vis, st, lane);
+      const float* const sc = s_scale + g * C::NBUF * 2 * C::KT + s_buf;
+      attn_tile<H, DH, NQ, C::KT, MASKED, C::CACHE>(kt, vt, sc, sc + C::KT, q, p.scale2, vis, st,
+                                                    lane);
     }
     if (QW == 1) {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -919,6 +1100,10 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   for (; t < tm; ++t) step(t, AttnFalse{});
   for (; t < t1; ++t) step(t, AttnTrue{});
   st.l = attn_sum_across<NQ>(st.l);
+  if constexpr (CODES && !__is_same(H, __bf16)) {
+#pragma unroll
+    for (int j = 0; j < C::PIECES; ++j) st.set(j, st.get(j) * st.vref);
+  }
   const int out_lane = attn_tid() & 63;
 
   // merge the groups
@@ -948,8 +1133,8 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   if (slot < 0) {
     const AttnQuery to = attn_query<NQ>(p, rq, u, wq, out_lane);
     if (to.live)
-      attn_store<H, DH, NQ>(p, ((int64_t)b * p.T + to.i) * p.q_heads + to.hq, 0, st.m, st.l, o,
-                            out_lane);
+      attn_store<H, DH, NQ, C::PIECES, EXT>(p, ((int64_t)b * p.T + to.i) * p.q_heads + to.hq, 0,
+                                            st.m, st.l, o, out_lane);
     return;
   }
   at_f32x4* part = (at_f32x4*)p.part + ((int64_t)slot * QW + wq) * C::PIECES * kWave + out_lane;
@@ -960,9 +1145,41 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   ml[1] = st.l;
 }
 
-template <typename H, int DH, int NQ, int QW>
+// The rows that all requests taken part share, in whole steps of every tile, for
+// a batch whose first shared_len rows lie on the same pages: no more than any
+// request has committed. from: a request whose page table maps them.
+__device__ __forceinline__ int attn_shared(const AttnParams& p, AttnScratch& sh, int& from) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int least = 0x7FFFFFFF, first = 0x7FFFFFFF;
+  for (int b = tid; b < p.requests; b += kAtThreads) {
+    const int past = p.past_len[b];
+    if (past < 0) continue;
+    least = past < least ? past : least;
+    first = b < first ? b : first;
+  }
+  least = -wave_max(-least);
+  first = -wave_max(-first);
+  if (lane == 0) {
+    sh.part[wave][0] = least;
+    sh.part[wave][1] = first;
+  }
+  __syncthreads();
+  for (int i = 0; i < kAtWaves; ++i) {
+    least = sh.part[i][0] < least ? (int)sh.part[i][0] : least;
+    first = sh.part[i][1] < first ? (int)sh.part[i][1] : first;
+  }
+  __syncthreads();  // before the plan takes sh
+  from = __builtin_amdgcn_readfirstlane(first);
+  int n = *p.shared_len;
+  n = n < least ? n : least;
+  n = n < p.rows.cap ? n : (int)p.rows.cap;
+  n = first == 0x7FFFFFFF || n < 0 ? 0 : n / kAtShare * kAtShare;
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+template <typename H, int DH, int NQ, int QW, int CACHE = kAtSame, bool EXT = false>
 __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(AttnParams p) {
-  using C = AttnTile<DH, NQ, QW>;
+  using C = AttnTile<DH, NQ, QW, CACHE>;
   __shared__ AttnLds<C> sh;
   static_assert(offsetof(AttnLds<C>, tiles) == 0, "the tiles at LDS address 0");
   AttnPos at, to;
@@ -970,15 +1187,28 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
   AttnPlace mark{};
   AttnCut cut;
   int k = id;
-  if (attn_plan<C>(p, sh.plan, id, k, cut, at, to)) {
+  bool some = true;
+  if (EXT) {
+    p.shared = 0;
+    if (p.mode == kAtPrefix) {
+      int from;
+      p.shared = attn_shared(p, sh.plan, from);
+      if (id == 0 && threadIdx.x == 0) *p.prefix = p.shared;
+      some = p.shared > 0;
+      if (some) p.rows.table += (int64_t)from * p.rows.width;
+    } else if (p.mode == kAtRest) {
+      p.shared = __builtin_amdgcn_readfirstlane(*p.prefix);
+    }
+  }
+  if (some && attn_plan<C, EXT>(p, sh.plan, id, k, cut, at, to)) {
     const bool whole = to.x < 0;
-    AttnReq rq = attn_request<C>(p, at.b);
+    AttnReq rq = attn_request<C, EXT>(p, at.b);
     do {  // uniform; no stretch is empty but for ends moved onto one another
       if (!whole && at.x >= to.x) break;
       if (at.u == rq.tiles * p.kv_heads) {  // on to the next request
         ++at.b;
         at.u = 0;
-        rq = attn_request<C>(p, at.b);
+        rq = attn_request<C, EXT>(p, at.b);
       }
       const int64_t left = whole ? rq.steps : to.x - at.x;
       const int t1 = at.s + left < rq.steps ? at.s + (int)left : rq.steps;
@@ -995,8 +1225,8 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
         }
         mark = AttnPlace{(int)(e - k), at.b, at.u, rq.rows, rq.waves, rq.tiles, {0, 0}};
       }
-      attn_piece<H, C>(p, sh.tiles, sh.any, at.b, at.u, rq, at.s, t1,
-                       begins && ends ? -1 : 2 * k + (begins ? 1 : 0));
+      attn_piece<H, C, EXT>(p, sh.tiles, sh.scale, sh.any, at.b, at.u, rq, at.s, t1,
+                            begins && ends ? -1 : 2 * k + (begins ? 1 : 0));
       if (ends && (at.u + 1) % rq.tiles == 0 && rq.rows < p.T)
         attn_clear<H, DH>(p, at.b, rq.rows, at.u / rq.tiles);
       at.x += t1 - at.s;
@@ -1013,13 +1243,14 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
 // through as many CUs as there are; four pieces to a wave against two: 5.0 and
 // 4.0 us for one tree, 11.3 and 8.9 for 24 units in 512 pieces, 5.0 and 5.9 for
 // the 64 trees, where it finds nothing to merge).
-template <typename H, int DH, int NQ, int QW>
+template <typename H, int DH, int NQ, int QW, int CACHE = kAtSame, bool EXT = false>
 __global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
-  using C = AttnTile<DH, NQ, QW>;
+  using C = AttnTile<DH, NQ, QW, CACHE>;
   constexpr int PP = kAtMerge, PER = C::PIECES / PP;  // waves of a state
   const int k = (int)(blockIdx.x / (QW * PER)), r = (int)(blockIdx.x % (QW * PER));
   const AttnPlace pl = p.place[k];
   if (pl.pieces == 0) return;
+  if (EXT && p.mode == kAtRest) p.shared = *p.prefix;
   const int lane = threadIdx.x, wq = r / PER, j0 = PP * (r % PER);
   AttnReq rq;
   rq.rows = pl.rows;
@@ -1045,7 +1276,8 @@ __global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
     for (int j = 0; j < PP; ++j) o[j] = o[j] * a + part[j * kWave] * b;
   }
   if (me.live)
-    attn_store<H, DH, NQ>(p, ((int64_t)pl.b * p.T + me.i) * p.q_heads + me.hq, j0, m, l, o, lane);
+    attn_store<H, DH, NQ, PP, EXT>(p, ((int64_t)pl.b * p.T + me.i) * p.q_heads + me.hq, j0, m, l,
+                                   o, lane);
 }
 
 }  // namespace ddt

@@ -40,6 +40,10 @@
  *    attention reads the cache under the ancestor mask, and the accepted
  *    path's rows are kept. DDTree explainer, section 5; SparklingTree post,
  *    section "Step 4".
+ *  - ddtree_append_kv8, ddtree_attention_kv8, ddtree_compact_kv8 and
+ *    ddtree_read_kv8: the same over caches of 8-bit rows, quantised as they are
+ *    written, and such rows read back. ddtree_attention_shared: the attention
+ *    of a batch whose requests share their first rows, computed once for all.
  *  - ddtree_accept_sampled, dspark_accept_sampled: acceptance at a
  *    temperature from given random numbers, for trees and for sampled chains
  *    (DSpark explainer, speculative decoding basics), in place of the greedy
@@ -87,8 +91,10 @@ enum {
 };
 
 /* Element types. Logits are DDT_BF16 or DDT_F32; the verification pass's
- * queries, keys and values are DDT_BF16 or DDT_F16. */
-enum { DDT_BF16 = 0, DDT_F32 = 1, DDT_F16 = 2 };
+ * queries, keys and values are DDT_BF16 or DDT_F16, and caches of 8-bit rows
+ * hold DDT_E4M3 (one sign, four exponent and three fraction bits, bias 7, no
+ * infinities, largest 448) or DDT_I8. */
+enum { DDT_BF16 = 0, DDT_F32 = 1, DDT_F16 = 2, DDT_E4M3 = 3, DDT_I8 = 4 };
 
 /* Supported region. */
 #define DDT_MAX_B 512   /* node budget */
@@ -348,6 +354,115 @@ int ddtree_compact_kv_paged(void* k_cache, void* v_cache, int64_t layers, int64_
                             const int32_t* past_len, const int32_t* accepted_nodes,
                             const int32_t* accept_len, int32_t L, int32_t* new_len,
                             hipStream_t stream);
+
+/*
+ * Caches of 8-bit rows. A layer's codes are [pages][kv_heads][page_size]
+ * [head_dim] bytes of cache_dtype (DDT_E4M3 or DDT_I8), its scales
+ * [pages][kv_heads][page_size] float (4-byte aligned): an element stands for
+ * code * scale. Pages, tables, blocks and requests taken out are those of the
+ * 16-bit caches above; page_table NULL is a contiguous cache in every call.
+ *
+ * ddtree_append_kv8 -- ddtree_append_kv into such a cache. With x a head's key
+ * (rotated in float32, each product and sum rounded by itself, not rounded to
+ * dtype) or value and M the largest code (448 or 127):
+ *   scale = max(max |x| * (1 / M), 2^-126), r = 1 / scale,
+ *   code = x * r rounded to the nearest code (ties to even), within +-M,
+ * all in float32, 1 / M rounded to it: code * scale is off x by at most half a
+ * step, 2^-4 of it for e4m3 (2^-10 scale below 2^-6 scale), scale / 2 for int8,
+ * and 2^-22 of max |x| (three roundings). A head's row that holds a NaN or an
+ * infinity has the scale NaN and codes 0. Queries, and the rows that are left
+ * out, are as in ddtree_append_kv, which has the other arguments too.
+ */
+int ddtree_append_kv8(const void* q, const void* k, const void* v, int dtype, int64_t batch,
+                      int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* rope,
+                      int64_t rope_len, int32_t rope_dim, int32_t interleaved,
+                      const int32_t* past_len, const int32_t* depths, const int32_t* num_nodes,
+                      const int32_t* page_table, int64_t table_width, int64_t pages,
+                      int32_t page_size, int cache_dtype, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, void* q_out, hipStream_t stream);
+
+/*
+ * ddtree_attention_kv8 -- ddtree_attention over a cache of 8-bit rows, K_n and
+ * V_n being what the rows stand for. The codes enter the products as they are
+ * (all have exact values in dtype); a score takes its key's scale in float32, a
+ * weight its value's before it is rounded to dtype for its product with V
+ * (DDT_F16: in units of the largest scale seen, or of twice that). Codes and
+ * scales of any finite value may lie in the cache; what a row does not see
+ * (NaN and infinite scales and e4m3 NaN codes included) does not reach it, and
+ * a row that sees a NaN has NaN.
+ * shared_len [1] int32 or NULL: as in ddtree_attention_shared (page_table is
+ * then required, DDT_EINVAL otherwise). The workspace's size takes `shared` = 1
+ * with it, 0 without. Everything else as in ddtree_attention.
+ */
+size_t ddtree_attention_kv8_workspace_size(int64_t batch, int32_t T, int32_t q_heads,
+                                           int32_t kv_heads, int32_t head_dim,
+                                           int64_t pages_per_request, int32_t page_size,
+                                           int32_t shared);
+int ddtree_attention_kv8(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
+                         int32_t kv_heads, int32_t head_dim, int cache_dtype, const void* k_cache,
+                         const void* v_cache, const float* k_scale, const float* v_scale,
+                         const int32_t* page_table, int64_t table_width, int64_t pages,
+                         int32_t page_size, const int32_t* past_len, const int32_t* num_nodes,
+                         const uint64_t* mask, const int32_t* shared_len, float scale, void* out,
+                         float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ddtree_attention_shared -- ddtree_attention of a batch whose requests share
+ * their first rows (a system prompt, a document asked about more than once):
+ * the page table maps rows [0, shared_len[0]) of every request that takes part
+ * (past_len >= 0) to the same pages, and the attention over them is computed
+ * once for the whole batch. What it gives is what ddtree_attention gives with
+ * the same arguments, up to rounding: the shared rows' part is joined with each
+ * request's own by their maxima and sums, in float32. shared_len [1] int32,
+ * device memory: a negative one is 0, and more rows than a request has
+ * committed (past_len) are never taken as shared. That the entries are alike is
+ * not tested: where they differ, the first such request's are used for all.
+ * With more than 64 query rows (T * q_heads / kv_heads) to a request's
+ * key/value head, and for one request, the call is ddtree_attention's: such
+ * calls are bound by their products, which sharing does not save.
+ * Supported as ddtree_attention, with a page table (DDT_EINVAL otherwise) and
+ * batch * T * q_heads / kv_heads < 2^31 - 2^13 (DDT_ENOTSUP). The workspace
+ * (ddtree_attention_shared_workspace_size) also holds the shared rows' part, a
+ * float32 row for each row of q.
+ */
+size_t ddtree_attention_shared_workspace_size(int64_t batch, int32_t T, int32_t q_heads,
+                                              int32_t kv_heads, int32_t head_dim,
+                                              int64_t pages_per_request, int32_t page_size);
+int ddtree_attention_shared(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
+                            int32_t kv_heads, int32_t head_dim, const void* k_cache,
+                            const void* v_cache, const int32_t* page_table, int64_t table_width,
+                            int64_t pages, int32_t page_size, const int32_t* past_len,
+                            const int32_t* num_nodes, const uint64_t* mask,
+                            const int32_t* shared_len, float scale, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ddtree_compact_kv8 -- ddtree_compact_kv_paged for caches of 8-bit rows, codes
+ * [layers][pages][heads][page_size][head_dim] and scales [layers][pages][heads]
+ * [page_size] together. Supported: head_dim a multiple of 8 up to 512, 1 <= L
+ * <= DDT_MAX_L. page_table NULL: contiguous caches, pages = batch.
+ */
+int ddtree_compact_kv8(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       int64_t layers, int64_t pages, int32_t heads, int32_t page_size,
+                       int32_t head_dim, const int32_t* page_table, int64_t table_width,
+                       int64_t batch, const int32_t* past_len, const int32_t* accepted_nodes,
+                       const int32_t* accept_len, int32_t L, int32_t* new_len,
+                       hipStream_t stream);
+
+/*
+ * ddtree_read_kv8 -- rows of a cache of 8-bit rows, read back: rows first[b] +
+ * i, i < min(count[b], n), of request b to k_out and v_out
+ * [batch][n][kv_heads][head_dim] of dtype (DDT_BF16, DDT_F16 or DDT_F32; 16-byte
+ * aligned): code * scale in float32, rounded once. Rows from count[b] on, and
+ * rows that do not exist or lie on no page, are 0. first [batch] int32, count
+ * [batch] int32 (NULL: n). Supported: head_dim a multiple of 8 up to 512.
+ */
+int ddtree_read_kv8(int cache_dtype, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, int32_t kv_heads, int32_t head_dim,
+                    const int32_t* page_table, int64_t table_width, int64_t pages,
+                    int32_t page_size, int64_t batch, const int32_t* first, const int32_t* count,
+                    int32_t n, int dtype, void* k_out, void* v_out, hipStream_t stream);
 
 /*
  * ddtree_accept_sampled -- the walk of ddtree_accept at a temperature, from

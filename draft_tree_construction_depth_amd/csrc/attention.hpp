@@ -85,18 +85,24 @@ enum { kAtSame, kAtE4M3, kAtI8 };
 template <int DH_, int NQ_, int QW_, int CACHE_ = kAtSame>
 struct AttnTile {
   static constexpr int DH = DH_, NQ = NQ_, QW = QW_, CACHE = CACHE_;
+  static constexpr bool CODES = CACHE != kAtSame;
   static constexpr int NG = kAtWaves / QW;                 // groups over cache rows
-  static constexpr int KT = QW == 4 && DH <= 128 ? 64 : 32;  // rows of a group's tile
+  static constexpr int SK = QW == 4 && DH <= 128 ? 64 : 32;  // rows that a wave works on at once
+  static constexpr int KT = CODES && QW == 4 && DH == 64 ? 2 * SK : SK;  // rows of a group's tile
   static constexpr int TR = NG * KT;                       // rows of a workgroup's step
   static constexpr int ROW = DH * 2;                       // bytes of a row in LDS
-  static constexpr int CROW = CACHE == kAtSame ? ROW : DH;  // ... in the cache
+  static constexpr int KROW = CODES ? ROW + 16 : ROW;      // ... of K's there, padded
+  static constexpr int CROW = CODES ? DH : ROW;            // ... in the cache
   static constexpr int CPR = CROW / 16;                    // 16-byte chunks of a row there
   static constexpr int LOADS = KT * CPR / (QW * kWave);    // chunks per thread, K and V each
   static constexpr int NBUF = QW == 1 ? 1 : 2;             // one wave needs no second buffer
-  static constexpr int TILE = KT * ROW;                    // bytes of K (or V) of a tile
-  static constexpr int LDS = NG * NBUF * 2 * TILE;
-  static constexpr int SCALES = CACHE == kAtSame ? 0 : NG * NBUF * 2 * KT;  // floats in LDS
+  static constexpr int KTILE = KT * KROW;                  // bytes of K of a tile
+  static constexpr int TILE = KT * ROW;                    // ... of V (and of K unpadded)
+  static constexpr int LDS = NG * NBUF * (KTILE + TILE);
+  static constexpr int SCALES = CODES ? NG * NBUF * 2 * KT : 0;  // floats in LDS
   static constexpr int PIECES = DH * NQ / (4 * kWave);     // 4-float pieces of O per lane
+  // tiles of codes in flight: two where the registers hold them
+  static constexpr int PREFETCH = DH == 64 && NQ == 16 ? 2 : 1;
 };
 
 // What a workgroup's stretch leaves to merge: the unit that it begins and does
@@ -215,6 +221,9 @@ struct AttnLds {
   int any[kAtWaves];
   AttnScratch plan;
   alignas(16) float scale[C::SCALES ? C::SCALES : 1];  // [NG][NBUF]: K's times scale2, then V's
+  // [NG][NBUF][QW]: of what a wave staged, the largest scale of V; NaN codes of V
+  alignas(16) float most[C::CODES ? kAtWaves * C::NBUF : 1];
+  int flag[C::CODES ? kAtWaves * C::NBUF : 1];
 };
 
 // The cut of the axis: end e of n stretches lies at total * e / n.
@@ -446,18 +455,23 @@ __device__ __forceinline__ void attn_values(at_u32x4 codes, at_u32x4 (&x)[2]) {
         hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.0f, true));
       }
     } else {
-      H h[4];
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      typedef H h2 __attribute__((ext_vector_type(2)));
+      float f[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = (H)(float)(int8_t)(codes[i] >> (8 * e));
-      const uint2 two = __builtin_bit_cast(uint2, h);
-      lo = two.x;
-      hi = two.y;
+      for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(codes[i] >> (8 * e));
+      lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{f[0], f[1]}, h2));
+      hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{f[2], f[3]}, h2));
     }
     x[i >> 1][2 * (i & 1)] = lo;
     x[i >> 1][2 * (i & 1) + 1] = hi;
   }
 }
 
+template <int N>
+struct AttnNumber {
+  static constexpr int value = N;
+};
 struct AttnFalse {
   static constexpr bool value = false;
 };
@@ -474,7 +488,7 @@ template <int DH>
 struct AttnState<DH, 32> {
   static constexpr int PIECES = DH / 8, R = 16;  // registers of an accumulator
   float m, mref, l;  // maximum in use (log2), the same less kBias or 0 while it is -inf, sum of weights
-  float vref, vinv;  // of float16 weights for caches of codes: o is in units of vref, 1 / vref
+  float unit;  // of float16 weights for caches of codes: o and l are in units of 2^unit
   at_f32x16 o[DH / 32];
   __device__ __forceinline__ at_f32x4 get(int j) const {
     const at_f32x16& x = o[j >> 2];
@@ -495,7 +509,7 @@ template <int DH>
 struct AttnState<DH, 16> {
   static constexpr int PIECES = DH / 16, R = 4;
   float m, mref, l;
-  float vref, vinv;
+  float unit;
   at_f32x4 o[DH / 16];
   __device__ __forceinline__ at_f32x4 get(int j) const { return o[j]; }
   __device__ __forceinline__ void set(int j, at_f32x4 v) { o[j] = v; }
@@ -527,13 +541,9 @@ __device__ __forceinline__ uint64_t attn_visible(const AttnParams& p, int64_t b,
   return v & held;
 }
 
-// One staged tile. k, v: its rows in LDS; MASKED: vis says which are seen. Of a
-// cache of codes the tile holds the codes' values, and ks, vs their scales: a
-// score is multiplied by its key's, a weight by its value's before it is
-// rounded, so that the codes enter the products as they are.
-template <typename H, int DH, int NQ, int KT, bool MASKED, int CACHE>
+// One staged tile. k, v: its rows in LDS; MASKED: vis says which are seen.
+template <typename H, int DH, int NQ, int KT, bool MASKED>
 __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned char* v,
-                                          const float* ks, const float* vs,
                                           const at_u32x4 (&q)[DH * NQ / 512], float scale2,
                                           uint64_t vis, AttnState<DH, NQ>& st, int lane) {
   typedef AttnState<DH, NQ> State;
@@ -562,17 +572,6 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     if (c + kAhead < kF) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
   // s[t][r] is row NQ t + 4 Z (r / 4) + 4 z + r % 4
-  if constexpr (CACHE != kAtSame) {
-    scale2 = 1.0f;  // ks holds it
-#pragma unroll
-    for (int t = 0; t < NB; ++t)
-#pragma unroll
-      for (int r = 0; r < R; r += 4) {
-        const at_f32x4 a = *(const at_f32x4*)(ks + NQ * t + Z * r + 4 * z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][r + e] *= a[e];
-      }
-  }
   if (MASKED) {
 #pragma unroll
     for (int t = 0; t < NB; ++t) {
@@ -638,35 +637,6 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     factor = 1.0f;
     ref = -Weight::kBias;
   }
-  // Float16 weights take their values' scales in units of vref, which is at
-  // least the largest scale that the query has seen (twice what passed it).
-  constexpr bool kUnits = CACHE != kAtSame && !__is_same(H, __bf16);
-  if constexpr (kUnits) {
-    float most = 0.0f;
-#pragma unroll
-    for (int r = 0; r < KT; r += 4 * Z) {
-      const at_f32x4 a = *(const at_f32x4*)(vs + r + 4 * z);
-      const uint32_t bits = (uint32_t)(vis >> (r + 4 * z));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = fabsf(a[e]);
-        const bool on = x < INFINITY && (!MASKED || (bits >> e & 1));  // no NaN
-        most = fmaxf(most, on ? x : 0.0f);
-      }
-    }
-    most = attn_max_across<NQ>(most);
-    if (__ballot(most > st.vref) != 0) {
-      const bool more = most > st.vref;
-      const float to = fminf(fmaxf(2.0f * most, 0x1p-126f), 0x1p126f);
-      const float keep = more ? st.vref / to : 1.0f;
-      st.vinv = more ? 1.0f / to : st.vinv;
-      st.vref = more ? to : st.vref;
-#pragma unroll
-      for (int d = 0; d < DH / NQ; ++d)
-#pragma unroll
-        for (int r = 0; r < R; ++r) st.o[d][r] *= keep;
-    }
-  }
   // Rows that a query does not see have weight 0, but 0 times a NaN or an
   // infinity among their values is no 0: such values (garbage behind the
   // block, on unmapped pages, or in other nodes' rows) are taken out of the
@@ -675,7 +645,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
   if (MASKED) {
     bool bad = false;
     if (lane < KT)
-      for (int c = 0; c < (CACHE == kAtI8 ? 0 : CPR); ++c) {
+      for (int c = 0; c < CPR; ++c) {
         const at_u32x4 x = *(const at_u32x4*)(v + lane * ROW + c * 16);
         bad |= attn_not_finite<H>(x[0]) || attn_not_finite<H>(x[1]) || attn_not_finite<H>(x[2]) ||
                attn_not_finite<H>(x[3]);
@@ -703,23 +673,8 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
     const int u = c / D, d = c % D;
     if (d == 0) {
       H w8[8];
-      if constexpr (CACHE == kAtSame) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w8[i] = (H)score(u, i);
-      } else {
-        const float* at = vs + 8 * Z * u + 4 * z;
-        const uint32_t bits = (uint32_t)(vis >> (8 * Z * u + 4 * z));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const at_f32x4 a = *(const at_f32x4*)(at + 4 * Z * h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float w = score(u, 4 * h + e) * (kUnits ? a[e] * st.vinv : a[e]);
-            if (MASKED && !(bits >> (4 * Z * h + e) & 1)) w = 0.0f;  // (the scale may be NaN)
-            w8[4 * h + e] = (H)w;
-          }
-        }
-      }
+      for (int i = 0; i < 8; ++i) w8[i] = (H)score(u, i);
       pb = __builtin_bit_cast(at_u32x4, w8);
     }
     if (MASKED && dirty)
@@ -752,6 +707,228 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
         st.set(j, o);
         if (j & 1) asm volatile("" ::: "memory");  // a few elements at a time
       }
+    }
+  }
+}
+
+// One staged tile of a cache of codes. k, v hold the codes' values; ks, vs the
+// rows' scales (K's times scale * log2(e)): a score takes its key's, a weight
+// its value's before it is rounded, so that the codes enter the products as
+// they are. most: the largest finite scale of the tile's values (of an unmasked
+// tile, for float16); scan: V may hold NaNs. The rest is attn_tile's.
+constexpr float kAtLeastUnit = -60.0f;  // 2^-60: values of smaller scales are 0 in float16
+
+template <typename H, int DH, int NQ, int KT, bool MASKED>
+__device__ __forceinline__ void attn_tile_codes(const unsigned char* k, const unsigned char* v,
+                                                const float* ks, const float* vs, float most,
+                                                bool scan, const at_u32x4 (&q)[DH * NQ / 512],
+                                                uint64_t vis, AttnState<DH, NQ>& st, int lane) {
+  typedef AttnState<DH, NQ> State;
+  typedef AttnWeight<H> Weight;
+  constexpr bool kUnits = !__is_same(H, __bf16);
+  constexpr int NB = KT / NQ, R = State::R, ROW = DH * 2, KROW = ROW + 16, CPR = DH / 8;
+  constexpr int Z = kWave / NQ;  // lanes with one query
+  const int z = lane / NQ;
+  decltype(st.o[0] + st.o[0]) s[NB];
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[t][r] = 0.0f;
+    const int row = NQ * t + lane % NQ;
+    at_u32x4 a[CPR / Z];
+#pragma unroll
+    for (int c = 0; c < CPR / Z; ++c)
+      a[c] = *(const at_u32x4*)(k + row * KROW + (Z * c + z) * 16);
+#pragma unroll
+    for (int c = 0; c < CPR / Z; ++c) s[t] = attn_mfma<H>(a[c], q[c], s[t]);
+  }
+  // four fragments' reads ahead of the products
+  constexpr int kF = NB * CPR / Z, kAhead = 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+  for (int c = 0; c < kF; ++c) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (c + kAhead < kF) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  // s[t][r] is row NQ t + 4 Z (r / 4) + 4 z + r % 4
+  // Weights for float16 are in units of 2^unit, above all scales of values that
+  // the query has seen.
+  if constexpr (kUnits) {
+    if (MASKED) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int r = 0; r < KT; r += 4 * Z) {
+        const at_u32x4 a = *(const at_u32x4*)(vs + r + 4 * z);
+        const uint32_t bits = (uint32_t)(vis >> (r + 4 * z));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // magnitudes as numbers, those seen and finite
+          const uint32_t x = a[e] & (uint32_t)((int32_t)(bits << (31 - e)) >> 31) & 0x7FFFFFFFu;
+          const uint32_t y = x < 0x7F800000u ? x : 0;
+          top = y > top ? y : top;
+        }
+      }
+      most = __uint_as_float(top);
+      most = attn_max_across<NQ>(most);
+    }
+    // (the unit is a float16 step or two above the scale, so it seldom moves)
+    const float need = fminf((float)(__builtin_amdgcn_frexp_expf(most) + 1), -kAtLeastUnit);
+    const bool more = (most > 0.0f) & (need > st.unit + 1.0f);
+    if (__ballot(more) != 0) {
+      const float to = more ? need : st.unit, keep = __builtin_amdgcn_exp2f(st.unit - to);
+#pragma unroll
+      for (int d = 0; d < DH / NQ; ++d)
+#pragma unroll
+        for (int r = 0; r < R; ++r) st.o[d][r] *= keep;
+      st.l *= keep;
+      st.mref += st.m > -INFINITY ? to - st.unit : 0.0f;
+      st.unit = to;
+    }
+  }
+  // A weight's exponent is score * ks - mref, in one FMA. Past 2^24 the product
+  // is rounded first and the maximum taken off it, mref's bias last.
+  const bool big = __ballot(fabsf(st.mref) > 0x1p24f - 256.0f) != 0;
+  const float from = big ? 0.0f : st.mref;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    const uint32_t bits = (uint32_t)(vis >> (NQ * t)) >> (4 * z);
+#pragma unroll
+    for (int r = 0; r < R; r += 4) {
+      const at_f32x4 a = *(const at_f32x4*)(ks + NQ * t + Z * r + 4 * z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = fmaf(s[t][r + e], a[e], -from);
+        if (MASKED) {  // a clear bit: -inf
+          const uint32_t on = (uint32_t)((int32_t)(bits << (31 - (Z * r + e))) >> 31);
+          x = __uint_as_float((on & __float_as_uint(x)) | (~on & 0xFF800000u));
+        }
+        s[t][r + e] = x;
+      }
+    }
+  }
+  // V^T fragments: product c = D u + d takes rows [8 Z u, 8 Z u + 8 Z), in
+  // two 4-row pieces of each lane, 4 Z rows apart, and head elements [NQ d,
+  // NQ d + NQ). Two are read ahead of the products, the first two here.
+  constexpr int U = KT / (8 * Z), D = DH / NQ;
+  const int ls = lane & 15, vrow = 4 * z + (ls >> 2);
+  const int vc = (NQ == 32 ? ((lane >> 4) & 1) * 2 : 0) + ((ls & 3) >> 1);
+  auto fragment = [&](int c) -> at_u32x4 {
+    typedef __attribute__((address_space(3))) at_s16x4 lds_s16x4;
+    const int u = c / D, d = c % D;
+    const int at = vrow * ROW + attn_v_chunk<DH>(vrow, NQ / 8 * d + vc) * 16 + (ls & 1) * 8;
+    struct {
+      at_s16x4 lo, hi;
+    } f;
+    f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (8 * Z * u) * ROW + at));
+    f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + (8 * Z * u + 4 * Z) * ROW + at));
+    return __builtin_bit_cast(at_u32x4, f);
+  };
+  at_u32x4 f[3] = {fragment(0), fragment(1), {0, 0, 0, 0}};
+  float top = s[0][0];
+#pragma unroll
+  for (int t = 0; t < NB; ++t)
+#pragma unroll
+    for (int r = 0; r < R; ++r) top = fmaxf(top, s[t][r]);
+  top = attn_max_across<NQ>(top) + from;
+  // The maximum moves only when a score passes it by more than kSlack.
+  const bool more = top > st.m + Weight::kSlack;
+  if (big || __ballot(more) != 0) {
+    const float m = more ? top : st.m, keep = more ? __builtin_amdgcn_exp2f(st.m - m) : 1.0f;
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int r = 0; r < R; ++r) st.o[d][r] *= keep;
+    st.l *= keep;
+    st.m = m;
+    const float bias = Weight::kBias - st.unit, ref = m > -INFINITY ? m : 0.0f;
+    st.mref = m > -INFINITY ? m - bias : 0.0f;
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[t][r] = (s[t][r] + (from - ref)) + bias;
+  }
+  // Rows that a query does not see have weight 0, but 0 times a NaN or an
+  // infinity among their values is no 0: such values (garbage behind the
+  // block, on unmapped pages, or in other nodes' rows) are taken out of the
+  // product and added by themselves for the queries that do see them.
+  uint64_t dirty = 0;
+  if (MASKED && scan) {  // uniform
+    bool bad = false;
+    const unsigned char* const mine = v + (lane & (KT - 1)) * ROW;
+    for (int c = 0; c < CPR; ++c) {
+      const at_u32x4 x = *(const at_u32x4*)(mine + c * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bad |= attn_not_finite<H>(x[e]);
+    }
+    bad &= lane < KT;
+    dirty = __ballot(bad);
+  }
+  // weight i (0..7) of the rows of product group u
+  auto score = [&](int u, int i) -> float {
+    return NQ == 32 ? s[u >> 1][(8 * (u & 1) + i) % R] : s[NQ == 32 ? 0 : 2 * u + (i >> 2)][i & 3];
+  };
+  float sum[2] = {0.0f, 0.0f};
+  auto weigh = [&](int u, int i) {
+    const float w = __builtin_amdgcn_exp2f(score(u, i));
+    if (NQ == 32)
+      s[u >> 1][(8 * (u & 1) + i) % R] = w;
+    else
+      s[NQ == 32 ? 0 : 2 * u + (i >> 2)][i & 3] = w;
+    sum[i & 1] += w;
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) weigh(0, i);
+  at_u32x4 pb;
+#pragma unroll
+  for (int c = 0; c < U * D; ++c) {
+    const int u = c / D, d = c % D;
+    if (d == 0) {
+      H w8[8];
+      const uint32_t bits = (uint32_t)(vis >> (8 * Z * u + 4 * z));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const at_f32x4 a = *(const at_f32x4*)(vs + 8 * Z * u + 4 * Z * h + 4 * z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float w = score(u, 4 * h + e) * a[e];
+          if (MASKED)  // 0 where the scale of a row that is not seen may be NaN
+            w = __uint_as_float(__float_as_uint(w) &
+                                (uint32_t)((int32_t)(bits << (31 - (4 * Z * h + e))) >> 31));
+          w8[4 * h + e] = (H)w;
+        }
+      }
+      pb = __builtin_bit_cast(at_u32x4, w8);
+    }
+    if (MASKED && dirty)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[c % 3][i] = attn_finite_only<H>(f[c % 3][i]);
+    st.o[d] = attn_mfma<H>(f[c % 3], pb, st.o[d]);
+    if (c + 2 < U * D) f[(c + 2) % 3] = fragment(c + 2);
+    // between the products: the exponentials of the next group
+    if (u + 1 < U)
+#pragma unroll
+      for (int i = 8 * d / D; i < 8 * (d + 1) / D; ++i) weigh(u + 1, i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  st.l += sum[0] + sum[1];
+  while (MASKED && dirty) {  // uniform
+    const int row = __builtin_ctzll(dirty);
+    dirty &= dirty - 1;
+    const bool seen = vis >> row & 1;
+#pragma unroll
+    for (int j = 0; j < State::PIECES; ++j) {
+      const int e = State::element(j, lane);
+      const uint2 x =
+          *(const uint2*)(v + row * ROW + attn_v_chunk<DH>(row, e >> 3) * 16 + (e & 7) * 2);
+      // what is not finite, times any weight; 0 elsewhere
+      const uint32_t two[2] = {x.x ^ attn_finite_only<H>(x.x), x.y ^ attn_finite_only<H>(x.y)};
+      at_f32x4 o = st.get(j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float y = (float)__builtin_bit_cast(H, (uint16_t)(two[i >> 1] >> (16 * (i & 1))));
+        o[i] += seen ? y : 0.0f;
+      }
+      st.set(j, o);
+      if (j & 1) asm volatile("" ::: "memory");  // a few elements at a time
     }
   }
 }
@@ -878,41 +1055,14 @@ __device__ __forceinline__ void attn_to_lds(const char* from, uint32_t to) {
                : "memory", "m0");
 }
 
-// Steps [t0, t1) of unit u of request b, into the output or workspace slot
-// `slot` (-1: the output).
-template <typename H, class C, bool EXT>
-__device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* lds, float* s_scale,
-                                           int* s_any, int b, int u, const AttnReq& rq, int t0,
-                                           int t1, int slot) {
+// Steps [t0, t1) of one key/value head's pass over a 16-bit cache.
+template <typename H, class C>
+__device__ __forceinline__ void attn_steps(const AttnParams& p, unsigned char* lds, int* s_any,
+                                           int b, const AttnReq& rq, int head, int t0, int t1,
+                                           int g, int wq, int lane, int i, bool live, bool busy,
+                                           const at_u32x4 (&q)[C::DH * C::NQ / 512],
+                                           AttnState<C::DH, C::NQ>& st) {
   constexpr int DH = C::DH, NQ = C::NQ, QW = C::QW;
-  const int tid = attn_tid(), lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int g = wave / QW, wq = wave % QW;
-  const int head = u / rq.tiles;
-  const AttnQuery me = attn_query<NQ>(p, rq, u, wq, lane);
-  const int i = me.i;
-  const bool live = me.live;
-  const bool busy = __ballot(live) != 0;  // a wave without queries only carries rows
-  if (EXT && p.mode == kAtRest) {  // steps behind the shared rows
-    t0 += p.shared / C::TR;
-    t1 += p.shared / C::TR;
-  }
-  if (rq.len == 0) t1 = t0;
-  constexpr int NF = DH * NQ / 512;  // Q fragments of 16 bytes
-  at_u32x4 q[NF];
-  {
-    const H* src =
-        (const H*)p.q + (((int64_t)b * p.T + i) * p.q_heads + me.hq) * DH + lane / NQ * 8;
-#pragma unroll
-    for (int c = 0; c < NF; ++c)
-      q[c] = live ? *(const at_u32x4*)(src + DH / NF * c) : at_u32x4{0, 0, 0, 0};
-  }
-  AttnState<DH, NQ> st;
-  st.m = -INFINITY;
-  st.mref = st.l = st.vref = st.vinv = 0.0f;
-#pragma unroll
-  for (int j = 0; j < C::PIECES; ++j) st.set(j, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-
   // this thread's chunks of a tile: row ld_row + k * STEP, chunk ld_c
   constexpr int STEP = QW * kWave / C::CPR;
   const int gt = wq * kWave + lane, ld_row = gt / C::CPR, ld_c = gt % C::CPR;
@@ -923,18 +1073,17 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   // With two buffers (in the first 64 KiB) a tile goes straight into
   // LDS, its chunks' order made by the lanes' addresses; otherwise it waits in
   // registers.
-  constexpr bool CODES = C::CACHE != kAtSame;
-  constexpr bool DIRECT = !CODES && C::NBUF == 2 && C::LDS <= 65536;
+  constexpr bool DIRECT = C::NBUF == 2 && C::LDS <= 65536;
   at_u32x4 kr[DIRECT ? 1 : C::LOADS], vr[DIRECT ? 1 : C::LOADS];
   // the entries of the next tile's pages, as read: a test here would wait for
   // them, and with them for the tile in flight
   int page[C::LOADS];
   const bool paged = p.rows.table != nullptr;
   const int32_t* const table = p.rows.table + (int64_t)b * p.rows.width;
-  const uint32_t page_bytes = (uint32_t)p.kv_heads * (uint32_t)p.rows.page_size * C::CROW;
+  const uint32_t page_bytes = (uint32_t)p.kv_heads * (uint32_t)p.rows.page_size * C::ROW;
   const int row_mask = paged ? p.rows.page_size - 1 : 0x7FFFFFFF;
   const int64_t base =
-      ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size * C::CROW;
+      ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size * C::ROW;
   const char* const kh = (const char*)p.k_cache + base;
   const char* const vh = (const char*)p.v_cache + base;
   auto row_of = [&](int t, int k) {  // the cache row that chunk k is of, clamped into the request
@@ -945,23 +1094,10 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   // once lie on one page, so its address is scalar. (The entry still comes by
   // a vector load: a scalar one would make every LDS wait a full one.)
   const bool wide = paged && p.rows.page_size >= STEP;
-  const uint32_t lane_at = (uint32_t)(ld_row * C::CROW + ld_c * 16);
+  const uint32_t lane_at = (uint32_t)(ld_row * C::ROW + ld_c * 16);
   int zero = 0;
   asm volatile("" : "+v"(zero));
-  // scales of a tile: the group's thread gt has that of K's row gt, or of V's row gt - KT
-  const bool scaler = CODES && gt < 2 * C::KT;
-  const int s_row = gt % C::KT;
-  const float* const scales =
-      CODES ? (gt < C::KT ? p.k_scale : p.v_scale) + base / C::CROW : nullptr;
-  float* const scale_to = s_scale + g * C::NBUF * 2 * C::KT + (scaler ? gt : 0);
-  int s_page = 0;
-  float s_value = 0.0f;
-  auto scale_row = [&](int t) {
-    const int r = t * C::TR + g * C::KT + s_row;
-    return r < rq.len ? r : rq.len - 1;
-  };
   auto find = [&](int t) {
-    if (scaler && paged) s_page = table[scale_row(t) >> p.rows.shift];
     if (wide) {
 #pragma unroll
       for (int k = 0; k < C::LOADS; ++k) {
@@ -977,10 +1113,6 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
     }
   };
   auto fetch = [&](int t) {
-    if (scaler) {  // (rows on no page: some row's, taken out by the mask)
-      const uint32_t pg = (uint32_t)s_page < (uint32_t)p.rows.pages && paged ? s_page : 0;
-      s_value = scales[(uint64_t)pg * (page_bytes / C::CROW) + (uint32_t)(scale_row(t) & row_mask)];
-    }
     if constexpr (DIRECT) {
       const uint32_t kt = tiles_at + (t & 1) * 2 * C::TILE;
 #pragma unroll
@@ -1010,7 +1142,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
         // (rows behind the request's last are on the page too)
         const uint64_t at =
             (uint64_t)pg * page_bytes +
-            (uint64_t)(uint32_t)((t * C::TR + g * C::KT + k * STEP) & row_mask) * C::CROW;
+            (uint64_t)(uint32_t)((t * C::TR + g * C::KT + k * STEP) & row_mask) * C::ROW;
         kr[k] = *(const at_u32x4*)(kh + at + lane_at);
         vr[k] = *(const at_u32x4*)(vh + at + lane_at);
       }
@@ -1020,7 +1152,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
         // rows on no page: some row's values, taken out by the mask
         const uint32_t pg = (uint32_t)page[k] < (uint32_t)p.rows.pages ? page[k] : 0;
         const uint64_t at = (uint64_t)pg * page_bytes +
-                            (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::CROW + ld_c * 16;
+                            (uint64_t)(uint32_t)(row_of(t, k) & row_mask) * C::ROW + ld_c * 16;
         kr[k] = *(const at_u32x4*)(kh + at);
         vr[k] = *(const at_u32x4*)(vh + at);
       }
@@ -1052,21 +1184,9 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
 #pragma unroll
     for (int k = 0; k < (DIRECT ? 0 : C::LOADS); ++k) {
       const int row = ld_row + k * STEP;
-      if constexpr (CODES) {
-        at_u32x4 x[2];
-        attn_values<H, C::CACHE>(kr[k], x);
-        *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, 2 * ld_c) * 16) = x[0];
-        *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, 2 * ld_c + 1) * 16) = x[1];
-        attn_values<H, C::CACHE>(vr[k], x);
-        *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, 2 * ld_c) * 16) = x[0];
-        *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, 2 * ld_c + 1) * 16) = x[1];
-      } else {
-        *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, ld_c) * 16) = kr[k];
-        *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, ld_c) * 16) = vr[k];
-      }
+      *(at_u32x4*)(kt + row * C::ROW + attn_k_chunk<DH>(row, ld_c) * 16) = kr[k];
+      *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, ld_c) * 16) = vr[k];
     }
-    const int s_buf = C::NBUF == 2 ? (t & 1) * 2 * C::KT : 0;
-    if (scaler) scale_to[s_buf] = gt < C::KT ? s_value * p.scale2 : s_value;
     if (QW > 1) {
       __syncthreads();
     } else {  // the tile is the wave's own: its LDS operations take effect in order
@@ -1086,9 +1206,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
         const bool held = lane < C::KT && r < rq.len && page_of(p.rows, b, r) >= 0;
         vis = attn_visible<C::KT>(p, b, rq.past, r0, i, live, __ballot(held));
       }
-      const float* const sc = s_scale + g * C::NBUF * 2 * C::KT + s_buf;
-      attn_tile<H, DH, NQ, C::KT, MASKED, C::CACHE>(kt, vt, sc, sc + C::KT, q, p.scale2, vis, st,
-                                                    lane);
+      attn_tile<H, DH, NQ, C::KT, MASKED>(kt, vt, q, p.scale2, vis, st, lane);
     }
     if (QW == 1) {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -1099,10 +1217,284 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   int t = t0;
   for (; t < tm; ++t) step(t, AttnFalse{});
   for (; t < t1; ++t) step(t, AttnTrue{});
-  st.l = attn_sum_across<NQ>(st.l);
-  if constexpr (CODES && !__is_same(H, __bf16)) {
+}
+
+// Rows of the tile that this lane's query sees, as bits: attn_visible's, for all
+// lanes alike.
+__device__ __forceinline__ uint64_t attn_visible_codes(const AttnParams& p, int64_t b, int past,
+                                                       int r0, int i, bool live, uint64_t held) {
+  const int a = past - r0;  // rows of the tile before the block
+  uint64_t v = a >= 64 ? ~0ull : (a > 0 ? (1ull << a) - 1 : 0ull);
+  if (a < 64) {  // (a is uniform)
+    if (p.mask) {
+      const uint64_t* words = p.mask + (b * p.T + (live ? i : 0)) * p.W;
+      if (a >= 0) {
+        v |= words[0] << a;
+      } else {
+        const int k = -a >> 6, s = -a & 63;
+        if (k < p.W) v |= words[k] >> s;
+        if (s && k + 1 < p.W) v |= words[k + 1] << (64 - s);
+      }
+    } else {
+      const int n = i + 1 + a;  // rows up to the query's own
+      v |= n >= 64 ? ~0ull : (n > 0 ? (1ull << (n & 63)) - 1 : 0ull);
+    }
+  }
+  return live ? v & held : 0;
+}
+
+// The same over a cache of codes. A step's codes wait in registers, two steps
+// ahead of their use where those suffice, and become values of H on their way
+// into LDS. No branch of a step depends on the lane: with nearly all registers
+// in use the compiler has moved values across such a branch's end for the lanes
+// inside it alone (zeros to be stored later came out as other numbers).
+template <typename H, class C>
+__device__ __forceinline__ void attn_steps_codes(const AttnParams& p, unsigned char* lds,
+                                                 float* s_scale, float* s_most, int* s_flag,
+                                                 int* s_any, int b,
+                                                 const AttnReq& rq, int head, int t0, int t1, int g,
+                                                 int wq, int lane, int i, bool live, bool busy,
+                                                 const at_u32x4 (&q)[C::DH * C::NQ / 512],
+                                                 AttnState<C::DH, C::NQ>& st) {
+  constexpr int DH = C::DH, NQ = C::NQ, QW = C::QW;
+  // this thread's chunks of a tile: row ld_row + k * STEP, chunk ld_c
+  constexpr int STEP = QW * kWave / C::CPR;
+  const int gt = wq * kWave + lane, ld_row = gt / C::CPR, ld_c = gt % C::CPR;
+  unsigned char* const tiles = lds + g * C::NBUF * (C::KTILE + C::TILE);
+  constexpr int DEEP = C::PREFETCH;  // tiles in flight
+  constexpr bool kUnits = !__is_same(H, __bf16);
+  at_u32x4 kr[DEEP][C::LOADS], vr[DEEP][C::LOADS];
+  // the entries of a tile's pages, read before the loads of the tile before it:
+  // waiting for them waits for nothing else
+  int page[DEEP][C::LOADS];
+  const bool paged = p.rows.table != nullptr;
+  const int32_t* const table = p.rows.table + (int64_t)b * p.rows.width;
+  const uint32_t page_rows = (uint32_t)p.kv_heads * (uint32_t)p.rows.page_size;
+  const uint32_t page_bytes = page_rows * C::CROW;
+  const int row_mask = paged ? p.rows.page_size - 1 : 0x7FFFFFFF;
+  const int64_t first = ((paged ? 0 : (int64_t)b * p.kv_heads) + head) * p.rows.page_size;
+  const char* const kh = (const char*)p.k_cache + first * C::CROW;
+  const char* const vh = (const char*)p.v_cache + first * C::CROW;
+  auto clamped = [&](int r) { return r < rq.len ? r : rq.len - 1; };
+  // (as above) pages of STEP rows or more: a load's address is scalar
+  const bool wide = paged && p.rows.page_size >= STEP;
+  const uint32_t lane_at = (uint32_t)(ld_row * C::CROW + ld_c * 16);
+  int zero = 0;
+  asm volatile("" : "+v"(zero));
+  // scales of a tile: the group's thread gt has that of K's row gt, or of V's row gt - KT
+  const bool scaler = wq * kWave < 2 * C::KT;  // whole waves
+  const int s_row = gt % C::KT;
+  const float* const scales = (gt < C::KT ? p.k_scale : p.v_scale) + first;
+  int s_page[DEEP];
+  float s_value[DEEP];
+  auto find = [&](int t, int d) {
+    const int r0 = t * C::TR + g * C::KT;
+    if (!paged) {
 #pragma unroll
-    for (int j = 0; j < C::PIECES; ++j) st.set(j, st.get(j) * st.vref);
+      for (int k = 0; k < C::LOADS; ++k) page[d][k] = 0;
+      s_page[d] = 0;
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < C::LOADS; ++k)
+      page[d][k] = wide ? table[(clamped(r0 + k * STEP) >> p.rows.shift) + zero]
+                        : table[clamped(r0 + ld_row + k * STEP) >> p.rows.shift];
+    s_page[d] = table[clamped(r0 + s_row) >> p.rows.shift];
+  };
+  auto fetch = [&](int t, int d) {
+    const int r0 = t * C::TR + g * C::KT;
+#pragma unroll
+    for (int k = 0; k < C::LOADS; ++k) {
+      // rows on no page: some row's values, taken out by the mask
+      uint64_t at;
+      if (wide) {  // (rows behind the request's last are on the page too)
+        uint32_t pg = (uint32_t)__builtin_amdgcn_readfirstlane(page[d][k]);
+        pg = pg < (uint32_t)p.rows.pages ? pg : 0;
+        at = (uint64_t)pg * page_bytes +
+             (uint64_t)(uint32_t)((r0 + k * STEP) & row_mask) * C::CROW + lane_at;
+      } else {
+        const uint32_t pg = (uint32_t)page[d][k] < (uint32_t)p.rows.pages ? page[d][k] : 0;
+        at = (uint64_t)pg * page_bytes +
+             (uint64_t)(uint32_t)(clamped(r0 + ld_row + k * STEP) & row_mask) * C::CROW + ld_c * 16;
+      }
+      kr[d][k] = *(const at_u32x4*)(kh + at);
+      vr[d][k] = *(const at_u32x4*)(vh + at);
+    }
+    if (scaler) {
+      const uint32_t pg = (uint32_t)s_page[d] < (uint32_t)p.rows.pages ? s_page[d] : 0;
+      s_value[d] =
+          scales[(uint64_t)pg * page_rows + (uint32_t)(clamped(r0 + s_row) & row_mask)];
+    }
+  };
+  // steps before tm see every row they hold
+  int tm = t0;
+  const int last = t1 - 1;
+  if (t0 < t1) {
+    find(t0, 0);
+    if (DEEP == 2) find(t0 < last ? t0 + 1 : last, DEEP - 1);
+    fetch(t0, 0);
+    find(t0 + DEEP < last ? t0 + DEEP : last, 0);
+    if (DEEP == 2) fetch(t0 < last ? t0 + 1 : last, DEEP - 1);
+    const int end = t1 * C::TR < rq.len ? t1 * C::TR : rq.len;
+    if (attn_mapped(p.rows, b, t0 * C::TR, end, s_any)) {
+      tm = (rq.past < rq.len ? rq.past : rq.len) / C::TR;
+      tm = tm < t0 ? t0 : (tm > t1 ? t1 : tm);
+    }
+  }
+  __syncthreads();  // the piece before is done with the LDS
+  auto step = [&](int t, auto number, auto is_masked) {
+    constexpr int d = decltype(number)::value;  // the step's registers
+    constexpr bool masked = decltype(is_masked)::value;
+    const int buf = C::NBUF == 1 ? 0 : (DEEP == 2 ? d : (t - t0) & 1);
+    unsigned char* const kt = tiles + buf * (C::KTILE + C::TILE);
+    unsigned char* const vt = kt + C::KTILE;
+    float* const sc = s_scale + (g * C::NBUF + buf) * 2 * C::KT;
+    int* const flag = s_flag + (g * C::NBUF + buf) * QW;
+    bool nan = false;
+#pragma unroll
+    for (int k = 0; k < C::LOADS; ++k) {
+      const int row = ld_row + k * STEP;
+      at_u32x4 x[2];
+      attn_values<H, C::CACHE>(kr[d][k], x);
+      unsigned char* const kx = kt + row * C::KROW + ld_c * 32;
+      *(at_u32x4*)kx = x[0];
+      *(at_u32x4*)(kx + 16) = x[1];
+      attn_values<H, C::CACHE>(vr[d][k], x);
+      *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, 2 * ld_c) * 16) = x[0];
+      *(at_u32x4*)(vt + row * C::ROW + attn_v_chunk<DH>(row, 2 * ld_c + 1) * 16) = x[1];
+      if (C::CACHE == kAtE4M3 && masked) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          nan |= (((vr[d][k][e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one chunk's values at a time
+    }
+    if (scaler) sc[gt] = gt < C::KT ? s_value[d] * p.scale2 : s_value[d];
+    float* const most = s_most + (g * C::NBUF + buf) * QW;
+    if (kUnits && !masked) {
+      const float x = fabsf(s_value[d]);
+      const float top = wave_max(scaler && gt >= C::KT && x < INFINITY ? x : 0.0f);
+      if (lane == 0) most[wq] = top;
+    }
+    if (C::CACHE == kAtE4M3 && masked) {
+      const uint64_t any = __ballot(nan);
+      if (lane == 0) flag[wq] = any != 0;
+    }
+    if (QW > 1) {
+      __syncthreads();
+    } else {  // the tile is the wave's own: its LDS operations take effect in order
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    // Behind the last step its tile comes again: a load that is always made
+    // leaves the compiler certain what is in flight.
+    if constexpr (DEEP == 2) {
+      find(t + 3 < last ? t + 3 : last, 1 - d);
+      fetch(t + 2 < last ? t + 2 : last, d);
+    } else if (t < last) {
+      fetch(t + 1, 0);
+      if (t + 1 < last) find(t + 2, 0);
+    }
+    if (busy) {
+      float top = 0.0f;
+      if (kUnits && !masked)
+#pragma unroll
+        for (int w = 0; w < QW; ++w) top = fmaxf(top, most[w]);
+#pragma unroll
+      for (int h = 0; h < C::KT; h += C::SK) {
+        const int r0 = t * C::TR + g * C::KT + h;
+        const unsigned char* const kh = kt + h * C::KROW;
+        const unsigned char* const vh = vt + h * C::ROW;
+        if constexpr (!masked) {
+          attn_tile_codes<H, DH, NQ, C::SK, false>(kh, vh, sc + h, sc + C::KT + h, top, false, q, 0,
+                                                   st, lane);
+        } else if (r0 < rq.len) {
+          const int r = r0 + lane;
+          bool held = (lane < C::SK) & (r < rq.len);
+          if (paged)
+            held &= (uint32_t)table[clamped(r) >> p.rows.shift] < (uint32_t)p.rows.pages;
+          const uint64_t vis =
+              attn_visible_codes(p, b, rq.past, r0, i, live, __ballot(held));
+          int scan = 0;
+          if (C::CACHE == kAtE4M3)
+#pragma unroll
+            for (int w = 0; w < QW; ++w) scan |= flag[w];
+          attn_tile_codes<H, DH, NQ, C::SK, true>(kh, vh, sc + h, sc + C::KT + h, 0.0f,
+                                                  __builtin_amdgcn_readfirstlane(scan) != 0, q, vis,
+                                                  st, lane);
+        }
+      }
+    }
+    if (QW == 1) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+  };
+  int t = t0;
+  while (t < tm) {
+    step(t++, AttnNumber<0>{}, AttnFalse{});
+    if constexpr (DEEP == 2) {
+      if (t == tm) break;
+      step(t++, AttnNumber<1>{}, AttnFalse{});
+    }
+  }
+  for (; t < t1; ++t) {
+    if (DEEP == 1 || !((t - t0) & 1))
+      step(t, AttnNumber<0>{}, AttnTrue{});
+    else if constexpr (DEEP == 2)
+      step(t, AttnNumber<1>{}, AttnTrue{});
+  }
+}
+
+// Steps [t0, t1) of unit u of request b, into the output or workspace slot
+// `slot` (-1: the output).
+template <typename H, class C, bool EXT>
+__device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* lds, float* s_scale,
+                                           float* s_most, int* s_flag, int* s_any, int b, int u,
+                                           const AttnReq& rq, int t0, int t1, int slot) {
+  constexpr int DH = C::DH, NQ = C::NQ, QW = C::QW;
+  const int tid = attn_tid(), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = wave / QW, wq = wave % QW;
+  const int head = u / rq.tiles;
+  const AttnQuery me = attn_query<NQ>(p, rq, u, wq, lane);
+  const int i = me.i;
+  const bool live = me.live;
+  const bool busy = __ballot(live) != 0;  // a wave without queries only carries rows
+  if (EXT && p.mode == kAtRest) {  // steps behind the shared rows
+    t0 += p.shared / C::TR;
+    t1 += p.shared / C::TR;
+  }
+  if (rq.len == 0) t1 = t0;
+  constexpr int NF = DH * NQ / 512;  // Q fragments of 16 bytes
+  at_u32x4 q[NF];
+  {
+    const H* src =
+        (const H*)p.q + (((int64_t)b * p.T + i) * p.q_heads + me.hq) * DH + lane / NQ * 8;
+#pragma unroll
+    for (int c = 0; c < NF; ++c)
+      q[c] = live ? *(const at_u32x4*)(src + DH / NF * c) : at_u32x4{0, 0, 0, 0};
+  }
+  AttnState<DH, NQ> st;
+  st.m = -INFINITY;
+  st.mref = st.l = 0.0f;
+  st.unit = C::CODES && !__is_same(H, __bf16) ? kAtLeastUnit : 0.0f;
+#pragma unroll
+  for (int j = 0; j < C::PIECES; ++j) st.set(j, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+
+  if constexpr (C::CODES)
+    attn_steps_codes<H, C>(p, lds, s_scale, s_most, s_flag, s_any, b, rq, head, t0, t1, g, wq, lane, i,
+                           live, busy, q, st);
+  else
+    attn_steps<H, C>(p, lds, s_any, b, rq, head, t0, t1, g, wq, lane, i, live, busy, q, st);
+  st.l = attn_sum_across<NQ>(st.l);
+  if constexpr (C::CODES && !__is_same(H, __bf16)) {
+    const float unit = __builtin_amdgcn_exp2f(st.unit);
+    st.l *= unit;
+#pragma unroll
+    for (int j = 0; j < C::PIECES; ++j) st.set(j, st.get(j) * unit);
   }
   const int out_lane = attn_tid() & 63;
 
@@ -1225,7 +1617,7 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
         }
         mark = AttnPlace{(int)(e - k), at.b, at.u, rq.rows, rq.waves, rq.tiles, {0, 0}};
       }
-      attn_piece<H, C, EXT>(p, sh.tiles, sh.scale, sh.any, at.b, at.u, rq, at.s, t1,
+      attn_piece<H, C, EXT>(p, sh.tiles, sh.scale, sh.most, sh.flag, sh.any, at.b, at.u, rq, at.s, t1,
                             begins && ends ? -1 : 2 * k + (begins ? 1 : 0));
       if (ends && (at.u + 1) % rq.tiles == 0 && rq.rows < p.T)
         attn_clear<H, DH>(p, at.b, rq.rows, at.u / rq.tiles);

@@ -146,6 +146,7 @@ struct AttnParams {
   float* pre_o;               // [batch][T][q_heads][head_dim], divided by the sums
   float* pre_ml;              // [batch][T][q_heads][2]: maximum (log2) and sum
   int32_t shared;             // *prefix, in the kernel
+  int32_t few;  // EXT: at most kAtThreads requests, all their steps counted in 31 bits
 };
 
 enum { kAtAlone, kAtPrefix, kAtRest };
@@ -158,32 +159,36 @@ struct AttnReq {
   int past, rows, len, steps, waves, tiles;
 };
 
+// The rest of a request, from its past and rows.
+template <class C, bool EXT>
+__device__ __forceinline__ void attn_request_sizes(const AttnParams& p, AttnReq& r) {
+  const int64_t n = (int64_t)r.past + (EXT && p.mode == kAtPrefix ? 0 : r.rows);
+  r.len = r.past < 0 ? 0 : (int)(n < p.rows.cap ? n : p.rows.cap);
+  // one step for an empty request: its rows are cleared
+  r.steps = r.len > C::TR ? (r.len + C::TR - 1) / C::TR : 1;
+  if (EXT && p.mode == kAtRest) {  // (len >= shared where a request has rows)
+    r.steps -= p.shared / C::TR;
+    r.steps = r.steps > 1 ? r.steps : 1;
+  }
+  r.waves = (r.rows * p.G + C::NQ - 1) / C::NQ;
+  r.tiles = r.waves > C::QW ? (r.waves + C::QW - 1) / C::QW : 1;
+}
+
 template <class C, bool EXT>
 __device__ __forceinline__ AttnReq attn_request(const AttnParams& p, int64_t b) {
   static_assert(kAtShare % C::TR == 0, "shared rows are whole steps");
   AttnReq r;
   if (EXT && p.mode == kAtPrefix) {
-    r.past = r.len = p.shared;
+    r.past = p.shared;
     r.rows = p.T;
-    r.steps = r.len / C::TR;
-    r.waves = (r.rows * p.G + C::NQ - 1) / C::NQ;
-    r.tiles = (r.waves + C::QW - 1) / C::QW;
+    attn_request_sizes<C, EXT>(p, r);
     return r;
   }
   r.past = p.past_len[b];
   int nodes = p.num_nodes ? p.num_nodes[b] : p.T - 1;
   nodes = nodes < 0 ? 0 : (nodes > p.T - 1 ? p.T - 1 : nodes);
   r.rows = r.past < 0 ? 0 : nodes + 1;
-  const int64_t n = (int64_t)r.past + r.rows;
-  r.len = r.past < 0 ? 0 : (int)(n < p.rows.cap ? n : p.rows.cap);
-  // one step for an empty request: its rows are cleared
-  r.steps = r.len > C::TR ? (r.len + C::TR - 1) / C::TR : 1;
-  if (EXT) {  // (len >= shared where a request has rows)
-    r.steps -= p.shared / C::TR;
-    r.steps = r.steps > 1 ? r.steps : 1;
-  }
-  r.waves = (r.rows * p.G + C::NQ - 1) / C::NQ;
-  r.tiles = r.waves > C::QW ? (r.waves + C::QW - 1) / C::QW : 1;
+  attn_request_sizes<C, EXT>(p, r);
   return r;
 }
 
@@ -212,14 +217,25 @@ struct AttnScratch {
   AttnPos pos[2];
 };
 
+// attn_plan_few's.
+struct AttnFew {
+  int part[2][kAtWaves][2];
+  int longest[kAtWaves];
+  alignas(16) int steps[kAtThreads];
+  int past[kAtThreads], rows[kAtThreads], order[kAtThreads], units[kAtThreads];
+  AttnPos pos[2];
+  int b, i;
+};
+
 // A workgroup's shared memory, all of it in one object, so that the tiles lie
 // at its start: loads straight into LDS go to the 64 KiB that m0's 16 bits
 // reach, which the tiles may fill.
-template <class C>
+template <class C, bool EXT>
 struct AttnLds {
   alignas(256) unsigned char tiles[C::LDS];
   int any[kAtWaves];
   AttnScratch plan;
+  alignas(16) unsigned char few[EXT ? sizeof(AttnFew) : 1];
   alignas(16) float scale[C::SCALES ? C::SCALES : 1];  // [NG][NBUF]: K's times scale2, then V's
   // [NG][NBUF][QW]: of what a wave staged, the largest scale of V; NaN codes of V
   alignas(16) float most[C::CODES ? kAtWaves * C::NBUF : 1];
@@ -370,6 +386,134 @@ __device__ bool attn_plan(const AttnParams& p, AttnScratch& sh, int w, int& k, A
     from = attn_uniform(sh.pos[0]);
     to = attn_uniform(sh.pos[1]);
   }
+  return true;
+}
+
+// Inclusive sum over the wave of one 32-bit number per lane, by DPP moves.
+__device__ __forceinline__ int attn_wave_sum(int x) {
+  x += (int)dpp_u32<0x111>((uint32_t)x);  // row_shr:1, 2, 4, 8
+  x += (int)dpp_u32<0x112>((uint32_t)x);
+  x += (int)dpp_u32<0x114>((uint32_t)x);
+  x += (int)dpp_u32<0x118>((uint32_t)x);
+  // the rows' totals: lane 15 to row 1 and lane 47 to row 3, lane 31 to rows 2 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
+}
+
+// attn_plan for at most kAtThreads requests whose steps are counted in 31 bits:
+// a thread holds a request, whose lengths are read once.
+//
+// The cut is attn_plan's. Whole units go to the workgroups of one XCD after the
+// other: key/value head h of request b is the work of XCD (b * kv_heads + h) % 8,
+// which reads its rows once for all its query tiles, and each XCD's longest
+// requests come first, so that the card runs dry at once. (64 trees of 129
+// rows over 1 to 2 k rows, a request's heads on one XCD and in the requests'
+// order: of 334 us a fifth passed with workgroups ending one by one.)
+template <class C>
+__device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, AttnCut& cut,
+                              AttnPos& from, AttnPos& to, AttnReq& rq) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, batch = (int)p.batch;
+  AttnReq r;
+  r.past = r.rows = r.steps = 0;
+  r.tiles = 1;
+  int units = 0;
+  if (tid < batch) {
+    r = attn_request<C, true>(p, tid);
+    units = r.tiles * p.kv_heads;
+  }
+  const int mine = units * r.steps;
+  const int steps_to = attn_wave_sum(mine), units_to = attn_wave_sum(units);
+  const int longest_here = wave_max(r.steps);
+  sh.steps[tid] = r.steps;
+  sh.past[tid] = r.past;
+  sh.rows[tid] = r.rows;
+  if (lane == 63) {
+    sh.part[0][wave][0] = steps_to;
+    sh.part[0][wave][1] = units_to;
+    sh.longest[wave] = longest_here;
+  }
+  __syncthreads();
+  int total = 0, all_units = 0, longest = 0, before = steps_to - mine;
+#pragma unroll
+  for (int i = 0; i < kAtWaves; ++i) {
+    before += i < wave ? sh.part[0][i][0] : 0;
+    total += sh.part[0][i][0];
+    all_units += sh.part[0][i][1];
+    longest = sh.longest[i] > longest ? sh.longest[i] : longest;
+  }
+  const bool whole = all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
+  if (!whole) {
+    const int want = (int)(((int64_t)total + p.least - 1) / p.least);
+    const int n = want < p.groups ? want : p.groups;
+    const int per = (n + 7) >> 3;
+    k = w;
+    if ((w >> 3) >= per) return false;
+    k = (w & 7) * per + (w >> 3);
+    if (k >= n) return false;
+    cut.n = n;
+    cut.total = total;
+    cut.range = total / n;
+    cut.extra = total - (int)cut.range * n;
+    cut.slack = cut.range < 8 ? cut.range >> 1 : cut.range >> 3;
+    const int x0 = (int)attn_end(cut, k), x1 = (int)attn_end(cut, k + 1);
+    auto place = [&](int e, int x, AttnPos& at) {
+      x -= before;
+      int u = (int)((uint32_t)x / (uint32_t)r.steps), s = x - u * r.steps;
+      if (e > 0 && e < n) s = (int)attn_near(cut, s, r.steps);
+      at.x = (int64_t)before + u * r.steps + s;
+      at.b = tid;
+      at.u = u + (s == r.steps);
+      at.s = s == r.steps ? 0 : s;
+    };
+    if (x0 >= before && x0 < before + mine) place(k, x0, sh.pos[0]);
+    if (x1 > before && x1 <= before + mine) place(k + 1, x1, sh.pos[1]);
+    __syncthreads();
+    from = attn_uniform(sh.pos[0]);
+    to = attn_uniform(sh.pos[1]);
+  } else {
+    // requests by their steps, the longest first
+    int rank = 0;
+    for (int j = 0; j < batch; j += 4) {
+      const int4 other = *(const int4*)(sh.steps + j);
+      rank += (other.x > r.steps) | ((other.x == r.steps) & (j < tid));
+      rank += (other.y > r.steps) | ((other.y == r.steps) & (j + 1 < tid));
+      rank += (other.z > r.steps) | ((other.z == r.steps) & (j + 2 < tid));
+      rank += (other.w > r.steps) | ((other.w == r.steps) & (j + 3 < tid));
+    }
+    // (threads without a request have no steps, requests one at least)
+    const int xcd = w & 7, h0 = (xcd - tid * p.kv_heads) & 7;
+    sh.order[rank] = tid;
+    sh.units[rank] =
+        tid < batch && h0 < p.kv_heads ? ((p.kv_heads - 1 - h0) / 8 + 1) * r.tiles : 0;
+    if (tid == 0) sh.b = -1;
+    __syncthreads();
+    const int have = tid < batch ? sh.units[tid] : 0, to_here = attn_wave_sum(have);
+    if (lane == 63) sh.part[1][wave][0] = to_here;
+    __syncthreads();
+    int first = to_here - have;
+#pragma unroll
+    for (int i = 0; i < kAtWaves; ++i) first += i < wave ? sh.part[1][i][0] : 0;
+    const int i = w >> 3;
+    if (i >= first && i < first + have) {
+      sh.b = sh.order[tid];
+      sh.i = i - first;
+    }
+    __syncthreads();
+    k = w;
+    const int b = __builtin_amdgcn_readfirstlane(sh.b);
+    if (b < 0) return false;
+    rq.past = sh.past[b];
+    rq.rows = sh.rows[b];
+    attn_request_sizes<C, true>(p, rq);
+    const int at = __builtin_amdgcn_readfirstlane(sh.i), group = at / rq.tiles;
+    const int head = ((xcd - b * p.kv_heads) & 7) + 8 * group;
+    from = AttnPos{-1, b, head * rq.tiles + (at - group * rq.tiles), 0};
+    to = AttnPos{-1, b, from.u + 1, 0};
+  }
+  rq.past = __builtin_amdgcn_readfirstlane(sh.past[from.b]);
+  rq.rows = __builtin_amdgcn_readfirstlane(sh.rows[from.b]);
+  attn_request_sizes<C, true>(p, rq);
   return true;
 }
 
@@ -1330,13 +1474,28 @@ __device__ __forceinline__ void attn_steps_codes(const AttnParams& p, unsigned c
   int tm = t0;
   const int last = t1 - 1;
   if (t0 < t1) {
+    // whether all rows' pages are the pool's: the entries are read before the
+    // first tile's, so that nothing waits for them alone
+    const int end = t1 * C::TR < rq.len ? t1 * C::TR : rq.len;
+    const int pages = ((end - 1) >> p.rows.shift) - (t0 * C::TR >> p.rows.shift) + 1;
+    const int32_t* const entries = table + (t0 * C::TR >> p.rows.shift);
+    const int at = (int)threadIdx.x < pages ? (int)threadIdx.x : pages - 1;
+    const int entry = paged && pages > 0 ? entries[at] : 0;
     find(t0, 0);
     if (DEEP == 2) find(t0 < last ? t0 + 1 : last, DEEP - 1);
     fetch(t0, 0);
     find(t0 + DEEP < last ? t0 + DEEP : last, 0);
     if (DEEP == 2) fetch(t0 < last ? t0 + 1 : last, DEEP - 1);
-    const int end = t1 * C::TR < rq.len ? t1 * C::TR : rq.len;
-    if (attn_mapped(p.rows, b, t0 * C::TR, end, s_any)) {
+    bool hole = (uint32_t)entry >= (uint32_t)p.rows.pages;
+    if (paged)
+      for (int e = kAtThreads; e < pages; e += kAtThreads) {  // uniform
+        const int next = e + (int)threadIdx.x;
+        hole |= (uint32_t)entries[next < pages ? next : pages - 1] >= (uint32_t)p.rows.pages;
+      }
+    const uint64_t any = __ballot(hole);
+    if (lane == 0) s_any[threadIdx.x >> 6] = any != 0;
+    __syncthreads();
+    if (!(s_any[0] | s_any[1] | s_any[2] | s_any[3])) {
       tm = (rq.past < rq.len ? rq.past : rq.len) / C::TR;
       tm = tm < t0 ? t0 : (tm > t1 ? t1 : tm);
     }
@@ -1572,8 +1731,9 @@ __device__ __forceinline__ int attn_shared(const AttnParams& p, AttnScratch& sh,
 template <typename H, int DH, int NQ, int QW, int CACHE = kAtSame, bool EXT = false>
 __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(AttnParams p) {
   using C = AttnTile<DH, NQ, QW, CACHE>;
-  __shared__ AttnLds<C> sh;
-  static_assert(offsetof(AttnLds<C>, tiles) == 0, "the tiles at LDS address 0");
+  using Lds = AttnLds<C, EXT>;
+  __shared__ Lds sh;
+  static_assert(offsetof(Lds, tiles) == 0, "the tiles at LDS address 0");
   AttnPos at, to;
   const int id = (int)blockIdx.x;
   AttnPlace mark{};
@@ -1592,9 +1752,16 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
       p.shared = __builtin_amdgcn_readfirstlane(*p.prefix);
     }
   }
-  if (some && attn_plan<C, EXT>(p, sh.plan, id, k, cut, at, to)) {
+  AttnReq rq;
+  bool mine = some;
+  if (EXT && p.few) {
+    mine = some && attn_plan_few<C>(p, *(AttnFew*)sh.few, id, k, cut, at, to, rq);
+  } else if (some) {
+    mine = attn_plan<C, EXT>(p, sh.plan, id, k, cut, at, to);
+    if (mine) rq = attn_request<C, EXT>(p, at.b);
+  }
+  if (mine) {
     const bool whole = to.x < 0;
-    AttnReq rq = attn_request<C, EXT>(p, at.b);
     do {  // uniform; no stretch is empty but for ends moved onto one another
       if (!whole && at.x >= to.x) break;
       if (at.u == rq.tiles * p.kv_heads) {  // on to the next request
@@ -1635,14 +1802,13 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
 // through as many CUs as there are; four pieces to a wave against two: 5.0 and
 // 4.0 us for one tree, 11.3 and 8.9 for 24 units in 512 pieces, 5.0 and 5.9 for
 // the 64 trees, where it finds nothing to merge).
-template <typename H, int DH, int NQ, int QW, int CACHE = kAtSame, bool EXT = false>
+template <typename H, int DH, int NQ, int QW>
 __global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
-  using C = AttnTile<DH, NQ, QW, CACHE>;
+  using C = AttnTile<DH, NQ, QW>;
   constexpr int PP = kAtMerge, PER = C::PIECES / PP;  // waves of a state
   const int k = (int)(blockIdx.x / (QW * PER)), r = (int)(blockIdx.x % (QW * PER));
   const AttnPlace pl = p.place[k];
   if (pl.pieces == 0) return;
-  if (EXT && p.mode == kAtRest) p.shared = *p.prefix;
   const int lane = threadIdx.x, wq = r / PER, j0 = PP * (r % PER);
   AttnReq rq;
   rq.rows = pl.rows;
@@ -1668,8 +1834,62 @@ __global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
     for (int j = 0; j < PP; ++j) o[j] = o[j] * a + part[j * kWave] * b;
   }
   if (me.live)
-    attn_store<H, DH, NQ, PP, EXT>(p, ((int64_t)pl.b * p.T + me.i) * p.q_heads + me.hq, j0, m, l,
-                                   o, lane);
+    attn_store<H, DH, NQ, PP, false>(p, ((int64_t)pl.b * p.T + me.i) * p.q_heads + me.hq, j0, m, l,
+                                     o, lane);
+}
+
+// The same with four waves to a state's part, each of every fourth piece, whose
+// results are joined in LDS: shared rows leave few units in many pieces (16
+// units of 128 queries in 512 pieces: 20.2 us with one wave, ... with four).
+template <typename H, int DH, int NQ, int QW, int CACHE>
+__global__ __launch_bounds__(kAtThreads) void attn_merge_many_kernel(AttnParams p) {
+  using C = AttnTile<DH, NQ, QW, CACHE>;
+  constexpr int PP = kAtMerge, PER = C::PIECES / PP;  // workgroups of a state
+  __shared__ at_f32x4 s_o[kAtWaves][PP][kWave];
+  __shared__ float2 s_ml[kAtWaves][kWave];
+  const int k = (int)(blockIdx.x / (QW * PER)), r = (int)(blockIdx.x % (QW * PER));
+  const AttnPlace pl = p.place[k];
+  if (pl.pieces == 0) return;
+  if (p.mode == kAtRest) p.shared = *p.prefix;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wq = r / PER, j0 = PP * (r % PER);
+  AttnReq rq;
+  rq.rows = pl.rows;
+  rq.waves = pl.waves;
+  rq.tiles = pl.tiles;
+  const AttnQuery me = attn_query<NQ>(p, rq, pl.u, wq, lane);
+  if (!__ballot(me.live)) return;  // all waves alike
+  float m = -INFINITY, l = 0.0f;
+  at_f32x4 o[PP];
+#pragma unroll
+  for (int j = 0; j < PP; ++j) o[j] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto join = [&](float2 ml, const at_f32x4* part, int step) {
+    const float top = fmaxf(m, ml.x);
+    const float a = m > -INFINITY ? __builtin_amdgcn_exp2f(m - top) : 0.0f;
+    const float b = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - top) : 0.0f;
+    m = top;
+    l = l * a + ml.y * b;
+#pragma unroll
+    for (int j = 0; j < PP; ++j) o[j] = o[j] * a + part[j * step] * b;
+  };
+#pragma unroll 4
+  for (int s = wave; s < pl.pieces; s += kAtWaves) {
+    const int64_t at = (int64_t)(s == 0 ? 2 * k + 1 : 2 * (k + s)) * QW + wq;
+    join(*(const float2*)(p.part_ml + (at * kWave + lane) * 2),
+         (const at_f32x4*)p.part + (at * C::PIECES + j0) * kWave + lane, kWave);
+  }
+  if (pl.pieces > 1) {
+    s_ml[wave][lane] = float2{m, l};
+#pragma unroll
+    for (int j = 0; j < PP; ++j) s_o[wave][j][lane] = o[j];
+    __syncthreads();
+    if (wave > 0) return;
+    for (int s = 1; s < kAtWaves && s < pl.pieces; ++s) join(s_ml[s][lane], &s_o[s][0][lane], kWave);
+  } else if (wave > 0) {
+    return;
+  }
+  if (me.live)
+    attn_store<H, DH, NQ, PP, true>(p, ((int64_t)pl.b * p.T + me.i) * p.q_heads + me.hq, j0, m, l,
+                                    o, lane);
 }
 
 }  // namespace ddt

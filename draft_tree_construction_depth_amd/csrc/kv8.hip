@@ -94,6 +94,9 @@ void set_work(ddt::AttnParams& ap, const AttnPlan& pl, char* at) {
   ap.place = (ddt::AttnPlace*)at;
   ap.part = (float*)(at + pl.part);
   ap.part_ml = (float*)(at + pl.ml);
+  // every tile has 32 rows or more to a step
+  const int64_t most = ap.rows.cap / 32 + 1, M = (int64_t)ap.T * ap.G / 16 + 1;
+  ap.few = ap.batch <= ddt::kAtThreads && ap.batch * ap.kv_heads <= 0x7FFFFFFFLL / M / most;
 }
 
 typedef int (*AttnLaunch)(const ddt::AttnParams&, const AttnPlan&, int, int, hipStream_t);

@@ -78,8 +78,9 @@ inline AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_
                            : batch * kv_heads * tiles * steps;
   const int64_t want = ((axis + pl.least - 1) / pl.least + 7) & ~(int64_t)7;
   if (want < pl.groups) pl.groups = want;
-  // or one for each unit, where there are many (attn_plan decides)
-  const int64_t units = (batch * kv_heads * tiles + 7) & ~(int64_t)7;
+  // or one for each unit, where there are many (attn_plan decides); the XCDs
+  // may have one key/value head of a request more or less
+  const int64_t units = ((batch * kv_heads + 7) & ~(int64_t)7) * tiles;
   pl.grid = units >= 2 * pl.groups ? units : pl.groups;
   pl.merge = steps > 1;
   const int64_t slots = pl.merge ? 2 * pl.groups : 0;
@@ -99,8 +100,12 @@ int launch_attn_tile(const AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   if (!pl.merge) return DDT_OK;
   const int64_t merges = pl.groups * QW * AttnTile<DH, NQ, QW>::PIECES / kAtMerge;
-  hipLaunchKernelGGL((attn_merge_kernel<H, DH, NQ, QW, CACHE, EXT>), dim3((unsigned)merges),
-                     dim3(kWave), 0, st, ap);
+  if constexpr (EXT)
+    hipLaunchKernelGGL((attn_merge_many_kernel<H, DH, NQ, QW, CACHE>), dim3((unsigned)merges),
+                       dim3(kAtThreads), 0, st, ap);
+  else
+    hipLaunchKernelGGL((attn_merge_kernel<H, DH, NQ, QW>), dim3((unsigned)merges), dim3(kWave), 0,
+                       st, ap);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
 }
 

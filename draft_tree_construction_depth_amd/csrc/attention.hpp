@@ -112,7 +112,8 @@ struct AttnTile {
 struct AttnPlace {
   int32_t pieces, b, u;
   int32_t rows, waves, tiles;  // of AttnReq
-  int32_t pad[2];
+  int32_t k;  // EXT: the stretch that begins it
+  int32_t pad;
 };
 
 struct AttnParams {
@@ -147,6 +148,9 @@ struct AttnParams {
   float* pre_ml;              // [batch][T][q_heads][2]: maximum (log2) and sum
   int32_t shared;             // *prefix, in the kernel
   int32_t few;  // EXT: at most kAtThreads requests, all their steps counted in 31 bits
+  // EXT: `place` has an entry for each unit if by_unit (of as many as
+  // place[places].pieces says), else for each workgroup
+  int32_t places, by_unit;
 };
 
 enum { kAtAlone, kAtPrefix, kAtRest };
@@ -225,6 +229,7 @@ struct AttnFew {
   int past[kAtThreads], rows[kAtThreads], order[kAtThreads], units[kAtThreads];
   AttnPos pos[2];
   int b, i;
+  int unit;  // units of requests before the first position's
 };
 
 // A workgroup's shared memory, all of it in one object, so that the tiles lie
@@ -412,7 +417,7 @@ __device__ __forceinline__ int attn_wave_sum(int x) {
 // order: of 334 us a fifth passed with workgroups ending one by one.)
 template <class C>
 __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, AttnCut& cut,
-                              AttnPos& from, AttnPos& to, AttnReq& rq) {
+                              AttnPos& from, AttnPos& to, AttnReq& rq, int& unit, int& all_units) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, batch = (int)p.batch;
   AttnReq r;
   r.past = r.rows = r.steps = 0;
@@ -434,10 +439,13 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     sh.longest[wave] = longest_here;
   }
   __syncthreads();
-  int total = 0, all_units = 0, longest = 0, before = steps_to - mine;
+  int total = 0, longest = 0, before = steps_to - mine;
+  all_units = 0;
+  int units_before = units_to - units;
 #pragma unroll
   for (int i = 0; i < kAtWaves; ++i) {
     before += i < wave ? sh.part[0][i][0] : 0;
+    units_before += i < wave ? sh.part[0][i][1] : 0;
     total += sh.part[0][i][0];
     all_units += sh.part[0][i][1];
     longest = sh.longest[i] > longest ? sh.longest[i] : longest;
@@ -455,7 +463,9 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     cut.total = total;
     cut.range = total / n;
     cut.extra = total - (int)cut.range * n;
-    cut.slack = cut.range < 8 ? cut.range >> 1 : cut.range >> 3;
+    // (a step at least: 64 requests of 4 to 9 steps behind shared rows, 6.5 to a
+    // stretch, 66 us with half a stretch to either side and 60 with one step)
+    cut.slack = cut.range < 4 ? cut.range >> 1 : (cut.range < 8 ? 1 : cut.range >> 3);
     const int x0 = (int)attn_end(cut, k), x1 = (int)attn_end(cut, k + 1);
     auto place = [&](int e, int x, AttnPos& at) {
       x -= before;
@@ -466,11 +476,15 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
       at.u = u + (s == r.steps);
       at.s = s == r.steps ? 0 : s;
     };
-    if (x0 >= before && x0 < before + mine) place(k, x0, sh.pos[0]);
+    if (x0 >= before && x0 < before + mine) {
+      place(k, x0, sh.pos[0]);
+      sh.unit = units_before;
+    }
     if (x1 > before && x1 <= before + mine) place(k + 1, x1, sh.pos[1]);
     __syncthreads();
     from = attn_uniform(sh.pos[0]);
     to = attn_uniform(sh.pos[1]);
+    unit = __builtin_amdgcn_readfirstlane(sh.unit);
   } else {
     // requests by their steps, the longest first
     int rank = 0;
@@ -1501,9 +1515,17 @@ __device__ __forceinline__ void attn_steps_codes(const AttnParams& p, unsigned c
     }
   }
   __syncthreads();  // the piece before is done with the LDS
+  // A CU's older workgroup comes before its younger one wherever both could go
+  // on, and ends a fifth earlier: they take turns (long chains 118 -> 114 us,
+  // chains behind shared rows 132 -> 126).
+  const int turn = (int)(blockIdx.x >> 8);
   auto step = [&](int t, auto number, auto is_masked) {
     constexpr int d = decltype(number)::value;  // the step's registers
     constexpr bool masked = decltype(is_masked)::value;
+    if ((t ^ turn) & 1)
+      __builtin_amdgcn_s_setprio(1);
+    else
+      __builtin_amdgcn_s_setprio(0);
     const int buf = C::NBUF == 1 ? 0 : (DEEP == 2 ? d : (t - t0) & 1);
     unsigned char* const kt = tiles + buf * (C::KTILE + C::TILE);
     unsigned char* const vt = kt + C::KTILE;
@@ -1754,8 +1776,10 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
   }
   AttnReq rq;
   bool mine = some;
+  int unit = 0, units = 0;  // of the requests before at.b, of all
   if (EXT && p.few) {
-    mine = some && attn_plan_few<C>(p, *(AttnFew*)sh.few, id, k, cut, at, to, rq);
+    mine = some && attn_plan_few<C>(p, *(AttnFew*)sh.few, id, k, cut, at, to, rq, unit,
+                                         units);
   } else if (some) {
     mine = attn_plan<C, EXT>(p, sh.plan, id, k, cut, at, to);
     if (mine) rq = attn_request<C, EXT>(p, at.b);
@@ -1765,6 +1789,7 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
     do {  // uniform; no stretch is empty but for ends moved onto one another
       if (!whole && at.x >= to.x) break;
       if (at.u == rq.tiles * p.kv_heads) {  // on to the next request
+        unit += at.u;
         ++at.b;
         at.u = 0;
         rq = attn_request<C, EXT>(p, at.b);
@@ -1782,8 +1807,10 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
           if (s >= rq.steps || attn_near(cut, s, rq.steps) == rq.steps) break;
           ++e;
         }
-        mark = AttnPlace{(int)(e - k), at.b, at.u, rq.rows, rq.waves, rq.tiles, {0, 0}};
+        mark = AttnPlace{(int)(e - k), at.b, at.u, rq.rows, rq.waves, rq.tiles, k, 0};
       }
+      if (EXT && p.by_unit && begins && !whole && threadIdx.x == 0)
+        p.place[unit + at.u] = ends ? AttnPlace{} : mark;
       attn_piece<H, C, EXT>(p, sh.tiles, sh.scale, sh.most, sh.flag, sh.any, at.b, at.u, rq, at.s, t1,
                             begins && ends ? -1 : 2 * k + (begins ? 1 : 0));
       if (ends && (at.u + 1) % rq.tiles == 0 && rq.rows < p.T)
@@ -1793,7 +1820,12 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
       ++at.u;
     } while (!whole);
   }
-  if (threadIdx.x == 0 && k < p.groups) p.place[k] = mark;
+  if (EXT && p.by_unit) {
+    // (without shared rows to attend to, or dealt out whole, no unit is cut)
+    if (id == 0 && threadIdx.x == 0) p.place[p.places].pieces = mine && to.x >= 0 ? units : 0;
+  } else if (threadIdx.x == 0 && k < p.groups) {
+    p.place[k] = mark;
+  }
 }
 
 // Merges the pieces of the unit that a workgroup's stretch began and did not
@@ -1847,9 +1879,11 @@ __global__ __launch_bounds__(kAtThreads) void attn_merge_many_kernel(AttnParams 
   constexpr int PP = kAtMerge, PER = C::PIECES / PP;  // workgroups of a state
   __shared__ at_f32x4 s_o[kAtWaves][PP][kWave];
   __shared__ float2 s_ml[kAtWaves][kWave];
-  const int k = (int)(blockIdx.x / (QW * PER)), r = (int)(blockIdx.x % (QW * PER));
-  const AttnPlace pl = p.place[k];
+  const int id = (int)(blockIdx.x / (QW * PER)), r = (int)(blockIdx.x % (QW * PER));
+  if (p.by_unit && id >= p.place[p.places].pieces) return;
+  const AttnPlace pl = p.place[id];
   if (pl.pieces == 0) return;
+  const int k = pl.k;
   if (p.mode == kAtRest) p.shared = *p.prefix;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wq = r / PER, j0 = PP * (r % PER);
   AttnReq rq;

@@ -97,6 +97,8 @@ void set_work(ddt::AttnParams& ap, const AttnPlan& pl, char* at) {
   // every tile has 32 rows or more to a step
   const int64_t most = ap.rows.cap / 32 + 1, M = (int64_t)ap.T * ap.G / 16 + 1;
   ap.few = ap.batch <= ddt::kAtThreads && ap.batch * ap.kv_heads <= 0x7FFFFFFFLL / M / most;
+  ap.by_unit = ap.few && pl.units <= pl.groups;
+  ap.places = (int32_t)(ap.by_unit ? pl.units : pl.groups);
 }
 
 typedef int (*AttnLaunch)(const ddt::AttnParams&, const AttnPlan&, int, int, hipStream_t);

@@ -44,6 +44,7 @@ inline bool valid_half(int dtype) { return dtype == DDT_BF16 || dtype == DDT_F16
 struct AttnPlan {
   int NQ, QW;  // queries of a wave, waves side by side
   int64_t groups, least, grid;
+  int64_t units;  // no call has more
   bool merge;  // a unit can be cut
   size_t part, ml, end;
 };
@@ -81,10 +82,11 @@ inline AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_
   // or one for each unit, where there are many (attn_plan decides); the XCDs
   // may have one key/value head of a request more or less
   const int64_t units = ((batch * kv_heads + 7) & ~(int64_t)7) * tiles;
+  pl.units = units;
   pl.grid = units >= 2 * pl.groups ? units : pl.groups;
   pl.merge = steps > 1;
   const int64_t slots = pl.merge ? 2 * pl.groups : 0;
-  size_t o = align_up((size_t)pl.groups * sizeof(AttnPlace));
+  size_t o = align_up((size_t)(pl.groups + 1) * sizeof(AttnPlace));
   pl.part = o;
   o = align_up(o + (size_t)slots * pl.QW * pl.NQ * head_dim * sizeof(float));
   pl.ml = o;
@@ -99,7 +101,7 @@ int launch_attn_tile(const AttnParams& ap, const AttnPlan& pl, hipStream_t st) {
                      dim3(kAtThreads), 0, st, ap);
   if (hipGetLastError() != hipSuccess) return DDT_EHIP;
   if (!pl.merge) return DDT_OK;
-  const int64_t merges = pl.groups * QW * AttnTile<DH, NQ, QW>::PIECES / kAtMerge;
+  const int64_t merges = (EXT ? ap.places : pl.groups) * QW * AttnTile<DH, NQ, QW>::PIECES / kAtMerge;
   if constexpr (EXT)
     hipLaunchKernelGGL((attn_merge_many_kernel<H, DH, NQ, QW, CACHE>), dim3((unsigned)merges),
                        dim3(kAtThreads), 0, st, ap);

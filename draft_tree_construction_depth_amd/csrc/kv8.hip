@@ -295,10 +295,10 @@ int ddtree_compact_kv8(void* k_cache, void* v_cache, float* k_scale, float* v_sc
   kp.L = L;
   kp.new_len = new_len;
   if (head_dim % 16 == 0)
-    hipLaunchKernelGGL(ddt::compact8_kernel<uint4>, dim3((unsigned)blocks), dim3(ddt::kK8Threads),
+    hipLaunchKernelGGL(ddt::compact8_kernel<ddt::k8_u32x4>, dim3((unsigned)blocks), dim3(ddt::kK8Threads),
                        0, stream, kp);
   else
-    hipLaunchKernelGGL(ddt::compact8_kernel<uint2>, dim3((unsigned)blocks), dim3(ddt::kK8Threads),
+    hipLaunchKernelGGL(ddt::compact8_kernel<ddt::k8_u32x2>, dim3((unsigned)blocks), dim3(ddt::kK8Threads),
                        0, stream, kp);
   return hipGetLastError() == hipSuccess ? DDT_OK : DDT_EHIP;
 }

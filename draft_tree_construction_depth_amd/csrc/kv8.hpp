@@ -214,6 +214,9 @@ struct Kv8CompactParams {
   int32_t* new_len;  // [batch], may be null
 };
 
+typedef unsigned int k8_u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int k8_u32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kK8Threads = 256;
 constexpr int kK8Batch = 8;     // load groups held in registers per batch
 constexpr int kK8MaxRows = 32;  // DDT_MAX_L
@@ -259,54 +262,53 @@ __global__ __launch_bounds__(kK8Threads) void compact8_kernel(Kv8CompactParams p
   const int64_t first = (int64_t)part * p.each;
   const int slices = (int)(first + p.each < all ? p.each : all - first);
   const int64_t layer_rows = p.rows.pages * p.heads * p.rows.page_size;
-  // rows of slice number `first + i` before its page's first
-  auto slice_row = [&](int i) -> int64_t {
-    const int64_t layer = (first + i) / p.heads;
-    return layer * layer_rows + ((first + i) - layer * p.heads) * p.rows.page_size;
-  };
+  int head = (int)(first % p.heads);
+  int64_t at = first / p.heads * layer_rows + (int64_t)head * p.rows.page_size;  // the slice's row 0
   // scales: lane l moves row l % 32 of K or, from lane 32 on, of V
-  for (int i0 = 0; i0 < slices; i0 += kK8Batch) {  // uniform
-    float x[kK8Batch];
-    float* const scale = lane < 32 ? p.k_scale : p.v_scale;
-    const int i = lane & 31;
-    const bool on = i < n && s_from[w][i & 31] >= 0;
-#pragma unroll
-    for (int k = 0; k < kK8Batch; ++k)
-      if (on && i0 + k < slices) x[k] = scale[slice_row(i0 + k) + s_from[w][i]];
-#pragma unroll
-    for (int k = 0; k < kK8Batch; ++k)
-      if (on && i0 + k < slices) scale[slice_row(i0 + k) + s_to[w][i]] = x[k];
-  }
+  float* const scale = lane < 32 ? p.k_scale : p.v_scale;
+  const int si = lane & 31;
+  const int64_t s_src = si < n ? s_from[w][si] : -1, s_dst = s_to[w][si < n ? si : 0];
   const int lpr = p.row_bytes / (int)sizeof(V);  // lanes per row
   const int rpi = kWave / lpr;                   // rows per load instruction
   const int q = lane / lpr, ch = lane - q * lpr;
   const bool lane_on = q < rpi;  // lanes past rpi * lpr idle
   const int groups = (n + rpi - 1) / rpi, items = slices * groups;
-  int s = 0, g = 0;
+  int g = 0;
   for (int k0 = 0; k0 < items; k0 += kK8Batch) {  // uniform
     V kr[kK8Batch], vr[kK8Batch];
-    int64_t dst[kK8Batch];
+    float sr[kK8Batch];
+    int64_t dst[kK8Batch], place[kK8Batch];
 #pragma unroll
     for (int k = 0; k < kK8Batch; ++k) {
-      dst[k] = -1;
+      dst[k] = place[k] = -1;
       const int i = g * rpi + q;
-      if (k0 + k < items && lane_on && i < n) {
-        const int64_t from = s_from[w][i];
-        if (from >= 0) {
-          const int64_t at = slice_row(s);
-          const int64_t src = (at + from) * p.row_bytes + (int)sizeof(V) * ch;
-          kr[k] = *(const V*)(p.k + src);
-          vr[k] = *(const V*)(p.v + src);
-          dst[k] = (at + s_to[w][i]) * p.row_bytes + (int)sizeof(V) * ch;
+      if (k0 + k < items) {
+        if (g == 0 && s_src >= 0) {
+          sr[k] = scale[at + s_src];
+          place[k] = at + s_dst;
+        }
+        if (lane_on && i < n) {
+          const int64_t from = s_from[w][i];
+          if (from >= 0) {
+            const int64_t src = (at + from) * p.row_bytes + (int)sizeof(V) * ch;
+            kr[k] = *(const V*)(p.k + src);
+            vr[k] = *(const V*)(p.v + src);
+            dst[k] = (at + s_to[w][i]) * p.row_bytes + (int)sizeof(V) * ch;
+          }
         }
       }
       if (++g == groups) {  // on to the next slice
         g = 0;
-        ++s;
+        at += p.rows.page_size;
+        if (++head == p.heads) {
+          head = 0;
+          at += layer_rows - (int64_t)p.heads * p.rows.page_size;
+        }
       }
     }
 #pragma unroll
     for (int k = 0; k < kK8Batch; ++k) {
+      if (place[k] >= 0) scale[place[k]] = sr[k];
       if (dst[k] >= 0) {
         *(V*)(p.k + dst[k]) = kr[k];
         *(V*)(p.v + dst[k]) = vr[k];

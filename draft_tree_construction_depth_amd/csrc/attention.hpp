@@ -156,6 +156,16 @@ struct AttnParams {
 enum { kAtAlone, kAtPrefix, kAtRest };
 constexpr int kAtShare = 128;  // shared rows are used in multiples of every tile's TR
 
+// Shared rows get a pass of their own where that keeps so many bytes from being
+// read again, by as many requests as there are beyond one: the pass and its
+// merge are 25 to 30 us, of which the reading that they save has to be more. us
+// without / with, 8 key/value heads of 128, 4 query rows to each, own rows of
+// 512: 16 bits, 2 requests x 8 k (34 MB saved) 33 / 36, 32 x 1 k (130 MB) 36 /
+// 42, 8 x 8 k (235 MB) 58 / 40, 32 x 8 k (1 GB) 152 / 54; e4m3, 8 x 8 k (117 MB)
+// 38 / 37, at 64 query rows 56 / 61, 16 x 8 k (252 MB) at 64 rows 92 / 83, 32 x 8 k
+// 87 / 50.
+constexpr int64_t kAtShareBytes = (int64_t)192 << 20;
+
 // One request's work: rows [0, rows) of its block see anything (0: the
 // request is taken out); its waves of NQ query rows per key/value head are
 // dealt evenly to `tiles` query tiles.
@@ -1720,33 +1730,40 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
 
 // The rows that all requests taken part share, in whole steps of every tile, for
 // a batch whose first shared_len rows lie on the same pages: no more than any
-// request has committed. from: a request whose page table maps them.
-__device__ __forceinline__ int attn_shared(const AttnParams& p, AttnScratch& sh, int& from) {
+// request has committed, and none where that saves too little. row_bytes: of all
+// heads' keys and values. from: a request whose page table maps them.
+__device__ __forceinline__ int attn_shared(const AttnParams& p, AttnScratch& sh, int row_bytes,
+                                           int& from) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int least = 0x7FFFFFFF, first = 0x7FFFFFFF;
-  for (int b = tid; b < p.requests; b += kAtThreads) {
-    const int past = p.past_len[b];
-    if (past < 0) continue;
-    least = past < least ? past : least;
-    first = b < first ? b : first;
+  int least = 0x7FFFFFFF, first = 0x7FFFFFFF, count = 0;
+  for (int b0 = 0; b0 < p.requests; b0 += kAtThreads) {  // uniform
+    const int b = b0 + tid;
+    const int past = b < p.requests ? p.past_len[b] : -1;
+    least = past >= 0 && past < least ? past : least;
+    first = past >= 0 && b < first ? b : first;
+    count += __popcll(__ballot(past >= 0));
   }
   least = -wave_max(-least);
   first = -wave_max(-first);
   if (lane == 0) {
     sh.part[wave][0] = least;
     sh.part[wave][1] = first;
+    sh.longest[wave] = count;
   }
   __syncthreads();
+  count = 0;
   for (int i = 0; i < kAtWaves; ++i) {
     least = sh.part[i][0] < least ? (int)sh.part[i][0] : least;
     first = sh.part[i][1] < first ? (int)sh.part[i][1] : first;
+    count += sh.longest[i];
   }
   __syncthreads();  // before the plan takes sh
   from = __builtin_amdgcn_readfirstlane(first);
   int n = *p.shared_len;
   n = n < least ? n : least;
   n = n < p.rows.cap ? n : (int)p.rows.cap;
-  n = first == 0x7FFFFFFF || n < 0 ? 0 : n / kAtShare * kAtShare;
+  n = n > 0 ? n / kAtShare * kAtShare : 0;
+  n = (int64_t)(count - 1) * n < (kAtShareBytes + row_bytes - 1) / row_bytes ? 0 : n;
   return __builtin_amdgcn_readfirstlane(n);
 }
 
@@ -1766,7 +1783,7 @@ __global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(Att
     p.shared = 0;
     if (p.mode == kAtPrefix) {
       int from;
-      p.shared = attn_shared(p, sh.plan, from);
+      p.shared = attn_shared(p, sh.plan, 2 * p.kv_heads * C::CROW, from);
       if (id == 0 && threadIdx.x == 0) *p.prefix = p.shared;
       some = p.shared > 0;
       if (some) p.rows.table += (int64_t)from * p.rows.width;

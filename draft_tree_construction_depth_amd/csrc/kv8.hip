@@ -38,9 +38,17 @@ void launch_read8(const ddt::Read8Params& rp, int64_t blocks, int cache_dtype, h
                        dim3(ddt::kR8Threads), 0, st, rp);
 }
 
-// Whether a batch's shared rows are worth a pass of their own.
-bool shares(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads) {
-  return batch > 1 && (int64_t)T * (q_heads / kv_heads) <= 64;
+// Whether a batch's shared rows can be worth a pass of their own, of `cap` rows
+// of `elem` bytes an element (attn_shared decides, by the lengths). Up to 80 query
+// rows to a key/value head the cache's bytes are what it takes long to read; with
+// more the products are, which sharing does not save: 32 requests x 8 k shared
+// rows of 16 bits, 64 / 80 / 96 / 112 / 128 query rows, without 154 / 170 / 170 /
+// 173 / 182 us, with 123 / 150 / 168 / 187 / 200.
+bool shares(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+            int64_t cap, int elem) {
+  return batch > 1 && (int64_t)T * (q_heads / kv_heads) <= 80 &&
+         (double)(batch - 1) * (double)cap * 2.0 * kv_heads * head_dim * elem >=
+             (double)ddt::kAtShareBytes;
 }
 
 // The attention of a batch that shares rows: the pass over them, with all
@@ -70,16 +78,17 @@ bool share_fits(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads) {
 
 bool launchable(const AttnPlan& pl) { return launchable(pl.grid, ddt::kAtThreads); }
 
+// shared_elem: bytes of an element of a cache whose first rows are shared, 0 if none are
 size_t attention_workspace(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
                            int32_t head_dim, int64_t pages_per_request, int32_t page_size,
-                           bool shared) {
+                           int shared_elem) {
   if (batch <= 0 || pages_per_request <= 0 || page_size <= 0 ||
       attn_check(DDT_BF16, batch, T, q_heads, kv_heads, head_dim) != DDT_OK)
     return 0;
   const int64_t cap = pages_per_request > 0x7FFFFFFFLL / page_size
                           ? 0x7FFFFFFFLL
                           : pages_per_request * page_size;
-  if (shared && shares(batch, T, q_heads, kv_heads)) {
+  if (shared_elem && shares(batch, T, q_heads, kv_heads, head_dim, cap, shared_elem)) {
     if (!share_fits(batch, T, q_heads, kv_heads)) return 0;
     const SharePlan pl = share_plan(batch, T, q_heads, kv_heads, head_dim, cap);
     return launchable(pl.shared) && launchable(pl.own) ? pl.end : 0;
@@ -146,7 +155,7 @@ int attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_head
   ap.out = out;
   ap.lse = lse;
   ap.mode = ddt::kAtAlone;
-  if (!shared_len || !shares(batch, T, q_heads, kv_heads)) {
+  if (!shared_len || !shares(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap, row_elem)) {
     const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap);
     if (!launchable(pl)) return DDT_ENOTSUP;
     if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
@@ -355,7 +364,7 @@ size_t ddtree_attention_kv8_workspace_size(int64_t batch, int32_t T, int32_t q_h
                                            int64_t pages_per_request, int32_t page_size,
                                            int32_t shared) {
   return attention_workspace(batch, T, q_heads, kv_heads, head_dim, pages_per_request, page_size,
-                             shared != 0);
+                             shared != 0 ? 1 : 0);
 }
 
 int ddtree_attention_kv8(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
@@ -378,7 +387,7 @@ size_t ddtree_attention_shared_workspace_size(int64_t batch, int32_t T, int32_t 
                                               int32_t kv_heads, int32_t head_dim,
                                               int64_t pages_per_request, int32_t page_size) {
   return attention_workspace(batch, T, q_heads, kv_heads, head_dim, pages_per_request, page_size,
-                             true);
+                             2);
 }
 
 int ddtree_attention_shared(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
@@ -389,8 +398,11 @@ int ddtree_attention_shared(const void* q, int dtype, int64_t batch, int32_t T, 
                             const int32_t* shared_len, float scale, void* out, float* lse,
                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (batch > 0 && (!shared_len || !page_table)) return DDT_EINVAL;
-  const bool apart = attn_check(dtype, batch, T, q_heads, kv_heads, head_dim) == DDT_OK &&
-                     batch > 0 && shares(batch, T, q_heads, kv_heads);
+  const bool apart =
+      attn_check(dtype, batch, T, q_heads, kv_heads, head_dim) == DDT_OK && batch > 0 &&
+      table_width > 0 && page_size > 0 &&
+      shares(batch, T, q_heads, kv_heads, head_dim,
+             table_width > 0x7FFFFFFFLL / page_size ? 0x7FFFFFFFLL : table_width * page_size, 2);
   if (!apart)
     return ddtree_attention(q, dtype, batch, T, q_heads, kv_heads, head_dim, k_cache, v_cache,
                             page_table, table_width, pages, page_size, past_len, num_nodes, mask,

@@ -418,9 +418,11 @@ int ddtree_attention_kv8(const void* q, int dtype, int64_t batch, int32_t T, int
  * device memory: a negative one is 0, and more rows than a request has
  * committed (past_len) are never taken as shared. That the entries are alike is
  * not tested: where they differ, the first such request's are used for all.
- * With more than 64 query rows (T * q_heads / kv_heads) to a request's
- * key/value head, and for one request, the call is ddtree_attention's: such
- * calls are bound by their products, which sharing does not save.
+ * Rows are shared in multiples of 128, and only where it pays: where they keep
+ * 192 MiB or more of cache rows from being read again (by the requests that take
+ * part, but one), and up to 80 query rows (T * q_heads / kv_heads) to a request's
+ * key/value head; with more, the products are what takes long, which sharing does
+ * not save. All other rows are attended to request by request.
  * Supported as ddtree_attention, with a page table (DDT_EINVAL otherwise) and
  * batch * T * q_heads / kv_heads < 2^31 - 2^13 (DDT_ENOTSUP). The workspace
  * (ddtree_attention_shared_workspace_size) also holds the shared rows' part, a

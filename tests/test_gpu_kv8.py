@@ -139,28 +139,23 @@ def test_codes_of_values_at_every_border(kind):
 
 # ---- attention ----------------------------------------------------------------------
 def check(q, cache, kind, past, table, nn, mask, scale=None, clean=None, **kw):
-    """One call against the oracle. cache: (k, v, k scales, v scales) as uint8 and float32 arrays, or
-    two 16-bit tensors with kind ""; `clean`: the caches to give the oracle."""
-    batch, T, Hq, dh = q.shape
-    args = dict(num_nodes=dev(nn), mask=dev(mask), scale=scale, with_lse=True, **kw)
-    if kind:
-        on = [codes_on(cache[0], kind), codes_on(cache[1], kind), dev(cache[2]), dev(cache[3])]
-        got = pkg.ddtree_attention_kv8(q.to(DEV), *on, dev(past), page_table=dev(table), **args)
-        kc, vc, ks, vs = clean or cache
-        ko, vo = K.values(kc, ks, kind), K.values(vc, vs, kind)
-    else:
-        shared = args.pop("shared_len")
-        got = pkg.ddtree_attention_shared(q.to(DEV), cache[0].to(DEV), cache[1].to(DEV), dev(past), shared, dev(table),
-                                          **args)
-        ko, vo = (f64(c) for c in (clean or cache))
-    compare(got, q, ko, vo, past, table, nn, mask, scale, kind)
+    """One call against the oracle. cache: (k, v, k scales, v scales) as uint8 and float32 arrays;
+    `clean`: the cache to give the oracle."""
+    on = [codes_on(cache[0], kind), codes_on(cache[1], kind), dev(cache[2]), dev(cache[3])]
+    got = pkg.ddtree_attention_kv8(q.to(DEV), *on, dev(past), page_table=dev(table), num_nodes=dev(nn), mask=dev(mask),
+                                   scale=scale, with_lse=True, **kw)
+    kc, vc, ks, vs = clean or cache
+    vo = K.values(vc, vs, kind)
+    with np.errstate(invalid="ignore"):
+        oracle = O.attend(f64(q), K.values(kc, ks, kind), vo, past, table, nn, mask, scale)
+        compare(got, q, oracle, np.nanmax(np.abs(vo)), past, kind)
     return got
 
 
-def compare(got, q, ko, vo, past, table, nn, mask, scale, kind):
-    batch, T, Hq, dh = q.shape
-    with np.errstate(invalid="ignore"):
-        out, lse, spread, score = O.attend(f64(q), ko, vo, past, table, nn, mask, scale)
+def compare(got, q, oracle, most, past, kind):
+    """most: the largest magnitude of a value in the cache."""
+    T, dh = q.shape[1], q.shape[3]
+    out, lse, spread, score = oracle
     g, gl = f64(got["out"]), f64(got["lse"])
     n = int(np.max(past)) + T
     half = torch.finfo(q.dtype).eps / 2
@@ -169,7 +164,7 @@ def compare(got, q, ko, vo, past, table, nn, mask, scale, kind):
     if q.dtype == HF:
         tiny = 2.0 ** -25  # half a step of the smallest float16s
         if kind:
-            tiny += n * 2.0 ** -37 * np.nanmax(np.abs(vo))
+            tiny += n * 2.0 ** -37 * most
     tol = half * np.abs(out) + spread * (1 + half) * (half + 2 * off + (n + 16) * 2.0 ** -24) + tiny
     assert np.all(np.abs(g - out) <= tol * 1.01), np.max(np.abs(g - out) / np.maximum(tol, 1e-30))
     assert np.array_equal(np.isinf(gl), np.isinf(lse))
@@ -363,13 +358,15 @@ def test_attention_of_a_padded_batch_and_rows_without_room(kind):
 
 
 # ---- shared rows ----------------------------------------------------------------------
+ENOUGH = 192 << 20  # bytes that sharing has to save before rows are shared
+
+
 def shared_pages(rng, batch, past, T, ps, shared):
     """A table whose requests share the pages of their first `shared` rows, -1 behind their own."""
     same = shared // ps
     own, pool = paging(rng, batch, np.maximum(past + T - same * ps, 1), ps)
     table = np.concatenate([np.tile(np.arange(pool, pool + same, dtype=np.int32), (batch, 1)), own], 1)
-    rng.shuffle(table[0, :same])
-    table[:, :same] = table[0, :same]
+    table[:, :same] = rng.permutation(table[0, :same])
     return table, pool + same
 
 
@@ -377,15 +374,84 @@ def one(n):
     return torch.tensor([n], dtype=torch.int32, device=DEV)
 
 
-def make_cache(rng, shape, kind, dtype):
-    if kind:
-        (kc, ks), (vc, vs) = (random_cache(rng, shape, kind) for _ in range(2))
-        return kc, vc, ks, vs
-    return rounded(rng, shape, dtype), rounded(rng, shape, dtype)
+def make_cache(g, shape, kind, dtype):
+    """Device caches of normal rows: (k, v), or (k, v, k scales, v scales) of a kind of codes."""
+    if not kind:
+        return tuple(torch.empty(shape, dtype=dtype, device=DEV).normal_(generator=g) for _ in range(2))
+    codes, scales = [], []
+    for _ in range(2):
+        c, s = torch.empty(shape, dtype=CODES[kind], device=DEV), torch.empty(shape[:-1], device=DEV)
+        for p in range(0, shape[0], 4096):
+            x = torch.randn(c[p:p + 4096].shape, device=DEV, generator=g)
+            most = x.abs().amax(-1, keepdim=True)
+            x = x / most * K.MOST[kind]
+            c[p:p + 4096] = x.round().to(torch.int8) if kind == "i8" else x.to(CODES[kind])
+            s[p:p + 4096] = most[..., 0] / K.MOST[kind] * 4.0 ** torch.empty_like(most[..., 0]).uniform_(-1, 1, generator=g)
+        codes.append(c)
+        scales.append(s)
+    return (*codes, *scales)
+
+
+def attend64(q, cache, kind, past, table, nn, mask, scale=None):
+    """O.attend on the device, in float64, for caches too long for it."""
+    batch, T, Hq, dh = q.shape
+    ps, Hkv = cache[0].shape[2], cache[0].shape[1]
+    G, scale = Hq // Hkv, dh ** -0.5 if scale is None else scale
+    out, spread = (torch.zeros(q.shape, dtype=torch.float64, device=DEV) for _ in range(2))
+    lse = torch.full((batch, T, Hq), -float("inf"), dtype=torch.float64, device=DEV)
+    score, most = torch.zeros((batch, T, Hq), dtype=torch.float64, device=DEV), 0.0
+    bits = None if mask is None else O.mask_bits(mask, T)
+    for b in range(batch):
+        n = T - 1 if nn is None else min(max(int(nn[b]), 0), T - 1)
+        if past[b] < 0:
+            continue
+        rows = np.arange(min(int(past[b]) + n + 1, table.shape[1] * ps))
+        page = table[b, rows // ps]
+        held = (page >= 0) & (page < cache[0].shape[0])
+        sees = np.tile(held, (n + 1, 1))
+        own = np.tril(np.ones((n + 1, n + 1), bool)) if bits is None else bits[b, :n + 1, :n + 1]
+        sees[:, past[b]:] &= own[:, :max(len(rows) - int(past[b]), 0)]
+        sees = dev(sees)[None]
+        at = (dev(np.where(held, page, 0)).long(), slice(None), dev(rows % ps).long())
+        k, v = (c.view(torch.int8)[at].view(c.dtype).double() * s[at].double()[..., None] if kind else c[at].double()
+                for c, s in zip(cache[:2], cache[2:] or (None, None)))
+        most = max(most, float(v.abs().max()))
+        for h in range(Hkv):
+            x = q[b, :n + 1, h * G:(h + 1) * G].to(DEV).double().transpose(0, 1).reshape(-1, dh)
+            kt, vh = k[:, h].t().contiguous(), v[:, h].contiguous()
+            y = torch.where(sees, (x @ kt * scale).view(G, n + 1, -1), -float("inf"))
+            z = torch.logsumexp(y, -1)
+            a = torch.where(sees, (y - z[..., None]).exp(), 0.0).view(G * (n + 1), -1)
+            put = lambda t: t.view(G, n + 1, dh).transpose(0, 1)  # noqa: E731
+            out[b, :n + 1, h * G:(h + 1) * G], spread[b, :n + 1, h * G:(h + 1) * G] = put(a @ vh), put(a @ vh.abs())
+            lse[b, :n + 1, h * G:(h + 1) * G] = z.t()
+            size = torch.where(sees, (x.abs() @ kt.abs() * scale).view(G, n + 1, -1), 0.0).amax(-1)
+            score[b, :n + 1, h * G:(h + 1) * G] = size.t()
+    return tuple(t.cpu().numpy() for t in (out, lse, spread, score)), most
+
+
+def check_shared(q, cache, kind, past, table, nn, mask, shared, used):
+    """One call on device caches against the oracle; used: the rows that it takes as shared, None
+    where it makes no pass over them."""
+    batch, T, Hq, dh = q.shape
+    Hkv, ps = cache[0].shape[1:3]
+    args = (batch, T, Hq, Hkv, dh, table.shape[1], ps)
+    size = pkg.lib().ddtree_attention_kv8_workspace_size(*args, 1) if kind else \
+        pkg.lib().ddtree_attention_shared_workspace_size(*args)
+    assert (size > pkg.lib().ddtree_attention_workspace_size(*args)) == (used is not None)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    call = pkg.ddtree_attention_kv8 if kind else pkg.ddtree_attention_shared
+    got = call(q.to(DEV), *cache, dev(past), page_table=dev(table), num_nodes=dev(nn), mask=dev(mask), shared_len=one(shared),
+               with_lse=True, ws=ws)
+    if used is not None:
+        assert int(ws[:4].view(torch.int32)) == used  # the pass leaves them at the workspace's start
+    oracle, most = attend64(q, cache, kind, past, table, nn, mask)
+    compare(got, q, oracle, most, past, kind)
+    return got
 
 
 # T * G rows of a key/value head: with batch requests, all arrangements of both passes
-SHARED = [(3, 1, 1), (2, 1, 8), (5, 3, 8), (3, 9, 6), (40, 5, 4), (6, 16, 4), (4, 33, 3)]
+SHARED = [(3, 1, 1), (2, 1, 8), (5, 3, 8), (3, 9, 6), (40, 5, 4), (6, 16, 4), (4, 26, 3)]
 
 
 @pytest.mark.parametrize("kind", ["", "e4m3", "i8"])
@@ -393,83 +459,87 @@ SHARED = [(3, 1, 1), (2, 1, 8), (5, 3, 8), (3, 9, 6), (40, 5, 4), (6, 16, 4), (4
 @pytest.mark.parametrize("dh", [64, 128, 256])
 @pytest.mark.parametrize("batch,T,G", SHARED, ids=[f"{b}x{t * g}rows" for b, t, g in SHARED])
 def test_shared_rows(batch, T, G, dh, dtype, kind):
-    """Trees and chains behind a prefix, in every arrangement, type and head size: long prefixes and
-    short ones, requests that have nothing but the prefix, pages that share a tile's rows."""
-    rng = np.random.default_rng(batch * T * dh)
-    for shared, ps in ((1536, 16), (128, 128), (300, 4)):
-        past = (shared + rng.integers(0, 200, batch)).astype(np.int32)
-        past[0] = shared
-        table, pool = shared_pages(rng, batch, past, T, ps, shared)
-        q = rounded(rng, (batch, T, 2 * G, dh), dtype, 2.0)
-        cache = make_cache(rng, (pool, 2, ps, dh), kind, dtype)
-        nn = rng.integers(0, T, batch).astype(np.int32)
-        mask = OR.mask(trees(rng, batch, T - 1)[0], nn, T - 1).view(np.int64) if T > 1 else None
-        check(q, cache, kind, past, table, nn, mask, shared_len=one(shared // ps * ps))
-        if ps == 16:
-            check(q, cache, kind, past, table, None, None, shared_len=one(shared))
+    """Trees behind a prefix that is just long enough to be shared, in every arrangement, type and
+    head size, with requests that have nothing but the prefix."""
+    rng, g = np.random.default_rng(batch * T * dh), torch.Generator(device=DEV)
+    g.manual_seed(batch * T * dh)
+    Hkv, ps = 2, 128
+    rows = -(-ENOUGH // ((batch - 1) * 2 * Hkv * dh * (1 if kind else 2)))
+    used = -(-rows // 128) * 128
+    past = (used + rng.integers(0, 200, batch)).astype(np.int32)
+    past[0] = used
+    table, pool = shared_pages(rng, batch, past, T, ps, used)
+    q = rounded(rng, (batch, T, Hkv * G, dh), dtype, 2.0)
+    cache = make_cache(g, (pool, Hkv, ps, dh), kind, dtype)
+    nn = rng.integers(0, T, batch).astype(np.int32)
+    mask = OR.mask(trees(rng, batch, T - 1)[0], nn, T - 1).view(np.int64) if T > 1 else None
+    check_shared(q, cache, kind, past, table, nn, mask, used, used)
 
 
 @pytest.mark.parametrize("kind", ["", "e4m3"])
 def test_shared_lengths_of_every_kind(kind):
-    """None, negative ones, odd ones, more than the shortest request has committed, more than the
-    table has rows; requests taken out (whose table rows are not used), all of them, full caches."""
-    rng = np.random.default_rng(20)
-    batch, T, G, dh, ps = 6, 3, 4, 64, 16
-    past = np.array([-1, 700, 640, 690, -7, 900], np.int32)
-    table, pool = shared_pages(rng, batch, past, T, ps, 640)
+    """None, negative ones, odd ones, too short ones, more than the shortest request has committed;
+    requests taken out (whose table rows are not used), all of them, full caches; pages of one row."""
+    rng, g = np.random.default_rng(20), torch.Generator(device=DEV)
+    g.manual_seed(20)
+    batch, T, G, dh, ps, Hkv = 6, 3, 2, 256, 16, 8
+    least = -(-ENOUGH // (3 * 2 * Hkv * dh * (1 if kind else 2)))  # four take part
+    least = -(-least // 128) * 128
+    most = least + 1280
+    past = np.array([-1, most + 60, most, most + 50, -7, most + 300], np.int32)
+    table, pool = shared_pages(rng, batch, past, T, ps, most)
     table[[0, 4]] = -1
-    q = rounded(rng, (batch, T, 2 * G, dh), BF, 2.0)
-    cache = make_cache(rng, (pool, 2, ps, dh), kind, BF)
-    for shared in (0, -5, -2 ** 31, 1, 127, 128, 129, 640):
-        got = check(q, cache, kind, past, table, None, None, shared_len=one(shared))
+    q = rounded(rng, (batch, T, Hkv * G, dh), BF, 2.0)
+    cache = make_cache(g, (pool, Hkv, ps, dh), kind, BF)
+    for shared, used in ((0, 0), (-5, 0), (-2 ** 31, 0), (least - 1, 0), (least, least), (least + 127, least),
+                         (least + 129, least + 128), (most, most)):
+        got = check_shared(q, cache, kind, past, table, None, None, shared, used)
         assert not got["out"][[0, 4]].any()
     # pages that are alike further than the shortest request reaches: what it has committed is shared
     alike = table.copy()
-    alike[[0, 2, 3, 4]] = table[5]
-    short = np.where(past < 0, past, np.array([0, 700, 130, 300, 0, 700])).astype(np.int32)
-    alike[1] = table[5]
-    for shared in (640, 10 ** 6, 2 ** 31 - 1):
-        check(q, cache, kind, short, alike, None, None, shared_len=one(shared))
+    alike[:] = table[5]
+    short = np.array([-1, most + 60, least + 130, most + 300, -7, most + 300], np.int32)
+    for shared in (most, 10 ** 6, 2 ** 31 - 1):
+        check_shared(q, cache, kind, short, alike, None, None, shared, least + 128)
+    short[2] = 5
+    check_shared(q, cache, kind, short, alike, None, None, most, 0)
     none = np.full(batch, -1, np.int32)
-    got = check(q, cache, kind, none, table, None, None, shared_len=one(640))
-    assert not got["out"].any()
-    # a cache that ends inside or at the end of the shared rows
-    for width in (40, 41, 8):
-        cut = np.ascontiguousarray(alike[:, :width])
-        full = np.array([-1, width * ps, width * ps + 5, width * ps - 1, -7, width * ps], np.int32)
-        check(q, cache, kind, full, cut, None, None, shared_len=one(width * ps))
+    assert not check_shared(q, cache, kind, none, table, None, None, most, 0)["out"].any()
+    # a cache that ends inside or at the end of the shared rows (for it, six take part)
+    for rows, used in ((least + 640, least + 640), (least + 656, least + 640), (least, least)):
+        cut = np.ascontiguousarray(alike[:, :rows // ps])
+        full = np.array([rows + 7, rows, rows + 5, rows, -7, rows], np.int32)
+        check_shared(q, cache, kind, full, cut, None, None, rows, used)
 
 
 @pytest.mark.parametrize("kind", ["", "i8"])
-def test_shared_rows_on_no_page_and_garbage_behind(kind):
-    """Entries of the prefix outside the pool, garbage on pages that nobody sees, a workspace full of
-    ones; many requests."""
-    rng = np.random.default_rng(21)
-    batch, T, dh, ps, shared = 300, 1, 64, 16, 512
-    past = (shared + rng.integers(0, 300, batch)).astype(np.int32)
+def test_shared_rows_on_no_page(kind):
+    """Entries of the prefix outside the pool; more requests than a workgroup has threads."""
+    rng, g = np.random.default_rng(21), torch.Generator(device=DEV)
+    g.manual_seed(21)
+    batch, T, dh, ps, Hkv = 300, 1, 64, 16, 2
+    used = -(-ENOUGH // (296 * 2 * Hkv * dh * (1 if kind else 2)) // 128) * 128 + 128
+    past = (used + rng.integers(0, 300, batch)).astype(np.int32)
     past[[0, 17, 290]] = -1
-    table, pool = shared_pages(rng, batch, past, T, ps, shared)
+    table, pool = shared_pages(rng, batch, past, T, ps, used)
     table[:, 3], table[:, 20] = -1, pool
     q = rounded(rng, (batch, T, 8, dh), BF)
-    cache = make_cache(rng, (pool, 2, ps, dh), kind, BF)
-    size = pkg.lib().ddtree_attention_shared_workspace_size(batch, T, 8, 2, dh, table.shape[1], ps)
-    check(q, cache, kind, past, table, None, None, shared_len=one(shared),
-          ws=torch.full((size,), 255, dtype=torch.uint8, device=DEV))
+    cache = make_cache(g, (pool, Hkv, ps, dh), kind, BF)
+    check_shared(q, cache, kind, past, table, None, None, used, used)
 
 
 @pytest.mark.parametrize("kind", ["", "e4m3"])
 def test_poison_in_shared_rows_reaches_everybody(kind):
-    rng = np.random.default_rng(22)
-    batch, T, G, dh, ps, shared = 4, 2, 2, 64, 16, 256
-    past = np.full(batch, 300, np.int32)
-    table, pool = shared_pages(rng, batch, past, T, ps, shared)
+    rng, g = np.random.default_rng(22), torch.Generator(device=DEV)
+    g.manual_seed(22)
+    batch, T, G, dh, ps, used = 40, 2, 2, 128, 16, 10240
+    past = np.full(batch, used + 44, np.int32)
+    table, pool = shared_pages(rng, batch, past, T, ps, used)
     q = rounded(rng, (batch, T, 2 * G, dh), BF).to(DEV)
-    cache = make_cache(rng, (pool, 2, ps, dh), kind, BF)
-    on = [codes_on(c, kind) if c.dtype == np.uint8 else dev(c) for c in cache] if kind else [c.to(DEV) for c in cache]
-    (on[3] if kind else on[1])[table[0, 5], 1, 7] = float("nan")  # a value of head 1
+    on = make_cache(g, (pool, 2, ps, dh), kind, BF)
+    (on[3] if kind else on[1])[int(table[0, 5]), 1, 7] = float("nan")  # a value of head 1
     call = pkg.ddtree_attention_kv8 if kind else pkg.ddtree_attention_shared
-    kw = dict(page_table=dev(table), shared_len=one(shared), with_lse=True)
-    got = call(q, *on, dev(past), **kw)
+    got = call(q, *on, dev(past), page_table=dev(table), shared_len=one(used), with_lse=True)
     assert got["out"][:, :, G:].isnan().all() and got["out"][:, :, :G].isfinite().all()
     assert got["lse"].isfinite().all()
 
@@ -477,17 +547,16 @@ def test_poison_in_shared_rows_reaches_everybody(kind):
 @pytest.mark.parametrize("kind", ["", "e4m3"])
 def test_shared_calls_are_deterministic_and_keep_apart(kind):
     """Two streams and several host threads on one, with the binding's own workspaces."""
-    rng = np.random.default_rng(23)
-    batch, T, ps, shared = 5, 3, 32, 900
-    past = np.array([900, 1000, 2000, 950, 901], np.int32)
-    table, pool = shared_pages(rng, batch, past, T, ps, shared // ps * ps)
+    rng, g = np.random.default_rng(23), torch.Generator(device=DEV)
+    g.manual_seed(23)
+    batch, T, ps, shared = 5, 3, 32, 53248
+    past = (shared + np.array([0, 100, 1100, 50, 1])).astype(np.int32)
+    table, pool = shared_pages(rng, batch, past, T, ps, shared)
     call = pkg.ddtree_attention_kv8 if kind else pkg.ddtree_attention_shared
-    kw = dict(page_table=dev(table), shared_len=one(shared // ps * ps))
+    kw = dict(page_table=dev(table), shared_len=one(shared))
     at, sets = dev(past), []
     for _ in range(4):
-        cache = make_cache(rng, (pool, 2, ps, 128), kind, BF)
-        on = [codes_on(c, kind) if c.dtype == np.uint8 else dev(c) for c in cache] if kind else [c.to(DEV) for c in cache]
-        sets.append((rounded(rng, (batch, T, 8, 128), BF).to(DEV), *on))
+        sets.append((rounded(rng, (batch, T, 16, 128), BF).to(DEV), *make_cache(g, (pool, 4, ps, 128), kind, BF)))
     run = lambda s: call(*s, at, **kw)["out"]  # noqa: E731
     ref = [run(s) for s in sets]
     torch.cuda.synchronize()
@@ -684,7 +753,9 @@ def test_a_round(kind):
         kc, vc, ks, vs = K.append(x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:], *(a[layer] for a in before), kind, past,
                                   rope, False, table, dep, nn)
         q, o = outs[layer]
-        compare(o, q.cpu(), K.values(kc, ks, kind), K.values(vc, vs, kind), past, table, nn, g["mask"].numpy(), None, kind)
+        vo = K.values(vc, vs, kind)
+        compare(o, q.cpu(), O.attend(f64(q), K.values(kc, ks, kind), vo, past, table, nn, g["mask"].numpy()), np.abs(vo).max(),
+                past, kind)
         acc, n = g["accepted_nodes"].numpy(), g["accept_len"].numpy()
         k2, v2, nl = O.compact_paged(kc[None], vc[None], table, past, acc, n)
         ks2, vs2, _ = O.compact_paged(ks[None, ..., None], vs[None, ..., None], table, past, acc, n)

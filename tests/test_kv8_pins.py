@@ -156,16 +156,16 @@ def attention_call(L, name):
 @pytest.mark.parametrize("name", ["kv8", "shared"])
 def test_attention_refusals(L, name):
     call = attention_call(L, name)
-    for T in (9, 40):  # rows shared apart, and not
+    for T, width in ((9, 4), (9, 1 << 16), (40, 1 << 16)):  # rows shared apart in the second alone
         for bad in (dict(q=None), dict(kc=None), dict(past=None), dict(out=None), dict(ws=None), dict(q=ODD),
                     dict(kc=ODD), dict(out=ODD), dict(ws=ODD), dict(dtype=1), dict(dtype=3), dict(Hq=0), dict(Hq=7),
                     dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
                     dict(scale=3.4e38), dict(table=None), dict(pages=0), dict(width=0), dict(batch=-1)):
-            assert call(**{"T": T, **bad}) == -1, bad
+            assert call(**{"T": T, "width": width, **bad}) == -1, bad
         for bad in (dict(dh=96), dict(dh=512), dict(ps=24), dict(batch=1 << 31), dict(width=1 << 24)):
-            assert call(**{"T": T, **bad}) == -2, bad
-        assert call(T=T, n=0) == -3
-        assert call(T=T, batch=0) == 0
+            assert call(**{"T": T, "width": width, **bad}) == -2, bad
+        assert call(T=T, width=width, n=0) == -3
+        assert call(T=T, width=width, batch=0) == 0
     assert call(T=0) == -1 and call(T=514) == -2
     if name == "kv8":
         for bad in (dict(code=0), dict(code=2), dict(code=5), dict(ksc=None), dict(vsc=None), dict(ksc=TORN)):
@@ -180,12 +180,16 @@ def test_attention_refusals(L, name):
 def test_attention_workspaces(L):
     plain, kv8 = L.ddtree_attention_workspace_size, L.ddtree_attention_kv8_workspace_size
     shared = L.ddtree_attention_shared_workspace_size
-    size = (6, 9, 8, 2, 128, 40, 16)
+    size = (6, 9, 8, 2, 128, 1 << 14, 16)
     assert kv8(*size, 0) == plain(*size) > 0
-    # the shared rows' part: a float32 row for each row of q, behind the larger of the two passes' needs
+    # the shared rows' part: a float32 row for each row of q, beside the larger of the two passes' needs
     assert kv8(*size, 1) == shared(*size) >= 6 * 9 * 8 * (128 + 2) * 4 + plain(*size)
-    for alone in ((1, 9, 8, 2, 128, 40, 16), (6, 17, 8, 2, 128, 40, 16)):  # one request; 68 rows a head
+    # one request; 84 rows a head; caches that hold too few rows for sharing to pay: 192 MiB
+    for alone in ((1, 9, 8, 2, 128, 1 << 14, 16), (6, 21, 8, 2, 128, 1 << 14, 16), (6, 9, 8, 2, 128, 40, 16)):
         assert kv8(*alone, 1) == shared(*alone) == plain(*alone) > 0
+    rows = (192 << 20) // (5 * 2 * 2 * 128)  # of 8 bits, for five requests beside the first
+    assert kv8(6, 9, 8, 2, 128, rows // 16 + 1, 16, 1) > plain(6, 9, 8, 2, 128, rows // 16 + 1, 16)
+    assert kv8(6, 9, 8, 2, 128, rows // 16 - 1, 16, 1) == plain(6, 9, 8, 2, 128, rows // 16 - 1, 16)
     for bad in ((0, 9, 8, 2, 128, 4, 16), (2, 9, 8, 2, 96, 4, 16), (2, 514, 8, 2, 128, 4, 16)):
         assert kv8(*bad, 0) == kv8(*bad, 1) == shared(*bad) == 0
 

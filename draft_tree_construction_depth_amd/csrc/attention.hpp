@@ -50,6 +50,20 @@
 // the merge is 4 and the steps are 6: a chain of waits. 32 blocks of 32 rows
 // with 16 heads of 256 on 4 over 2 to 4 k: 194 us; 2 pieces of a prompt of 513
 // rows over 4 to 8 k: 180 us.
+//
+// Caches of 8-bit rows (CACHE) go the same way: codes are loaded to registers
+// and become values of the queries' type, which all of them have exactly, on
+// their way into LDS; a row's scale multiplies its scores, or its weight. They
+// halve the bytes and leave the products as they are. The same sizes: 64 single
+// tokens 174 us (806 MB + 25 of scales at 4.8 TB/s: the last workgroups end at
+// 173, the first at 107), 64 trees 268 to 300, 3 chains 114 (bound by the
+// vector units: exponentials, scales and masks), one tree 19.
+//
+// Rows that all requests share (EXT, kAtPrefix and kAtRest): one pass over them
+// with the query rows of the whole batch, whose maxima, sums and rows go to the
+// workspace, then each request's own rows, which begin from those. 64 single
+// tokens behind 8 k shared rows of 16 bits: 90 us, against 305 without; 24
+// chains of 5 rows (f16) behind 30 k of 8 bits: 126.
 #pragma once
 
 #include "paged.hpp"
@@ -460,7 +474,20 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     all_units += sh.part[0][i][1];
     longest = sh.longest[i] > longest ? sh.longest[i] : longest;
   }
-  const bool whole = all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
+  bool whole;
+  if (p.by_unit) {
+    // One round: whole units spare the second start of most stretches and the
+    // merge, and workgroups of long and short units share a CU; cut ones fill the
+    // card. us cut / whole over 0.5 to 1 k rows, 2 to 4 k: 64 single tokens (128 rows
+    // to a step) 34 / 30, 93 / 90, 52 of them 32 / 28, 71 / 74, 33 of them 25 /
+    // 26, 48 / 67; 64 requests of 128 query rows (64 to a step) 65 / 53, 156 /
+    // 151, 46 of them 53 / 50, 123 / 141; 64 of 64 query rows over 8 to 16 k 430 / 461.
+    const int64_t even = total, g = p.groups;  // (steps of an even cut, in 1 / g)
+    whole = 2 * longest * g <= 3 * even + 8 * g && longest * g <= even + 20 * g &&
+            even * g <= (even + 4 * g) * all_units;
+  } else {
+    whole = all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
+  }
   if (!whole) {
     const int want = (int)(((int64_t)total + p.least - 1) / p.least);
     const int n = want < p.groups ? want : p.groups;
@@ -884,7 +911,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* k, const unsigned
 // its value's before it is rounded, so that the codes enter the products as
 // they are. most: the largest finite scale of the tile's values (of an unmasked
 // tile, for float16); scan: V may hold NaNs. The rest is attn_tile's.
-constexpr float kAtLeastUnit = -60.0f;  // 2^-60: values of smaller scales are 0 in float16
+constexpr float kAtLeastUnit = -60.0f;  // log2: values of smaller scales are 0 in a float16 output
 
 template <typename H, int DH, int NQ, int KT, bool MASKED>
 __device__ __forceinline__ void attn_tile_codes(const unsigned char* k, const unsigned char* v,
@@ -1889,7 +1916,7 @@ __global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
 
 // The same with four waves to a state's part, each of every fourth piece, whose
 // results are joined in LDS: shared rows leave few units in many pieces (16
-// units of 128 queries in 512 pieces: 20.2 us with one wave, ... with four).
+// units of 128 queries in 512 pieces: 20.2 us with one wave, 10.6 with four).
 template <typename H, int DH, int NQ, int QW, int CACHE>
 __global__ __launch_bounds__(kAtThreads) void attn_merge_many_kernel(AttnParams p) {
   using C = AttnTile<DH, NQ, QW, CACHE>;

@@ -1,5 +1,6 @@
-// The attention of a batch that shares its first rows, over 16-bit caches (csrc/attention.hpp), a source of
-// its own so that the variants are compiled side by side.
+// The attention of a batch that shares its first rows, over 16-bit caches
+// (csrc/attention.hpp), a source of its own so that the variants are compiled
+// side by side.
 #include "verify.hpp"
 
 namespace ddt {

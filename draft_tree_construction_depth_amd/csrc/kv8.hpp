@@ -13,7 +13,9 @@
 // Append: one workgroup per row of the block, as in append.hpp. A key or value
 // head is the work of a group of lanes, a power of two of them inside a wave,
 // that find the row's largest magnitude by exchanges and then quantise what
-// they hold in registers: the inputs are read once.
+// they hold in registers: the inputs are read once. 64 blocks of 129 rows, 32
+// and 8 heads of 128: 27 us, 140 MB at 5.2 TB/s (HBM); one row: 3.1 us, two
+// dependent reads (length, page) and the exchanges.
 #pragma once
 
 #include "append.hpp"
@@ -225,7 +227,10 @@ constexpr int kK8MaxRows = 32;  // DDT_MAX_L
 // (csrc/kv.hpp has the 16-bit caches' and why it can be done in place: node
 // numbers increase along a path, and of one slice loads come before the stores
 // of the same or of later rows). A wave finds its request's rows once and moves
-// them for `each` slices; V is the piece that a lane moves at once.
+// them for `each` slices; V is the piece that a lane moves at once. All of a
+// batch's loads are in flight before its first store, scales among them (64
+// requests of 15 rows in 36 layers of 8 heads of 128, 73 MB: 37.5 -> 20 us), at
+// 3.6 TB/s: single rows of 128 bytes, and of 4 for the scales, at random places.
 template <typename V>
 __global__ __launch_bounds__(kK8Threads) void compact8_kernel(Kv8CompactParams p) {
   __shared__ int64_t s_from[kK8Threads / kWave][kK8MaxRows];
@@ -337,7 +342,9 @@ struct Read8Params {
 constexpr int kR8Threads = 256;
 
 // code * scale in float32, rounded once: a thread takes eight codes of K and of
-// V. Rows that no page holds, and those from count on, are cleared.
+// V. Rows that no page holds, and those from count on, are cleared. Bound by
+// HBM writes: 16 requests of 8 k rows, 8 heads of 128, int8 to bf16, 744 MB in
+// 146 us (5.1 TB/s); 129 rows 3.7 us.
 template <typename O, int CODE>
 __global__ __launch_bounds__(kR8Threads) void read8_kernel(Read8Params p) {
   const int64_t b = blockIdx.x / p.parts;

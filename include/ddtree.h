@@ -387,8 +387,10 @@ int ddtree_append_kv8(const void* q, const void* k, const void* v, int dtype, in
  * V_n being what the rows stand for. The codes enter the products as they are
  * (all have exact values in dtype); a score takes its key's scale in float32, a
  * weight its value's before it is rounded to dtype for its product with V
- * (DDT_F16: in units of the largest scale seen, or of twice that). Codes and
- * scales of any finite value may lie in the cache; what a row does not see
+ * (DDT_F16: in units of a power of two above the scales seen, of 2^-60 at least:
+ * smaller values are 0 in a float16 output too; with scales from 2^60 on a
+ * finite output is not promised). Codes and scales of any finite value, negative
+ * scales too, may lie in the cache; what a row does not see
  * (NaN and infinite scales and e4m3 NaN codes included) does not reach it, and
  * a row that sees a NaN has NaN.
  * shared_len [1] int32 or NULL: as in ddtree_attention_shared (page_table is

@@ -450,6 +450,34 @@ def check_shared(q, cache, kind, past, table, nn, mask, shared, used):
     return got
 
 
+LENGTHS = {"cut": [2600, 1531, 64], "one": [3001], "whole": [700, 0, 450, 699, 31, 512] * 7,
+           "uneven": [3000] + [40] * 30, "many": [130, 7, -1] * 100}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("T,G", [(1, 8), (9, 3), (12, 4), (40, 3)], ids=["8rows", "27rows", "48rows", "120rows"])
+def test_units_cut_and_whole(T, G, dh, dtype, kind):
+    """Batches whose work is cut into even stretches and merged, is dealt out as whole requests, and
+    is planned for more requests than a workgroup has threads; every one twice, with the same bits."""
+    rng, g = np.random.default_rng(T * dh + 3), torch.Generator(device=DEV)
+    g.manual_seed(T * dh + 3)
+    ps = 16
+    for past in LENGTHS.values():
+        past = np.array(past, np.int32)
+        batch = len(past)
+        table, pool = paging(rng, batch, past + T, ps)
+        q = rounded(rng, (batch, T, 2 * G, dh), dtype, 2.0)
+        cache = make_cache(g, (pool, 2, ps, dh), kind, dtype)
+        nn = rng.integers(0, T, batch).astype(np.int32)
+        mask = OR.mask(trees(rng, batch, T - 1)[0], nn, T - 1).view(np.int64) if T > 1 else None
+        got, again = (pkg.ddtree_attention_kv8(q.to(DEV), *cache, dev(past), page_table=dev(table), num_nodes=dev(nn),
+                                               mask=dev(mask), with_lse=True) for _ in range(2))
+        assert torch.equal(got["out"], again["out"]) and torch.equal(got["lse"], again["lse"])
+        compare(got, q, *attend64(q, cache, kind, past, table, nn, mask), past, kind)
+
+
 # T * G rows of a key/value head: with batch requests, all arrangements of both passes
 SHARED = [(3, 1, 1), (2, 1, 8), (5, 3, 8), (3, 9, 6), (40, 5, 4), (6, 16, 4), (4, 26, 3)]
 

@@ -55,14 +55,14 @@
 // and become values of the queries' type, which all of them have exactly, on
 // their way into LDS; a row's scale multiplies its scores, or its weight. They
 // halve the bytes and leave the products as they are. The same sizes: 64 single
-// tokens 174 us (806 MB + 25 of scales at 4.8 TB/s: the last workgroups end at
-// 173, the first at 107), 64 trees 268 to 300, 3 chains 114 (bound by the
-// vector units: exponentials, scales and masks), one tree 19.
+// tokens 171 us (806 MB and 25 of scales at 4.9 TB/s), 64 trees 264 to 276, 3
+// chains 107 (bound by the vector units: exponentials, scales and masks), one
+// tree 20.
 //
 // Rows that all requests share (EXT, kAtPrefix and kAtRest): one pass over them
 // with the query rows of the whole batch, whose maxima, sums and rows go to the
 // workspace, then each request's own rows, which begin from those. 64 single
-// tokens behind 8 k shared rows of 16 bits: 90 us, against 305 without; 24
+// tokens behind 8 k shared rows of 16 bits: 83 us, against 305 without; 24
 // chains of 5 rows (f16) behind 30 k of 8 bits: 126.
 #pragma once
 
@@ -102,7 +102,13 @@ struct AttnTile {
   static constexpr bool CODES = CACHE != kAtSame;
   static constexpr int NG = kAtWaves / QW;                 // groups over cache rows
   static constexpr int SK = QW == 4 && DH <= 128 ? 64 : 32;  // rows that a wave works on at once
-  static constexpr int KT = CODES && QW == 4 && DH == 64 ? 2 * SK : SK;  // rows of a group's tile
+  // Workgroups of a CU. Codes of heads of 64 leave LDS and registers for three,
+  // with shorter tiles and some registers spilled. us with two / three, bf16, 8
+  // key/value heads: 85 query rows, 3 requests over 50 to 100 k rows 117 / 110, 16
+  // over 4 to 8 k 57 / 56, 64 over 1 to 2 k 54 / 60; 516 query rows 382 / 363, 180 /
+  // 164, 185 / 169; f16 127 / 122, 65 / 65, 65 / 70; 429 / 413, 208 / 190, 221 / 202.
+  static constexpr int PER_CU = DH == 256 ? 1 : (CODES && DH == 64 && NQ == 32 ? 3 : 2);
+  static constexpr int KT = CODES && QW == 4 && DH == 64 && PER_CU == 2 ? 2 * SK : SK;  // rows of a group's tile
   static constexpr int TR = NG * KT;                       // rows of a workgroup's step
   static constexpr int ROW = DH * 2;                       // bytes of a row in LDS
   static constexpr int KROW = CODES ? ROW + 16 : ROW;      // ... of K's there, padded
@@ -482,7 +488,8 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     // to a step) 34 / 30, 93 / 90, 52 of them 32 / 28, 71 / 74, 33 of them 25 /
     // 26, 48 / 67; 64 requests of 128 query rows (64 to a step) 65 / 53, 156 /
     // 151, 46 of them 53 / 50, 123 / 141; 64 of 64 query rows over 8 to 16 k 430 / 461.
-    const int64_t even = total, g = p.groups;  // (steps of an even cut, in 1 / g)
+    // (Two workgroups to a CU keep it nearly as busy as three.)
+    const int64_t even = total, g = p.groups < 512 ? p.groups : 512;  // steps of an even cut, in 1 / g
     whole = 2 * longest * g <= 3 * even + 8 * g && longest * g <= even + 20 * g &&
             even * g <= (even + 4 * g) * all_units;
   } else {
@@ -1795,7 +1802,8 @@ __device__ __forceinline__ int attn_shared(const AttnParams& p, AttnScratch& sh,
 }
 
 template <typename H, int DH, int NQ, int QW, int CACHE = kAtSame, bool EXT = false>
-__global__ __launch_bounds__(kAtThreads, DH == 256 ? 1 : 2) void attn_kernel(AttnParams p) {
+__global__ __launch_bounds__(
+    kAtThreads, (AttnTile<DH, NQ, QW, CACHE>::PER_CU)) void attn_kernel(AttnParams p) {
   using C = AttnTile<DH, NQ, QW, CACHE>;
   using Lds = AttnLds<C, EXT>;
   __shared__ Lds sh;

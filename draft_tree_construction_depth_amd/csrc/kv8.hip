@@ -59,13 +59,13 @@ struct SharePlan {
 };
 
 SharePlan share_plan(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                     int64_t cap) {
+                     int64_t cap, bool codes) {
   SharePlan pl;
-  pl.shared = attn_plan_host(1, (int32_t)(batch * T), q_heads, kv_heads, head_dim, cap);
+  pl.shared = attn_plan_host(1, (int32_t)(batch * T), q_heads, kv_heads, head_dim, cap, codes);
   // a stretch's start and its pieces' way to the merge are worth steps: 64 single
   // tokens behind 8 k rows, 2048 steps: stretches of 4 92 us, of 8 89, of 16 95
   pl.shared.least = 8;
-  pl.own = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap);
+  pl.own = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap, codes);
   const size_t rows = (size_t)batch * T * q_heads;
   pl.ml = align_up(sizeof(int32_t));
   pl.o = align_up(pl.ml + rows * 2 * sizeof(float));
@@ -81,22 +81,22 @@ bool share_fits(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads) {
 
 bool launchable(const AttnPlan& pl) { return launchable(pl.grid, ddt::kAtThreads); }
 
-// shared_elem: bytes of an element of a cache whose first rows are shared, 0 if none are
+// elem: bytes of an element of the cache, one if it holds codes
 size_t attention_workspace(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
                            int32_t head_dim, int64_t pages_per_request, int32_t page_size,
-                           int shared_elem) {
+                           int elem, bool shared) {
   if (batch <= 0 || pages_per_request <= 0 || page_size <= 0 ||
       attn_check(DDT_BF16, batch, T, q_heads, kv_heads, head_dim) != DDT_OK)
     return 0;
   const int64_t cap = pages_per_request > 0x7FFFFFFFLL / page_size
                           ? 0x7FFFFFFFLL
                           : pages_per_request * page_size;
-  if (shared_elem && shares(batch, T, q_heads, kv_heads, head_dim, cap, shared_elem)) {
+  if (shared && shares(batch, T, q_heads, kv_heads, head_dim, cap, elem)) {
     if (!share_fits(batch, T, q_heads, kv_heads)) return 0;
-    const SharePlan pl = share_plan(batch, T, q_heads, kv_heads, head_dim, cap);
+    const SharePlan pl = share_plan(batch, T, q_heads, kv_heads, head_dim, cap, elem == 1);
     return launchable(pl.shared) && launchable(pl.own) ? pl.end : 0;
   }
-  const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap);
+  const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap, elem == 1);
   return launchable(pl) ? pl.end : 0;
 }
 
@@ -115,8 +115,8 @@ void set_work(ddt::AttnParams& ap, const AttnPlan& pl, char* at) {
 
 typedef int (*AttnLaunch)(const ddt::AttnParams&, const AttnPlan&, int, int, hipStream_t);
 
-// Attention over a cache of row_elem bytes an element; shared_len null: no
-// shared rows.
+// Attention over a cache of row_elem bytes an element (one: codes); shared_len
+// null: no shared rows.
 int attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
               int32_t kv_heads, int32_t head_dim, int row_elem, AttnLaunch launch,
               const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
@@ -159,14 +159,16 @@ int attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_head
   ap.lse = lse;
   ap.mode = ddt::kAtAlone;
   if (!shared_len || !shares(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap, row_elem)) {
-    const AttnPlan pl = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap);
+    const AttnPlan pl =
+        attn_plan_host(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap, row_elem == 1);
     if (!launchable(pl)) return DDT_ENOTSUP;
     if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
     set_work(ap, pl, (char*)workspace);
     return launch(ap, pl, dtype, head_dim, stream);
   }
   if (!share_fits(batch, T, q_heads, kv_heads)) return DDT_ENOTSUP;
-  const SharePlan pl = share_plan(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap);
+  const SharePlan pl =
+      share_plan(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap, row_elem == 1);
   if (!launchable(pl.shared) || !launchable(pl.own)) return DDT_ENOTSUP;
   if (workspace_bytes < pl.end) return DDT_EWORKSPACE;
   char* const ws = (char*)workspace;
@@ -367,7 +369,7 @@ size_t ddtree_attention_kv8_workspace_size(int64_t batch, int32_t T, int32_t q_h
                                            int64_t pages_per_request, int32_t page_size,
                                            int32_t shared) {
   return attention_workspace(batch, T, q_heads, kv_heads, head_dim, pages_per_request, page_size,
-                             shared != 0 ? 1 : 0);
+                             1, shared != 0);
 }
 
 int ddtree_attention_kv8(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,
@@ -390,7 +392,7 @@ size_t ddtree_attention_shared_workspace_size(int64_t batch, int32_t T, int32_t 
                                               int32_t kv_heads, int32_t head_dim,
                                               int64_t pages_per_request, int32_t page_size) {
   return attention_workspace(batch, T, q_heads, kv_heads, head_dim, pages_per_request, page_size,
-                             2);
+                             2, true);
 }
 
 int ddtree_attention_shared(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_heads,

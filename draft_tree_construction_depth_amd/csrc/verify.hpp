@@ -50,7 +50,7 @@ struct AttnPlan {
 };
 
 inline AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads,
-                        int32_t head_dim, int64_t cap) {
+                        int32_t head_dim, int64_t cap, bool codes = false) {
   AttnPlan pl;
   const int G = q_heads / kv_heads;
   // M query rows share a key/value head's pass. Up to 64: 16 to a wave, as many
@@ -72,8 +72,8 @@ inline AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_
   const int64_t tiles = (M + pl.NQ * pl.QW - 1) / (pl.NQ * pl.QW);
   pl.least = 2;
   // two workgroups on each of 256 CUs (one where a tile fills the LDS or the
-  // registers), fewer for little work
-  pl.groups = head_dim == 256 ? 256 : 512;
+  // registers, or AttnTile::PER_CU), fewer for little work
+  pl.groups = head_dim == 256 ? 256 : (codes && head_dim == 64 && pl.NQ == 32 ? 768 : 512);
   const int64_t axis = steps > ((int64_t)1 << 31) / (kv_heads * tiles) / batch
                            ? (int64_t)1 << 31
                            : batch * kv_heads * tiles * steps;

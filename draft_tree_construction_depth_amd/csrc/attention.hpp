@@ -62,8 +62,8 @@
 // Rows that all requests share (EXT, kAtPrefix and kAtRest): one pass over them
 // with the query rows of the whole batch, whose maxima, sums and rows go to the
 // workspace, then each request's own rows, which begin from those. 64 single
-// tokens behind 8 k shared rows of 16 bits: 83 us, against 305 without; 24
-// chains of 5 rows (f16) behind 30 k of 8 bits: 126.
+// tokens behind 8 k shared rows of 16 bits: 83 us, 270 without; 24
+// chains of 5 rows (f16) behind 30 k of 8 bits: 126 us, 311 without.
 #pragma once
 
 #include "paged.hpp"

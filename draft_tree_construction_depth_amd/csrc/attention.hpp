@@ -449,6 +449,74 @@ template <class C>
 __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, AttnCut& cut,
                               AttnPos& from, AttnPos& to, AttnReq& rq, int& unit, int& all_units) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, batch = (int)p.batch;
+  auto dealt_whole = [&](int total, int longest) -> bool {
+    if (!p.by_unit) return all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
+    // One round: whole units spare the second start of most stretches and the
+    // merge, and workgroups of long and short units share a CU; cut ones fill the
+    // card. us cut / whole over 0.5 to 1 k rows, 2 to 4 k: 64 single tokens (128 rows
+    // to a step) 34 / 30, 93 / 90, 52 of them 32 / 28, 71 / 74, 33 of them 25 /
+    // 26, 48 / 67; 64 requests of 128 query rows (64 to a step) 65 / 53, 156 /
+    // 151, 46 of them 53 / 50, 123 / 141; 64 of 64 query rows over 8 to 16 k 430 / 461.
+    // (Two workgroups to a CU keep it nearly as busy as three.)
+    const int64_t even = total, g = p.groups < 512 ? p.groups : 512;  // steps of an even cut, in 1 / g
+    return 2 * longest * g <= 3 * even + 8 * g && longest * g <= even + 20 * g &&
+           even * g <= (even + 4 * g) * all_units;
+  };
+  // the cut, and whether workgroup w has stretch k of it
+  auto stretch = [&](int total) -> bool {
+    const int want = __builtin_amdgcn_readfirstlane(
+        (int)(((uint32_t)total + (uint32_t)p.least - 1) / (uint32_t)p.least));
+    const int n = want < p.groups ? want : p.groups;
+    const int per = (n + 7) >> 3;
+    k = w;
+    if ((w >> 3) >= per) return false;
+    k = (w & 7) * per + (w >> 3);
+    if (k >= n) return false;
+    const int range = __builtin_amdgcn_readfirstlane((int)((uint32_t)total / (uint32_t)n));
+    cut.n = n;
+    cut.total = total;
+    cut.range = range;
+    cut.extra = total - range * n;
+    // (a step at least: 64 requests of 4 to 9 steps behind shared rows, 6.5 to a
+    // stretch, 66 us with half a stretch to either side and 60 with one step)
+    cut.slack = range < 4 ? range >> 1 : (range < 8 ? 1 : range >> 3);
+    return true;
+  };
+  auto end = [&](int e) -> int {  // attn_end: extra * e is below 2^20
+    const uint32_t more = (uint32_t)((int)cut.extra * e) / (uint32_t)(int)cut.n;
+    return (int)cut.range * e + __builtin_amdgcn_readfirstlane((int)more);
+  };
+  if (batch == 1) {
+    // One request (and a batch's shared rows): nothing to add up, so all of it is
+    // in scalars, without the LDS (one tree of 65 rows over 1 k: 19.9 -> 19.1 us).
+    rq = attn_request<C, true>(p, 0);
+    rq.past = __builtin_amdgcn_readfirstlane(rq.past);
+    rq.rows = __builtin_amdgcn_readfirstlane(rq.rows);
+    attn_request_sizes<C, true>(p, rq);
+    all_units = rq.tiles * p.kv_heads;
+    unit = 0;
+    const int total = all_units * rq.steps;
+    k = w;
+    if (dealt_whole(total, rq.steps)) {
+      const int xcd = w & 7, at = w >> 3, group = at / rq.tiles, head = xcd + 8 * group;
+      if (head >= p.kv_heads) return false;
+      from = AttnPos{-1, 0, head * rq.tiles + (at - group * rq.tiles), 0};
+      to = AttnPos{-1, 0, from.u + 1, 0};
+      return true;
+    }
+    if (!stretch(total)) return false;
+    auto place = [&](int e) -> AttnPos {
+      const int x = end(e);
+      const int u = __builtin_amdgcn_readfirstlane((int)((uint32_t)x / (uint32_t)rq.steps));
+      int step = x - u * rq.steps;
+      if (e > 0 && e < (int)cut.n) step = (int)attn_near(cut, step, rq.steps);
+      const bool past = step == rq.steps;
+      return attn_uniform(AttnPos{(int64_t)u * rq.steps + step, 0, u + past, past ? 0 : step});
+    };
+    from = place(k);
+    to = place(k + 1);
+    return true;
+  }
   AttnReq r;
   r.past = r.rows = r.steps = 0;
   r.tiles = 1;
@@ -480,37 +548,12 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     all_units += sh.part[0][i][1];
     longest = sh.longest[i] > longest ? sh.longest[i] : longest;
   }
-  bool whole;
-  if (p.by_unit) {
-    // One round: whole units spare the second start of most stretches and the
-    // merge, and workgroups of long and short units share a CU; cut ones fill the
-    // card. us cut / whole over 0.5 to 1 k rows, 2 to 4 k: 64 single tokens (128 rows
-    // to a step) 34 / 30, 93 / 90, 52 of them 32 / 28, 71 / 74, 33 of them 25 /
-    // 26, 48 / 67; 64 requests of 128 query rows (64 to a step) 65 / 53, 156 /
-    // 151, 46 of them 53 / 50, 123 / 141; 64 of 64 query rows over 8 to 16 k 430 / 461.
-    // (Two workgroups to a CU keep it nearly as busy as three.)
-    const int64_t even = total, g = p.groups < 512 ? p.groups : 512;  // steps of an even cut, in 1 / g
-    whole = 2 * longest * g <= 3 * even + 8 * g && longest * g <= even + 20 * g &&
-            even * g <= (even + 4 * g) * all_units;
-  } else {
-    whole = all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
-  }
-  if (!whole) {
-    const int want = (int)(((int64_t)total + p.least - 1) / p.least);
-    const int n = want < p.groups ? want : p.groups;
-    const int per = (n + 7) >> 3;
-    k = w;
-    if ((w >> 3) >= per) return false;
-    k = (w & 7) * per + (w >> 3);
-    if (k >= n) return false;
-    cut.n = n;
-    cut.total = total;
-    cut.range = total / n;
-    cut.extra = total - (int)cut.range * n;
-    // (a step at least: 64 requests of 4 to 9 steps behind shared rows, 6.5 to a
-    // stretch, 66 us with half a stretch to either side and 60 with one step)
-    cut.slack = cut.range < 4 ? cut.range >> 1 : (cut.range < 8 ? 1 : cut.range >> 3);
-    const int x0 = (int)attn_end(cut, k), x1 = (int)attn_end(cut, k + 1);
+  total = __builtin_amdgcn_readfirstlane(total);
+  longest = __builtin_amdgcn_readfirstlane(longest);
+  all_units = __builtin_amdgcn_readfirstlane(all_units);
+  if (!dealt_whole(total, longest)) {
+    if (!stretch(total)) return false;
+    const int x0 = end(k), x1 = end(k + 1), n = (int)cut.n;
     auto place = [&](int e, int x, AttnPos& at) {
       x -= before;
       int u = (int)((uint32_t)x / (uint32_t)r.steps), s = x - u * r.steps;

@@ -449,6 +449,11 @@ template <class C>
 __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, AttnCut& cut,
                               AttnPos& from, AttnPos& to, AttnReq& rq, int& unit, int& all_units) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, batch = (int)p.batch;
+  auto stretches = [&](int total) -> int {
+    const int want = __builtin_amdgcn_readfirstlane(
+        (int)(((uint32_t)total + (uint32_t)p.least - 1) / (uint32_t)p.least));
+    return want < p.groups ? want : p.groups;
+  };
   auto dealt_whole = [&](int total, int longest) -> bool {
     if (!p.by_unit) return all_units >= 2 * p.groups && longest * (int64_t)p.groups <= total;
     // One round: whole units spare the second start of most stretches and the
@@ -457,16 +462,21 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     // to a step) 34 / 30, 93 / 90, 52 of them 32 / 28, 71 / 74, 33 of them 25 /
     // 26, 48 / 67; 64 requests of 128 query rows (64 to a step) 65 / 53, 156 /
     // 151, 46 of them 53 / 50, 123 / 141; 64 of 64 query rows over 8 to 16 k 430 / 461.
-    // (Two workgroups to a CU keep it nearly as busy as three.)
-    const int64_t even = total, g = p.groups < 512 ? p.groups : 512;  // steps of an even cut, in 1 / g
-    return 2 * longest * g <= 3 * even + 8 * g && longest * g <= even + 20 * g &&
-           even * g <= (even + 4 * g) * all_units;
+    // (Two workgroups to a CU keep it nearly as busy as three.) Too little work for
+    // that is cut into stretches of p.least steps, which end sooner than units of
+    // more than twice that: a call over 150 rows, 64-row steps, one tree of 65 16 /
+    // 17, 16 of them 30 / 24; heads of 256, 32-row steps, 16 query rows 15.5 / 19.6.
+    constexpr int kFull = C::PER_CU == 1 ? 256 : 512;
+    int g = stretches(total);
+    const int spare = g < kFull ? 2 : 4;
+    g = g < kFull ? g : kFull;
+    const int64_t even = total;  // steps of an even stretch, in 1 / g
+    return 2 * (int64_t)longest * g <= 3 * even + 8 * g && longest * (int64_t)g <= even + 20 * g &&
+           even * g < (even + spare * g) * all_units;
   };
   // the cut, and whether workgroup w has stretch k of it
   auto stretch = [&](int total) -> bool {
-    const int want = __builtin_amdgcn_readfirstlane(
-        (int)(((uint32_t)total + (uint32_t)p.least - 1) / (uint32_t)p.least));
-    const int n = want < p.groups ? want : p.groups;
+    const int n = stretches(total);
     const int per = (n + 7) >> 3;
     k = w;
     if ((w >> 3) >= per) return false;

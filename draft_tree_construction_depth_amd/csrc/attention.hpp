@@ -56,14 +56,14 @@
 // their way into LDS; a row's scale multiplies its scores, or its weight. They
 // halve the bytes and leave the products as they are. The same sizes: 64 single
 // tokens 171 us (806 MB and 25 of scales at 4.9 TB/s), 64 trees 264 to 276, 3
-// chains 107 (bound by the vector units: exponentials, scales and masks), one
-// tree 20.
+// chains 105 to 118 (bound by the vector units: exponentials, scales and masks),
+// one tree 19.
 //
 // Rows that all requests share (EXT, kAtPrefix and kAtRest): one pass over them
 // with the query rows of the whole batch, whose maxima, sums and rows go to the
 // workspace, then each request's own rows, which begin from those. 64 single
-// tokens behind 8 k shared rows of 16 bits: 83 us, 270 without; 24
-// chains of 5 rows (f16) behind 30 k of 8 bits: 126 us, 311 without.
+// tokens behind 8 k shared rows of 16 bits: 82 us, 270 without; 24 chains of 5
+// rows (f16) behind 30 k of 8 bits: 126 us, 311 without.
 #pragma once
 
 #include "paged.hpp"

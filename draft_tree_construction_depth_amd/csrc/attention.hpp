@@ -195,7 +195,7 @@ struct AttnReq {
 
 // The rest of a request, from its past and rows.
 template <class C, bool EXT>
-__device__ __forceinline__ void attn_request_sizes(const AttnParams& p, AttnReq& r) {
+__host__ __device__ __forceinline__ void attn_request_sizes(const AttnParams& p, AttnReq& r) {
   const int64_t n = (int64_t)r.past + (EXT && p.mode == kAtPrefix ? 0 : r.rows);
   r.len = r.past < 0 ? 0 : (int)(n < p.rows.cap ? n : p.rows.cap);
   // one step for an empty request: its rows are cleared
@@ -1217,11 +1217,22 @@ struct AttnQuery {
   bool live;  // it takes part
 };
 
-template <int NQ>
-__device__ __forceinline__ AttnQuery attn_query(const AttnParams& p, const AttnReq& r, int u, int wq,
-                                                int lane) {
+// A request's waves are dealt evenly to its query tiles: this is the first of
+// tile `tile`, floor(tile * waves / tiles). That product leaves 32 bits from
+// 1.5 M query rows on, which a batch's shared rows may have; the waves that the
+// tiles are short of, fewer than QW for all of them together (QW for a request
+// without rows), give the same number.
+template <int QW>
+__host__ __device__ __forceinline__ int attn_first_wave(const AttnReq& r, int tile) {
+  const int spare = QW * r.tiles - r.waves;
+  return QW * tile - (tile * spare + r.tiles - 1) / r.tiles;
+}
+
+template <int NQ, int QW>
+__host__ __device__ __forceinline__ AttnQuery attn_query(const AttnParams& p, const AttnReq& r, int u,
+                                                         int wq, int lane) {
   const int head = u / r.tiles, tile = u - head * r.tiles;
-  const int w0 = tile * r.waves / r.tiles, w1 = (tile + 1) * r.waves / r.tiles;
+  const int w0 = attn_first_wave<QW>(r, tile), w1 = attn_first_wave<QW>(r, tile + 1);
   const int col = (w0 + wq) * NQ + lane % NQ;
   AttnQuery q;
   q.i = col / p.G;
@@ -1737,7 +1748,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = wave / QW, wq = wave % QW;
   const int head = u / rq.tiles;
-  const AttnQuery me = attn_query<NQ>(p, rq, u, wq, lane);
+  const AttnQuery me = attn_query<NQ, QW>(p, rq, u, wq, lane);
   const int i = me.i;
   const bool live = me.live;
   const bool busy = __ballot(live) != 0;  // a wave without queries only carries rows
@@ -1801,7 +1812,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams& p, unsigned char* l
 #pragma unroll
   for (int j = 0; j < C::PIECES; ++j) o[j] = st.get(j);
   if (slot < 0) {
-    const AttnQuery to = attn_query<NQ>(p, rq, u, wq, out_lane);
+    const AttnQuery to = attn_query<NQ, QW>(p, rq, u, wq, out_lane);
     if (to.live)
       attn_store<H, DH, NQ, C::PIECES, EXT>(p, ((int64_t)b * p.T + to.i) * p.q_heads + to.hq, 0,
                                             st.m, st.l, o, out_lane);
@@ -1951,7 +1962,7 @@ __global__ __launch_bounds__(kWave) void attn_merge_kernel(AttnParams p) {
   rq.rows = pl.rows;
   rq.waves = pl.waves;
   rq.tiles = pl.tiles;
-  const AttnQuery me = attn_query<NQ>(p, rq, pl.u, wq, lane);
+  const AttnQuery me = attn_query<NQ, QW>(p, rq, pl.u, wq, lane);
   if (!__ballot(me.live)) return;
   float m = -INFINITY, l = 0.0f;
   at_f32x4 o[PP];
@@ -1995,7 +2006,7 @@ __global__ __launch_bounds__(kAtThreads) void attn_merge_many_kernel(AttnParams 
   rq.rows = pl.rows;
   rq.waves = pl.waves;
   rq.tiles = pl.tiles;
-  const AttnQuery me = attn_query<NQ>(p, rq, pl.u, wq, lane);
+  const AttnQuery me = attn_query<NQ, QW>(p, rq, pl.u, wq, lane);
   if (!__ballot(me.live)) return;  // all waves alike
   float m = -INFINITY, l = 0.0f;
   at_f32x4 o[PP];

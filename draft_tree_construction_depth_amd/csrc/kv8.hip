@@ -52,7 +52,9 @@ bool shares(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t
 }
 
 // The attention of a batch that shares rows: the pass over them, with all
-// requests' block rows as one request's, then the requests' own.
+// requests' block rows as one request's, then the requests' own. (attn_check
+// leaves fewer than 2^29 query rows to a key/value head: they are counted in 31
+// bits.)
 struct SharePlan {
   AttnPlan shared, own;
   size_t ml, o, work, end;  // workspace; *prefix lies at its start
@@ -74,11 +76,6 @@ SharePlan share_plan(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads
   return pl;
 }
 
-// batch * T * G block rows of a key/value head are counted in 31 bits
-bool share_fits(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads) {
-  return batch <= 0x7FFFFFFFLL / T / (q_heads / kv_heads) - 64;
-}
-
 bool launchable(const AttnPlan& pl) { return launchable(pl.grid, ddt::kAtThreads); }
 
 // elem: bytes of an element of the cache, one if it holds codes
@@ -92,7 +89,6 @@ size_t attention_workspace(int64_t batch, int32_t T, int32_t q_heads, int32_t kv
                           ? 0x7FFFFFFFLL
                           : pages_per_request * page_size;
   if (shared && shares(batch, T, q_heads, kv_heads, head_dim, cap, elem)) {
-    if (!share_fits(batch, T, q_heads, kv_heads)) return 0;
     const SharePlan pl = share_plan(batch, T, q_heads, kv_heads, head_dim, cap, elem == 1);
     return launchable(pl.shared) && launchable(pl.own) ? pl.end : 0;
   }
@@ -166,7 +162,6 @@ int attention(const void* q, int dtype, int64_t batch, int32_t T, int32_t q_head
     set_work(ap, pl, (char*)workspace);
     return launch(ap, pl, dtype, head_dim, stream);
   }
-  if (!share_fits(batch, T, q_heads, kv_heads)) return DDT_ENOTSUP;
   const SharePlan pl =
       share_plan(batch, T, q_heads, kv_heads, head_dim, ap.rows.cap, row_elem == 1);
   if (!launchable(pl.shared) || !launchable(pl.own)) return DDT_ENOTSUP;

@@ -323,7 +323,7 @@ int ddtree_append_kv(const void* q, const void* k, const void* v, int dtype, int
  * (DDT_EINVAL otherwise), T <= DDT_MAX_B + 1, scale > 0 with scale * log2(e)
  * finite in float32 (DDT_EINVAL),
  * at most 2^27 cache rows per request (table_width * page_size), pages of a
- * layer below 4 GiB.
+ * layer below 4 GiB, batch * T * q_heads below 2^29.
  * The workspace (ddtree_attention_workspace_size bytes, no zero-fill needed;
  * pages_per_request = table_width, or 1 without a table) holds partial
  * results of long caches split over workgroups.
@@ -425,10 +425,9 @@ int ddtree_attention_kv8(const void* q, int dtype, int64_t batch, int32_t T, int
  * part, but one), and up to 80 query rows (T * q_heads / kv_heads) to a request's
  * key/value head; with more, the products are what takes long, which sharing does
  * not save. All other rows are attended to request by request.
- * Supported as ddtree_attention, with a page table (DDT_EINVAL otherwise) and
- * batch * T * q_heads / kv_heads < 2^31 - 2^13 (DDT_ENOTSUP). The workspace
- * (ddtree_attention_shared_workspace_size) also holds the shared rows' part, a
- * float32 row for each row of q.
+ * Supported as ddtree_attention, with a page table (DDT_EINVAL otherwise). The
+ * workspace (ddtree_attention_shared_workspace_size) also holds the shared rows'
+ * part, a float32 row for each row of q.
  */
 size_t ddtree_attention_shared_workspace_size(int64_t batch, int32_t T, int32_t q_heads,
                                               int32_t kv_heads, int32_t head_dim,

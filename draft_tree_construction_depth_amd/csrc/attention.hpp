@@ -1295,20 +1295,26 @@ __device__ __forceinline__ bool attn_mapped(const PagedRows& p, int b, int r0, i
   return !(s_any[0] | s_any[1] | s_any[2] | s_any[3]);
 }
 
-// Clears the rows of request b that see nothing, for one key/value head.
+// Row of the output that is query row k of block rows [rows, T) of a key/value
+// head, k < (T - rows) * G.
+__host__ __device__ __forceinline__ int64_t attn_row_behind(const AttnParams& p, int64_t b, int rows,
+                                                            int head, int k) {
+  const int row = k / p.G;
+  return (b * p.T + rows + row) * p.q_heads + head * p.G + (k - row * p.G);
+}
+
+// Clears the rows of request b that see nothing, for one key/value head. (Rows
+// are counted, which stay below 2^29, and not their pieces of 16 bytes.)
 template <typename H, int DH>
 __device__ __forceinline__ void attn_clear(const AttnParams& p, int64_t b, int rows, int head) {
-  const int per = p.G * DH / 8;  // 16-byte pieces of a block row's heads
-  for (int k = threadIdx.x; k < (p.T - rows) * per; k += kAtThreads) {
-    const int row = k / per, c = k - row * per;
-    const int64_t at = ((b * p.T + rows + row) * p.q_heads + (int64_t)head * p.G) * DH + c * 8;
-    *(at_u32x4*)((H*)p.out + at) = at_u32x4{0, 0, 0, 0};
-  }
+  constexpr int PIECES = DH / 8;
+  const int tid = attn_tid(), n = (p.T - rows) * p.G, c = tid % PIECES;
+  for (int k = tid / PIECES; k < n; k += kAtThreads / PIECES)
+    *(at_u32x4*)((H*)p.out + attn_row_behind(p, b, rows, head, k) * DH + c * 8) =
+        at_u32x4{0, 0, 0, 0};
   if (p.lse)
-    for (int k = threadIdx.x; k < (p.T - rows) * p.G; k += kAtThreads) {
-      const int row = k / p.G;
-      p.lse[(b * p.T + rows + row) * p.q_heads + head * p.G + (k - row * p.G)] = -INFINITY;
-    }
+    for (int k = tid; k < n; k += kAtThreads)
+      p.lse[attn_row_behind(p, b, rows, head, k)] = -INFINITY;
 }
 
 // 64 lanes' 16-byte pieces from global memory straight into 1 KiB of LDS at

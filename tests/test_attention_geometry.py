@@ -77,6 +77,24 @@ void none(int G) {
       for (int lane = 0; lane < kWave; ++lane) CHECK((!attn_query<NQ, QW>(p, r, u, wq, lane).live));
 }
 
+// Query rows of block rows [rows, T) of a head lie one behind the other, block row by block row.
+void behind(int T, int rows, int G, int kv_heads) {
+  using C = AttnTile<64, 16, 2>;
+  AttnParams p{};
+  p.T = T;
+  p.G = G;
+  p.kv_heads = kv_heads;
+  p.q_heads = G * kv_heads;
+  int tile = 0;
+  const int64_t all = (int64_t)(T - rows) * G;
+  const int64_t around[] = {0, G, 2 * (int64_t)G, all / 2, all, 1 << 26, 1 << 28};
+  const int head = kv_heads - 1;
+  for (int64_t at : around)
+    for (int64_t k = at < 2 ? 0 : at - 2; k < at + 3 && k < all; ++k)
+      CHECK(attn_row_behind(p, 3, rows, head, (int)k) ==
+            (3 * (int64_t)T + rows + k / G) * p.q_heads + (int64_t)head * G + k % G);
+}
+
 template <int DH, int NQ, int QW>
 void all() {
   const int rows[] = {1, 2, 7, 16, 17, 63, 64, 65, 129, 1000, 513 * 80, 1480000, 1490000, 1500001, 2960000, 2980000,
@@ -98,12 +116,18 @@ int main() {
   all<64, 32, 4>();
   all<256, 16, 2>();
   all<256, 16, 4>();
+  for (int G : {1, 5, 128, 100000, (1 << 29) / 513}) {
+    behind(513, 1, G, 1);
+    behind(513, 0, G, 1);
+    if (G < 1000) behind(9, 5, G, 7);
+  }
+  behind(1, 0, (1 << 29) - 1, 1);
   puts("fine");
 }
 """
 
 
-def test_query_rows_of_any_count_are_dealt_once(tmp_path):
+def test_query_rows_of_any_count(tmp_path):
     source, program = tmp_path / "geometry.hip", tmp_path / "geometry"
     source.write_text(PROGRAM)
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

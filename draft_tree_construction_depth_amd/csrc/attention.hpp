@@ -237,6 +237,15 @@ __device__ __forceinline__ int64_t attn_wave_scan(int64_t x) {
   return x;
 }
 
+// Which of n stretches or units is workgroup w's (n or more: none, each number
+// once). Consecutive workgroups of one XCD (ids 8 apart) take consecutive ones:
+// query tiles of one key/value head read its rows from one L2, and no XCD has
+// more than an eighth of all.
+__host__ __device__ __forceinline__ int attn_nth(int w, int n) {
+  const int per = (n + 7) >> 3;
+  return (w >> 3) < per ? (w & 7) * per + (w >> 3) : w;
+}
+
 // A position on the axis of steps: request, unit of the request (key/value
 // head, then query tile) and step.
 struct AttnPos {
@@ -444,7 +453,13 @@ __device__ __forceinline__ int attn_wave_sum(int x) {
 // which reads its rows once for all its query tiles, and each XCD's longest
 // requests come first, so that the card runs dry at once. (64 trees of 129
 // rows over 1 to 2 k rows, a request's heads on one XCD and in the requests'
-// order: of 334 us a fifth passed with workgroups ending one by one.)
+// order: of 334 us a fifth passed with workgroups ending one by one.) One
+// request's units, and those of few heads in many query tiles, of which some
+// XCDs would get more than others, are dealt as attn_plan deals them (us by head
+// / as here: 32832 query rows of one head of 256 over 2 k rows of int8 2228 / 407,
+// three requests of 12312 918 / 411; behind 8 k shared rows of 16 bits, heads of
+// 128, 163840 query rows of one 4764 / 907, 40960 of each of four 1448 / 865, of
+// twelve 3221 / 2440, of eight 1612 / 1612).
 template <class C>
 __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, AttnCut& cut,
                               AttnPos& from, AttnPos& to, AttnReq& rq, int& unit, int& all_units) {
@@ -477,10 +492,7 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
   // the cut, and whether workgroup w has stretch k of it
   auto stretch = [&](int total) -> bool {
     const int n = stretches(total);
-    const int per = (n + 7) >> 3;
-    k = w;
-    if ((w >> 3) >= per) return false;
-    k = (w & 7) * per + (w >> 3);
+    k = attn_nth(w, n);
     if (k >= n) return false;
     const int range = __builtin_amdgcn_readfirstlane((int)((uint32_t)total / (uint32_t)n));
     cut.n = n;
@@ -508,10 +520,10 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     const int total = all_units * rq.steps;
     k = w;
     if (dealt_whole(total, rq.steps)) {
-      const int xcd = w & 7, at = w >> 3, group = at / rq.tiles, head = xcd + 8 * group;
-      if (head >= p.kv_heads) return false;
-      from = AttnPos{-1, 0, head * rq.tiles + (at - group * rq.tiles), 0};
-      to = AttnPos{-1, 0, from.u + 1, 0};
+      const int u = attn_nth(w, all_units);
+      if (u >= all_units) return false;
+      from = AttnPos{-1, 0, u, 0};
+      to = AttnPos{-1, 0, u + 1, 0};
       return true;
     }
     if (!stretch(total)) return false;
@@ -582,6 +594,16 @@ __device__ bool attn_plan_few(const AttnParams& p, AttnFew& sh, int w, int& k, A
     from = attn_uniform(sh.pos[0]);
     to = attn_uniform(sh.pos[1]);
     unit = __builtin_amdgcn_readfirstlane(sh.unit);
+  } else if (!p.by_unit && batch * p.kv_heads < 64 && (batch * p.kv_heads & 7)) {
+    // heads that do not fill the XCDs alike, in query tiles that fill the card
+    const int n = attn_nth(w, all_units);
+    k = w;
+    if (n >= all_units) return false;
+    if (n >= units_before && n < units_before + units)
+      sh.pos[0] = AttnPos{-1, tid, n - units_before, 0};
+    __syncthreads();
+    from = attn_uniform(sh.pos[0]);
+    to = AttnPos{-1, from.b, from.u + 1, 0};
   } else {
     // requests by their steps, the longest first
     int rank = 0;

@@ -80,8 +80,10 @@ inline AttnPlan attn_plan_host(int64_t batch, int32_t T, int32_t q_heads, int32_
   const int64_t want = ((axis + pl.least - 1) / pl.least + 7) & ~(int64_t)7;
   if (want < pl.groups) pl.groups = want;
   // or one for each unit, where there are many (attn_plan decides); the XCDs
-  // may have one key/value head of a request more or less
-  const int64_t units = ((batch * kv_heads + 7) & ~(int64_t)7) * tiles;
+  // may have one unit of one request more or less, or one key/value head of
+  // several requests
+  const int64_t units = batch == 1 ? (kv_heads * tiles + 7) & ~(int64_t)7
+                                   : ((batch * kv_heads + 7) & ~(int64_t)7) * tiles;
   pl.units = units;
   pl.grid = units >= 2 * pl.groups ? units : pl.groups;
   pl.merge = steps > 1;

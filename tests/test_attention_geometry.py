@@ -14,6 +14,7 @@ PROGRAM = r"""
 #include <cstddef>
 #include <cstdio>
 #include <cstdlib>
+#include <vector>
 #include "attention.hpp"
 
 using namespace ddt;
@@ -95,6 +96,23 @@ void behind(int T, int rows, int G, int kv_heads) {
             (3 * (int64_t)T + rows + k / G) * p.q_heads + (int64_t)head * G + k % G);
 }
 
+// Each of n stretches or units is one workgroup's, and no XCD (id % 8) has more than an eighth.
+void nth(int n) {
+  using C = AttnTile<64, 16, 2>;
+  AttnParams p{};
+  int tile = n;
+  const int grid = (n + 7) / 8 * 8 + 24;
+  std::vector<int> had(grid), per(8);
+  for (int w = 0; w < grid; ++w) {
+    const int k = attn_nth(w, n);
+    CHECK(k >= 0 && k < grid && !had[k]);
+    had[k] = 1;
+    if (k < n) ++per[w % 8];
+  }
+  for (int k = 0; k < n; ++k) CHECK(had[k]);
+  for (int x = 0; x < 8; ++x) CHECK(per[x] <= (n + 7) / 8);
+}
+
 template <int DH, int NQ, int QW>
 void all() {
   const int rows[] = {1, 2, 7, 16, 17, 63, 64, 65, 129, 1000, 513 * 80, 1480000, 1490000, 1500001, 2960000, 2980000,
@@ -122,6 +140,7 @@ int main() {
     if (G < 1000) behind(9, 5, G, 7);
   }
   behind(1, 0, (1 << 29) - 1, 1);
+  for (int n : {1, 2, 7, 8, 9, 63, 64, 100, 511, 512, 513, 579, 1024, 3 * 257, 12 * 86, 8388607}) nth(n);
   puts("fine");
 }
 """

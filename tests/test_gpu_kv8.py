@@ -651,6 +651,37 @@ def test_compact(case, paged, kind):
     assert np.array_equal(nl.cpu().numpy(), ne)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case,each", [((13, 400, 5, 8, 4, 7, 12), 3), ((41, 500, 7, 16, 4, 4, 6), 16),
+                                       ((13, 400, 5, 128, 4, 15, 20), 3), ((6, 1000, 3, 256, 2, 9, 12), 2)], ids=str)
+def test_compact_of_many_slices(case, each, kind):
+    """So many slices (a layer's head of a request) that a wave moves `each` of them: over the end of
+    a layer, in groups of loads that hold several slices or a part of one, with a shorter last part."""
+    layers, batch, heads, dh, ps, L, B = case
+    slices = layers * heads
+    assert min(slices * batch // 8192, 16) == each and (slices % each or heads % each)
+    rng = np.random.default_rng(sum(case))
+    past = rng.integers(0, 7, batch).astype(np.int32)
+    past[5] = -1
+    n = rng.integers(0, L + 1, batch).astype(np.int32)
+    n[0] = L
+    acc = np.full((batch, L), -1, np.int32)
+    for b in range(batch):
+        acc[b, :n[b]] = np.sort(rng.choice(np.arange(1, B + 1), n[b], replace=False))
+    table, pool = paging(rng, batch, np.maximum(past, 0) + B + 1, ps)
+    table[1, 1] = -1
+    shape = (layers, pool, heads, ps, dh)
+    k, v = (rng.integers(0, 256, shape, np.uint8) for _ in range(2))
+    ks, vs = (rng.random(shape[:-1], dtype=np.float32) for _ in range(2))
+    on = [codes_on(k, kind), codes_on(v, kind), dev(ks), dev(vs)]
+    nl = pkg.ddtree_compact_kv8(*on, dev(table), dev(past), dev(acc), dev(n))
+    ke, ve, ne = O.compact_paged(k, v, table, past, acc, n)
+    kse, vse, _ = O.compact_paged(ks[..., None], vs[..., None], table, past, acc, n)
+    assert np.array_equal(codes_of(on[0]), ke) and np.array_equal(codes_of(on[1]), ve)
+    assert np.array_equal(on[2].cpu().numpy(), kse[..., 0]) and np.array_equal(on[3].cpu().numpy(), vse[..., 0])
+    assert np.array_equal(nl.cpu().numpy(), ne)
+
+
 READ = [(1, 1, 1, 128, 16), (3, 40, 2, 64, 8), (2, 129, 8, 128, 64), (4, 7, 3, 40, 1), (2, 300, 1, 512, 32),
         (2, 33, 5, 256, None), (3, 2, 200, 24, 4)]
 

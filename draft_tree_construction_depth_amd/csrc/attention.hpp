@@ -38,15 +38,15 @@
 // workspace for attn_merge_kernel.
 //
 // Measured per call, by box and day (bf16, 32 query and 8 key/value heads of
-// 128, unless said otherwise). 64 single tokens over 4 to 8 k rows: 304 to 314
-// us, 1.61 GB at 5.1 to 5.3 TB/s, bound by HBM reads. 64 trees of 129 rows over
+// 128, unless said otherwise). 64 single tokens over 4 to 8 k rows: 297 to 314
+// us, 1.61 GB at 5.1 to 5.4 TB/s, bound by HBM reads. 64 trees of 129 rows over
 // 1 to 2 k: 272 to 294 us (f16 286 to 302), 166 GFLOP at 0.56 to 0.61 PFLOP/s;
 // two waves on each SIMD (the accumulators, the queries and the scores fill
 // the registers) leave the matrix units busy 26%, the vector units 35% and the
 // LDS 24% of the time, and wait 38% of theirs; tiles of 32 rows with three
 // workgroups to a CU spill (499 us), workgroups of eight waves take 335. 3
-// chains of 17 rows over 50 to 100 k (f16, heads of 64, 40 and 8): 115 to 122 us,
-// 461 MB at 3.8 to 4 TB/s. One tree of 65 rows over 1 k: 20 to 21 us, of which
+// chains of 17 rows over 50 to 100 k (f16, heads of 64, 40 and 8): 110 to 122 us,
+// 461 MB at 3.8 to 4.2 TB/s. One tree of 65 rows over 1 k: 20 to 21 us, of which
 // the merge is 4 and the steps are 6: a chain of waits. 32 blocks of 32 rows
 // with 16 heads of 256 on 4 over 2 to 4 k: 194 us; 2 pieces of a prompt of 513
 // rows over 4 to 8 k: 180 us.
@@ -55,15 +55,16 @@
 // and become values of the queries' type, which all of them have exactly, on
 // their way into LDS; a row's scale multiplies its scores, or its weight. They
 // halve the bytes and leave the products as they are. The same sizes: 64 single
-// tokens 171 us (806 MB and 25 of scales at 4.9 TB/s), 64 trees 264 to 276, 3
-// chains 105 to 118 (bound by the vector units: exponentials, scales and masks),
-// one tree 19.
+// tokens 166 to 174 us (806 MB and 25 of scales at 4.9 TB/s), 64 trees 264 to
+// 280, 3 chains 105 to 122 (bound by the vector units: exponentials, scales and
+// masks; bf16 92 to 98), one tree 19. Heads of 256, one workgroup to a CU: 32
+// blocks of 32 rows 186, 64 single tokens of 4 heads 229.
 //
 // Rows that all requests share (EXT, kAtPrefix and kAtRest): one pass over them
 // with the query rows of the whole batch, whose maxima, sums and rows go to the
 // workspace, then each request's own rows, which begin from those. 64 single
 // tokens behind 8 k shared rows of 16 bits: 82 us, 270 without; 24 chains of 5
-// rows (f16) behind 30 k of 8 bits: 126 us, 311 without.
+// rows (f16) behind 30 k of 8 bits: 123 to 132 us, 311 without.
 #pragma once
 
 #include "paged.hpp"
@@ -1539,9 +1540,11 @@ __device__ __forceinline__ uint64_t attn_visible_codes(const AttnParams& p, int6
 
 // The same over a cache of codes. A step's codes wait in registers, two steps
 // ahead of their use where those suffice, and become values of H on their way
-// into LDS. No branch of a step depends on the lane: with nearly all registers
-// in use the compiler has moved values across such a branch's end for the lanes
-// inside it alone (zeros to be stored later came out as other numbers).
+// into LDS. Masks are bit operations and addresses are clamped: a branch of a
+// step that depends on the lane holds one store of one number (the largest scale,
+// the flag of NaN codes). With nearly all registers in use the compiler has moved
+// values across the end of longer ones for the lanes inside them alone (zeros to
+// be stored later came out as other numbers).
 template <typename H, class C>
 __device__ __forceinline__ void attn_steps_codes(const AttnParams& p, unsigned char* lds,
                                                  float* s_scale, float* s_most, int* s_flag,

@@ -40,10 +40,10 @@ void launch_read8(const ddt::Read8Params& rp, int64_t blocks, int cache_dtype, h
 
 // Whether a batch's shared rows can be worth a pass of their own, of `cap` rows
 // of `elem` bytes an element (attn_shared decides, by the lengths). Up to 80 query
-// rows to a key/value head the cache's bytes are what it takes long to read; with
-// more the products are, which sharing does not save: 32 requests x 8 k shared
-// rows of 16 bits, 64 / 80 / 96 / 112 / 128 query rows, without 154 / 170 / 170 /
-// 173 / 182 us, with 123 / 150 / 168 / 187 / 200.
+// rows to a key/value head reading the rows again takes longer than the pass over
+// them; with more the pass takes longer, at half the rate of a large product: 32
+// requests x 8 k shared rows of 16 bits, 64 / 80 / 96 / 112 / 128 query rows,
+// without 154 / 170 / 170 / 173 / 182 us, with 123 / 150 / 168 / 187 / 200.
 bool shares(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
             int64_t cap, int elem) {
   return batch > 1 && (int64_t)T * (q_heads / kv_heads) <= 80 &&

@@ -423,8 +423,8 @@ int ddtree_attention_kv8(const void* q, int dtype, int64_t batch, int32_t T, int
  * Rows are shared in multiples of 128, and only where it pays: where they keep
  * 192 MiB or more of cache rows from being read again (by the requests that take
  * part, but one), and up to 80 query rows (T * q_heads / kv_heads) to a request's
- * key/value head; with more, the products are what takes long, which sharing does
- * not save. All other rows are attended to request by request.
+ * key/value head; with more, a pass over them takes longer than the reading that
+ * it saves. All other rows are attended to request by request.
  * Supported as ddtree_attention, with a page table (DDT_EINVAL otherwise). The
  * workspace (ddtree_attention_shared_workspace_size) also holds the shared rows'
  * part, a float32 row for each row of q.

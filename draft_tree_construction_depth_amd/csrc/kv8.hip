@@ -64,8 +64,11 @@ SharePlan share_plan(int64_t batch, int32_t T, int32_t q_heads, int32_t kv_heads
                      int64_t cap, bool codes) {
   SharePlan pl;
   pl.shared = attn_plan_host(1, (int32_t)(batch * T), q_heads, kv_heads, head_dim, cap, codes);
-  // a stretch's start and its pieces' way to the merge are worth steps: 64 single
-  // tokens behind 8 k rows, 2048 steps: stretches of 4 92 us, of 8 89, of 16 95
+  // a stretch's start and its pieces' way to the merge are worth steps, too long
+  // ones leave CUs idle. us in stretches of 4 / 8 / 16 steps at least, 8 heads of
+  // 128, 16 bits: 64 single tokens behind 8 k rows 88 / 84 / 89, of e4m3 68 / 65 /
+  // 74, behind 30 k 117 / 116 / 120, 8 of them behind 16 k 46 / 44 / 49; heads of
+  // 64 54 / 53 / 58, 32 of 4 heads of 256 75 / 75 / 80; chains of 5 and 16 alike
   pl.shared.least = 8;
   pl.own = attn_plan_host(batch, T, q_heads, kv_heads, head_dim, cap, codes);
   const size_t rows = (size_t)batch * T * q_heads;
